@@ -76,6 +76,19 @@ def lib() -> ctypes.CDLL:
     L.w4a8_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
     L.awq_stream_read.argtypes = [vp, i64, vp, vp]
     L.awq_plan_info.argtypes = [i32, i64, i64, i64, i32, i32, i32, ctypes.POINTER(PlanInfo)]
+    f32 = ctypes.c_float
+    L.w4a8_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
+    L.w4a8_fp8_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
+    L.awq_kv4_head_words.argtypes = [i64, i64]
+    L.awq_kv4_head_words.restype = i64
+    L.awq_kv4_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64,
+                                 i32, i32, vp]
+    L.awq_kv4_attention.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i64, i64, f32, i64,
+                                    i32, vp, sz, vp]
+    L.awq_kv4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
+    L.awq_kv4_attention_workspace_bytes.restype = sz
+    for f in ("w4a8_rmsnorm_quant", "w4a8_fp8_rmsnorm_quant", "awq_kv4_append", "awq_kv4_attention"):
+        getattr(L, f).restype = i32
     for f in ("awq_pack", "awq_unpack", "awq_gemm_w4a16", "awq_gemv_w4a16", "w4a8_quant_act", "w4a8_gemm", "w4a8_linear",
               "awq_stream_read", "awq_plan_info", "awq_gemv_w4a16_static",
               "awq_dequant_w4a16", "w4a8_fp8_quant_act", "w4a8_fp8_gemm", "w4a8_fp8_linear", "awq_repack_v2"):

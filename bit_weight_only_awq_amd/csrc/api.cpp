@@ -561,6 +561,70 @@ static int run_w4a16(const void *x, const int32_t *qweight, const void *scales, 
     return hip_status(e);
 }
 
+// ---------------------------------------------------------------------------
+// RMS norm, rotary append and attention over the 4-bit cache.
+static bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+static bool known_dtype(int dtype) { return dtype == AWQ_DTYPE_F16 || dtype == AWQ_DTYPE_BF16; }
+
+// out8: the call has codes and scales (a, s1; fp8: asum too)
+static int run_rmsnorm(const void *x, const void *residual, const void *weight, void *residual_out, void *y, void *a,
+                       float *s1, float *asum, bool fp8, int64_t M, int64_t K, float eps, int dtype, void *stream) {
+    if (!x || !weight || (!residual != !residual_out)) return AWQ_EINVAL;
+    if (fp8 ? (!a || !s1 || !asum) : (!a != !s1 || (!a && !y))) return AWQ_EINVAL;
+    if (M < 1 || K < 1 || M > (int64_t(1) << 31) - 1 || K > kMaxDim) return AWQ_EINVAL;
+    if (!known_dtype(dtype) || !(eps >= 0.0f) || !std::isfinite(eps)) return AWQ_EINVAL;
+    for (const void *p : {x, residual, weight, (const void *)residual_out, (const void *)y, (const void *)a,
+                          (const void *)s1, (const void *)asum})
+        if (!aligned16(p)) return AWQ_EALIGN;
+    const NormArgs n{x, residual, weight, residual_out, y, a, s1, asum, M, K, eps, dtype};
+    return hip_status(launch_rmsnorm(n, static_cast<hipStream_t>(stream)));
+}
+
+static constexpr int64_t kMaxHeads = 4096;
+static constexpr int64_t kMaxTokens = int64_t(1) << 30;
+static int check_kv4(int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t num_pages, int dtype) {
+    if (Hkv < 1 || Hq < 0 || Hq > kMaxHeads || Hkv > kMaxHeads || D < 1 || P < 1 || num_pages < 1) return AWQ_EINVAL;
+    if (!known_dtype(dtype)) return AWQ_EINVAL;
+    if (D != 64 && D != 128) return AWQ_EUNSUPPORTED;
+    if (P < 16 || P > 1024 || (P & (P - 1))) return AWQ_EUNSUPPORTED;
+    // slots, and words of the pool, in 62 bits
+    if (num_pages > (int64_t(1) << 40) / (P * Hkv)) return AWQ_EINVAL;
+    return AWQ_OK;
+}
+
+struct Kv4Plan {
+    int nt, splits, min_steps, part_cols;
+    int64_t col_tiles, tiles;
+    size_t workspace_bytes;
+};
+// How an attention call is launched (pure function of the shape; the lengths
+// themselves are known on the device only, where a sequence takes as many of
+// its workgroups as it has steps for).
+static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_kv,
+                        const DeviceProps &d) {
+    Kv4Plan p{};
+    const int64_t rows = max_q * (Hq / Hkv);
+    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.col_tiles = cdiv(rows, 16 * p.nt);
+    p.part_cols = (int)std::min<int64_t>(rows, 16 * p.nt);
+    p.min_steps = 4;
+    p.tiles = B * Hkv * p.col_tiles;
+    const int64_t most = cdiv(cdiv(max_kv, 32), p.min_steps);
+    p.splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({cdiv(4 * (int64_t)d.cus, p.tiles), most, (int64_t)kKv4MaxSplits}));
+    if (p.splits > 1)
+        p.workspace_bytes =
+            (size_t)(split_counters_bytes(p.tiles) + p.tiles * p.splits * p.part_cols * (D + 4) * 4);
+    return p;
+}
+static int check_attention(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_kv) {
+    if (B < 0 || max_q < 1 || max_kv < 0 || B > kMaxDim || max_q > 16 * kMaxDim || max_kv > kMaxTokens)
+        return AWQ_EINVAL;
+    if (Hkv < 1 || Hq < 1 || Hq > kMaxHeads || Hkv > kMaxHeads || Hq % Hkv) return AWQ_EINVAL;
+    if (D != 64 && D != 128) return D < 1 ? AWQ_EINVAL : AWQ_EUNSUPPORTED;
+    return AWQ_OK;
+}
+
 }  // namespace awq4
 
 using namespace awq4;
@@ -857,6 +921,86 @@ int w4a8_linear(const void *x_f16, int8_t *a8, float *s1, const int32_t *b_packe
     rc = hip_status(launch_w4a8_quant(x_f16, a8, s1, M, K, dtype, st));
     if (rc != AWQ_OK) return rc;
     return hip_status(launch_w4a8(a, p, st));
+}
+
+int w4a8_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *residual_out, void *y,
+                       int8_t *a8, float *s1, int64_t M, int64_t K, float eps, int dtype, void *stream) {
+    return run_rmsnorm(x, residual, weight, residual_out, y, a8, s1, nullptr, false, M, K, eps, dtype, stream);
+}
+
+int w4a8_fp8_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *residual_out, void *y,
+                           uint8_t *a, float *s1, float *asum, int64_t M, int64_t K, float eps, int dtype,
+                           void *stream) {
+    return run_rmsnorm(x, residual, weight, residual_out, y, a, s1, asum, true, M, K, eps, dtype, stream);
+}
+
+int64_t awq_kv4_head_words(int64_t head_dim, int64_t page_size) {
+    if (check_kv4(0, 1, head_dim, page_size, 1, AWQ_DTYPE_F16) != AWQ_OK) return 0;
+    return page_size * (head_dim / 4 + 2);
+}
+
+int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   const float *rope, const int32_t *positions, const int64_t *slots, void *q_out, int32_t *cache,
+                   int64_t T, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t page_size, int64_t num_pages,
+                   int64_t rot, int64_t max_pos, int interleaved, int dtype, void *stream) {
+    const int rc = check_kv4(Hq, Hkv, head_dim, page_size, num_pages, dtype);
+    if (rc != AWQ_OK) return rc;
+    if (T < 0 || T > kMaxTokens || rot < 0 || rot > head_dim || rot % 16) return AWQ_EINVAL;
+    if (rot > 0 && (max_pos < 1 || max_pos > kMaxTokens)) return AWQ_EINVAL;
+    if (interleaved != 0 && interleaved != 1) return AWQ_EINVAL;
+    if (T == 0) return AWQ_OK;
+    if (!k || !v || !slots || !cache || (Hq > 0 && (!q || !q_out)) || (rot > 0 && (!rope || !positions)))
+        return AWQ_EINVAL;
+    if (k_stride < Hkv * head_dim || v_stride < Hkv * head_dim || (Hq > 0 && q_stride < Hq * head_dim))
+        return AWQ_EINVAL;
+    const int64_t far = int64_t(1) << 32;
+    if (k_stride > far || v_stride > far || q_stride > far) return AWQ_EINVAL;
+    if (k_stride % 8 || v_stride % 8 || (Hq > 0 && q_stride % 8)) return AWQ_EALIGN;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) ||
+        (rot > 0 && (!aligned16(rope) || !aligned_to(positions, 4))) || !aligned_to(slots, 8))
+        return AWQ_EALIGN;
+    const Kv4AppendArgs g{q,     k,     v,         q_stride,  k_stride, v_stride,      rope,     positions,   slots,
+                          q_out, cache, T,         num_pages, (int)Hq,  (int)Hkv,      (int)head_dim,
+                          (int)page_size, (int)rot, (int)max_pos, interleaved, dtype};
+    return hip_status(launch_kv4_append(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t awq_kv4_attention_workspace_bytes(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t head_dim,
+                                         int64_t max_kv) {
+    if (check_attention(B, max_q, Hq, Hkv, head_dim, max_kv) != AWQ_OK || B == 0) return 0;
+    return plan_kv4(B, max_q, Hq, Hkv, head_dim, max_kv, stream_props(nullptr)).workspace_bytes;
+}
+
+int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables, const int32_t *lens,
+                      const int32_t *cu_q, void *out, int64_t B, int64_t total_q, int64_t max_q, int64_t max_kv,
+                      int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t page_size, int64_t num_pages,
+                      int64_t table_stride, float scale, int64_t window, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    int rc = check_attention(B, max_q, Hq, Hkv, head_dim, max_kv);
+    if (rc != AWQ_OK) return rc;
+    rc = check_kv4(Hq, Hkv, head_dim, page_size, num_pages, dtype);
+    if (rc != AWQ_OK) return rc;
+    if (total_q < 0 || total_q > kMaxTokens || window < 0 || table_stride < 1 || table_stride > kMaxTokens / page_size)
+        return AWQ_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return AWQ_EINVAL;
+    if (!cu_q && (total_q != B || max_q != 1)) return AWQ_EINVAL;
+    if (B == 0 || total_q == 0) return AWQ_OK;
+    if (!q || !cache || !tables || !lens || !out) return AWQ_EINVAL;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned_to(tables, 4) || !aligned_to(lens, 4) ||
+        !aligned_to(cu_q, 4))
+        return AWQ_EALIGN;
+    const Kv4Plan p = plan_kv4(B, max_q, Hq, Hkv, head_dim, max_kv, stream_props(stream));
+    if (p.tiles * p.splits >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;
+    rc = check_workspace(workspace, workspace_bytes, p.workspace_bytes);
+    if (rc != AWQ_OK) return rc;
+    Kv4AttnArgs g{q, cache, tables, lens, cu_q, out, num_pages, (int)B, (int)total_q, (int)max_q, (int)Hq, (int)Hkv,
+                  (int)head_dim, (int)page_size, (int)table_stride, (int)std::min<int64_t>(window, kMaxTokens), dtype,
+                  scale, p.nt, (int)p.col_tiles, p.splits, p.min_steps, p.part_cols, nullptr, nullptr};
+    if (p.workspace_bytes) {
+        g.counters = static_cast<uint32_t *>(workspace);
+        g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + split_counters_bytes(p.tiles));
+    }
+    return hip_status(launch_kv4_attention(g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

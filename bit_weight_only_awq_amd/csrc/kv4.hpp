@@ -1,0 +1,38 @@
+// kv4.hpp -- the paged key/value cache in 4 bits, as the kernels address it
+// (kv4_append.hip writes it, kv4_attention.hip and kv4_prefill.hip read it).
+//
+// int32 [pages, kv_heads, P (D/4 + 2)]; the words of one page and head:
+//   K words  [P][D/8]       AWQ order along the head dimension: nibble i of
+//                           word j holds dimension 8j + {0,2,4,6,1,3,5,7}[i]
+//   V words  [P/4][D/8][4]  the same words, those of four consecutive tokens
+//                           side by side
+//   K meta   [P]            scale bits (activation type) | zero point << 16
+//   V meta   [P]
+// value = (code - zero point) * scale, one scale and zero point per token and
+// head.
+//
+// Why this layout: Q K^T sums over the head dimension, so a lane's matrix-core
+// operand is a run of one token's words; P V sums over the tokens, so a lane
+// wants one word column of several tokens.  With four tokens' V words side by
+// side both are 16-byte loads, and 16 tokens of either are 64 D bytes in one
+// run, yet appending a token writes whole words only (no read-modify-write of
+// a word that another token shares).
+#pragma once
+
+#include "device.hpp"
+
+namespace awq4 {
+
+template <int D>
+struct Kv4Layout {
+    static constexpr int kWords = D / 8;  // packed words of one token and head
+    __host__ __device__ static constexpr int head_words(int P) { return P * (D / 4 + 2); }
+    __host__ __device__ static constexpr int k_word(int t, int j) { return t * kWords + j; }
+    __host__ __device__ static constexpr int v_word(int P, int t, int j) {
+        return P * kWords + ((t >> 2) * kWords + j) * 4 + (t & 3);
+    }
+    __host__ __device__ static constexpr int k_meta(int P, int t) { return 2 * P * kWords + t; }
+    __host__ __device__ static constexpr int v_meta(int P, int t) { return 2 * P * kWords + P + t; }
+};
+
+}  // namespace awq4

@@ -1,0 +1,479 @@
+// kv4_attention.hip -- causal attention over the paged 4-bit cache (layout:
+// kv4.hpp) for few query rows per key/value head: decode, several tokens at
+// once, short chunks.
+//
+// Query i of a sequence with n new tokens and L tokens in all stands at
+// position p = L - n + i and sees the keys j <= p (with a window w: j > p - w).
+//   t_j = scale s_j (Q . c_j - z_j sum_d Q_d)
+//   O   = sum_j softmax(t)_j s'_j (c'_j - z'_j)
+// with codes c, zero points z and scales s of the keys, primed ones of the
+// values.  The codes enter the matrix cores as they are: a masked pair of
+// nibbles is a pair of fp16 subnormals, exactly c 2^-24 (16 c 2^-24 for the
+// upper nibble of a byte), one AND and no conversion.  Scales and zero points
+// act on the fp32 scores, and on the value side the scale is folded into the
+// probabilities, whose one rounding (to fp16, the matrix cores' type; the
+// values' codes are exact in it) is the only one between q and the output's:
+//   P_j = fp16(softmax numerator * s'_j 2^(14 - E)),  O = sum P_j c'_j - sum P_j z'_j
+// E is the exponent of the largest s' met so far, raised together with the
+// running maximum: P then uses fp16's whole range (a probability 2^-28 times
+// the largest still has all 11 bits) whatever the scales' magnitude.  The sum
+// of z' takes the rounded P, so that a code and its zero point lose the same.
+// Queries are scaled by a power of two to just below 2^15 before they become
+// fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest.
+//
+// Tiles are transposed, S^T = K Q^T and O^T = V^T P^T: the lanes of a column
+// (one query row) hold the scores of the tokens that they then need as the
+// second product's operand, so probabilities never move between lanes.  16
+// tokens x 16 query rows a tile; the rows of a sequence and key/value head are
+// its (new token, head of the group) pairs.
+//
+// Bound: device memory (D + 8 bytes a token and head, read once).  A workgroup
+// of four waves takes a run of tokens, each wave 32 of every 128; the four
+// join their sums through LDS, and the workgroups of a sequence (as many as
+// its length asks for, known only on the device) join theirs through the
+// workspace: the last to arrive adds them in order, writes and clears.
+#include "kv4.hpp"
+#include "launch.hpp"
+
+namespace awq4 {
+
+constexpr int kAttnWaves = 4;
+
+// The larger of the values of the four lanes of a column (lanes l, l ^ 16, l ^
+// 32, l ^ 48), in each of them.
+__device__ __forceinline__ float column_max(float v) {
+    const uint32_t b = bit_as<uint32_t>(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const float m = fmaxf(bit_as<float>((uint32_t)h[0]), bit_as<float>((uint32_t)h[1]));
+    const uint32_t c = bit_as<uint32_t>(m);
+    const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+    return fmaxf(bit_as<float>((uint32_t)q[0]), bit_as<float>((uint32_t)q[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+    const uint32_t b = bit_as<uint32_t>(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const float m = bit_as<float>((uint32_t)h[0]) + bit_as<float>((uint32_t)h[1]);
+    const uint32_t c = bit_as<uint32_t>(m);
+    const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+    return bit_as<float>((uint32_t)q[0]) + bit_as<float>((uint32_t)q[1]);
+}
+
+// The eight codes of a word as matrix-core operand (fp16 subnormals), columns
+// 0..7 in order; columns 2, 3, 6, 7 carry a factor 16.
+__device__ __forceinline__ u32x4 word_operand(uint32_t w) {
+    return (u32x4){w & 0x000F000Fu, w & 0x00F000F0u, (w >> 8) & 0x000F000Fu, (w >> 8) & 0x00F000F0u};
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    typedef float f32x2v __attribute__((ext_vector_type(2)));
+    return bit_as<uint32_t>(__builtin_convertvector((f32x2v){a, b}, f16x2));
+}
+
+// What one wave reads for 32 tokens: two tiles of 16.
+template <int D>
+struct Kv4Step {
+    static constexpr int KW = D / 32;  // words of a token in a lane
+    uint32_t k[2][KW];
+    u32x4 v[2], km[2], vm[2];
+};
+
+template <int DT, int D, int NT>
+__global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnArgs g) {
+    using L = Kv4Layout<D>;
+    constexpr int COLS = 16 * NT, KW = D / 32, VM = D / 16, ROW = D + 4;
+    constexpr float kNegInf = -__builtin_inff();
+    __shared__ float lds_o[kAttnWaves][16][ROW];  // one 16-column tile of every wave; at D its m, at D + 1 its l
+    __shared__ float lds_l[16];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, grp = lane >> 4;
+    // workgroup -> (sequence, split, head, column tile)
+    int id = blockIdx.x;
+    const int tile_h = id % (g.Hkv * g.col_tiles);
+    id /= g.Hkv * g.col_tiles;
+    const int split = id % g.splits, b = id / g.splits;
+    const int h = tile_h / g.col_tiles, ct = tile_h % g.col_tiles;
+    const int G = g.Hq / g.Hkv;
+
+    // the sequence's rows and length; whatever the arrays hold, no index
+    // leaves the tensors
+    int q0 = b, q1 = b + 1;
+    if (g.cu_q) {
+        q0 = min(max(g.cu_q[b], 0), g.total_q);
+        q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
+    }
+    const int nq = q1 - q0;
+    const int kv_len = (int)min((int64_t)max(g.lens[b], 0), (int64_t)g.table_stride * g.P);
+    const int64_t rows = (int64_t)min(nq, g.max_q) * G;
+    const int64_t c0 = (int64_t)ct * COLS;
+    if (c0 >= rows) return;
+    const int ncols = (int)min((int64_t)COLS, rows - c0);
+
+    // tokens that any column of the tile sees: [kv_lo, kv_hi)
+    const int first_pos = kv_len - nq + (int)(c0 / G), last_pos = kv_len - nq + (int)((c0 + ncols - 1) / G);
+    const int kv_hi = max(last_pos + 1, 0);
+    const int kv_lo = g.window > 0 ? min(max(first_pos - g.window + 1, 0), kv_hi) : 0;
+    // ... and that all of them see: [all_lo, all_hi)
+    const int all_hi = first_pos + 1;
+    const int all_lo = g.window > 0 ? last_pos - g.window + 1 : 0;
+    const int step0 = kv_lo >> 5, steps = kv_hi > kv_lo ? ((kv_hi + 31) >> 5) - step0 : 0;
+    const int splits = max(1, min(g.splits, (steps + g.min_steps - 1) / g.min_steps));
+    if (split >= splits) return;
+    const int per = (steps + splits - 1) / splits;
+    const int s_begin = step0 + split * per, s_end = min(step0 + steps, s_begin + per);
+
+    // this lane's columns: their rows of q as matrix-core operand, in fp16
+    u32x4 qf[NT][KW];
+    float qz[NT], cf[NT];
+    int lo[NT], hi[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int col = 16 * n + r16;
+        const bool live = col < ncols;
+        const int64_t row = c0 + (live ? col : 0);
+        const int qi = (int)(row / G), hg = (int)(row - (int64_t)qi * G);
+        const int pos = kv_len - nq + qi;
+        hi[n] = pos + 1;
+        lo[n] = g.window > 0 ? pos - g.window + 1 : 0;
+        const uint16_t *src = (const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D + 8 * KW * grp;
+        float f[KW][8], mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            const u32x4 w = *(const u32x4 *)(src + 8 * i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[i][e] = live ? act_bits_to_f32<DT>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) : 0.0f;
+                mx = fmaxf(mx, fabsf(f[i][e]));
+            }
+        }
+        mx = column_max(mx);
+        const int ex = (int)(bit_as<uint32_t>(mx) >> 23);
+        const int up = ex == 255 ? 0 : 127 + 14 - ex;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[i][e] = __builtin_ldexpf(f[i][e], up);
+                sum += f[i][e];
+            }
+            // columns 2, 3, 6, 7 meet codes times 16
+            qf[n][i] = (u32x4){pack_f16(f[i][0], f[i][1]), pack_f16(f[i][2] * 0.0625f, f[i][3] * 0.0625f),
+                               pack_f16(f[i][4], f[i][5]), pack_f16(f[i][6] * 0.0625f, f[i][7] * 0.0625f)};
+        }
+        qz[n] = column_sum(sum) * 0x1p-24f;
+        cf[n] = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
+    }
+
+    const int lgP = __builtin_ctz(g.P);
+    const int32_t *table = g.tables + (size_t)b * g.table_stride;
+    const int hw = L::head_words(g.P);
+    // the page that holds tokens t .. t + 15, or -1
+    auto page_of = [&](int t) -> int {
+        if (t >= kv_len) return -1;
+        const int p = table[t >> lgP];
+        return p >= 0 && p < g.num_pages ? p : -1;
+    };
+    auto load = [&](Kv4Step<D> &s, int p0, int p1, int t0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int page = max(i ? p1 : p0, 0), t = (t0 + 16 * i) & (g.P - 1);
+            const uint32_t *base = (const uint32_t *)g.cache + ((size_t)page * g.Hkv + h) * hw;
+            const uint32_t *kp = base + L::k_word(t + r16, KW * grp);
+            if (KW == 4) {
+                const u32x4 w = *(const u32x4 *)kp;
+#pragma unroll
+                for (int j = 0; j < KW; ++j) s.k[i][j] = w[j];
+            } else {
+                const u32x2 w = *(const u32x2 *)kp;
+#pragma unroll
+                for (int j = 0; j < KW; ++j) s.k[i][j] = w[j];
+            }
+            s.v[i] = *(const u32x4 *)(base + L::v_word(g.P, t + 4 * grp, D == 128 ? r16 : (r16 & 7)));
+            s.km[i] = *(const u32x4 *)(base + L::k_meta(g.P, t + 4 * grp));
+            s.vm[i] = *(const u32x4 *)(base + L::v_meta(g.P, t + 4 * grp));
+        }
+    };
+
+    f32x4 o[NT][VM], oz[NT];
+    float m[NT], l[NT];
+    int e_run = 27;  // exponent field of the largest value scale so far (from 2^-100 on)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = kNegInf;
+        l[n] = 0.0f;
+        oz[n] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < VM; ++t) o[n][t] = (f32x4){0, 0, 0, 0};
+    }
+    const uint32_t half_sel = (D == 128 || r16 < 8) ? 0x05040100u : 0x07060302u;
+
+    auto compute = [&](Kv4Step<D> &s, int p0, int p1, int t0) {
+        const bool plain = p0 >= 0 && p1 >= 0 && t0 >= all_lo && t0 + 32 <= all_hi && t0 >= kv_lo;
+        if (!plain) {
+            // tokens that no column sees, or without a page: whatever their
+            // meta words hold must not reach the sums
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = t0 + 16 * i + 4 * grp + r;
+                    const bool any = (i ? p1 : p0) >= 0 && j >= kv_lo && j < kv_hi;
+                    s.km[i][r] = any ? s.km[i][r] : 0u;
+                    s.vm[i][r] = any ? s.vm[i][r] : 0u;
+                }
+        }
+        float ks[2][4], kz[2][4], vs[2][4], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                ks[i][r] = act_bits_to_f32<DT>(s.km[i][r] & 0xFFFFu);
+                kz[i][r] = (float)((s.km[i][r] >> 16) & 0xFFu);
+                vs[i][r] = act_bits_to_f32<DT>(s.vm[i][r] & 0xFFFFu);
+                top = fmaxf(top, vs[i][r]);  // (a NaN scale does not count)
+            }
+        top = column_max(top);
+        const int e_now = max(e_run, min((int)(bit_as<uint32_t>(top) >> 23), 254));
+        const float down = __builtin_ldexpf(1.0f, e_run - e_now), vf = __builtin_ldexpf(1.0f, 127 + 14 - e_now);
+        const bool raised = e_now != e_run;
+        e_run = e_now;
+        u32x4 ko[2][KW];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < KW; ++j) ko[i][j] = word_operand(s.k[i][j]);
+        u32x4 pf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x[2][4], mx = kNegInf;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < KW; ++j) a = mfma_f16(ko[i][j], qf[n][j], a);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[i][r] = __builtin_fmaf(-kz[i][r], qz[n], a[r]) * ks[i][r];
+                    if (!plain) {
+                        const int j = t0 + 16 * i + 4 * grp + r;
+                        const bool seen = (i ? p1 : p0) >= 0 && j >= lo[n] && j < hi[n];
+                        x[i][r] = seen ? x[i][r] : kNegInf;
+                    }
+                    mx = fmaxf(mx, x[i][r]);
+                }
+            }
+            mx = fmaxf(m[n], column_max(mx));
+            if (__builtin_amdgcn_ballot_w64(mx > m[n]) != 0 || raised) {
+                const float alpha = m[n] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m[n] - mx) * cf[n]);
+                const float od = alpha * down;
+                l[n] *= alpha;
+                oz[n] *= od;
+#pragma unroll
+                for (int t = 0; t < VM; ++t) o[n][t] *= od;
+                m[n] = mx;
+            }
+            const float ref = mx == kNegInf ? 0.0f : mx * cf[n];
+            float p[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], cf[n], -ref));
+                    float w = e * (vs[i][r] * vf);
+                    if (!plain) {
+                        const bool seen = x[i][r] != kNegInf;
+                        e = seen ? e : 0.0f;
+                        w = seen ? w : 0.0f;
+                    }
+                    l[n] += e;
+                    p[i][r] = w;
+                }
+            pf[n] = (u32x4){pack_f16(p[0][0], p[0][1]), pack_f16(p[0][2], p[0][3]), pack_f16(p[1][0], p[1][1]),
+                            pack_f16(p[1][2], p[1][3])};
+        }
+        // the values' zero points as an operand with equal rows
+        u32x4 zo;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            zo[2 * i] = perm_b32(s.vm[i][1], s.vm[i][0], 0x07060302u);
+            zo[2 * i + 1] = perm_b32(s.vm[i][3], s.vm[i][2], 0x07060302u);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) oz[n] = mfma_f16(zo, pf[n], oz[n]);
+        // the values' codes: consecutive tokens side by side, one column a mask
+        uint32_t px[4], py[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w0 = s.v[i >> 1][2 * (i & 1)], w1 = s.v[i >> 1][2 * (i & 1) + 1];
+            px[i] = perm_b32(w1, w0, half_sel);
+            py[i] = D == 128 ? pair_y(w0, w1) : 0u;
+        }
+#pragma unroll
+        for (int t = 0; t < VM; ++t) {
+            // D = 128: column t of the word; D = 64: position t of the lane's half
+            const int pos = D == 128 ? t >> 1 : t;
+            const uint32_t mask = pos & 1 ? 0x00F000F0u : 0x000F000Fu;
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = D == 128 && (t & 1) ? py[i] : px[i];
+                a[i] = (pos & 2 ? w >> 8 : w) & mask;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[n][t] = mfma_f16(a, pf[n], o[n][t]);
+        }
+    };
+
+    {
+        int st = s_begin + wave;
+        if (st < s_end) {
+            Kv4Step<D> cur, nxt;
+            int p0 = page_of(32 * st), p1 = page_of(32 * st + 16);
+            load(cur, p0, p1, 32 * st);
+            while (true) {
+                const int sn = st + kAttnWaves;
+                const bool more = sn < s_end;
+                int n0 = -1, n1 = -1;
+                if (more) {
+                    n0 = page_of(32 * sn);
+                    n1 = page_of(32 * sn + 16);
+                    load(nxt, n0, n1, 32 * sn);
+                }
+                compute(cur, p0, p1, 32 * st);
+                if (!more) break;
+                cur = nxt;
+                st = sn;
+                p0 = n0;
+                p1 = n1;
+            }
+        }
+    }
+
+    // Join the four waves, 16 columns at a time; then write, or exchange with
+    // the sequence's other workgroups.
+    const int64_t tile = ((int64_t)b * g.Hkv + h) * g.col_tiles + ct;
+    float *part = splits > 1 ? g.partials + tile * g.splits * (g.part_cols * ROW) : nullptr;
+    auto put_row = [&](int col, int d, f32x4 v) {
+        const int64_t row = c0 + col;
+        const int qi = (int)(row / G), hg = (int)(row - (int64_t)qi * G);
+        *(uint2 *)((uint16_t *)g.out + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D + d) = quad_out_bits<DT>(v);
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int nc = min(16, ncols - 16 * n);
+        if (nc <= 0) break;
+        if (n) __syncthreads();
+        const float lsum = column_sum(l[n]);
+        const int back = e_run - 127 - 14 + 24;
+#pragma unroll
+        for (int t = 0; t < VM; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * grp + r;
+                const int d = D == 128 ? 8 * i + t : 8 * (i & 7) + 2 * t + (i >> 3);
+                const bool x16 = (D == 128 ? t >> 1 : t) & 1;
+                const float v = (x16 ? o[n][t][r] * 0.0625f : o[n][t][r]) - oz[n][r];
+                lds_o[wave][r16][d] = __builtin_ldexpf(v, back);
+            }
+        if (grp == 0) {
+            lds_o[wave][r16][D] = m[n] == kNegInf ? kNegInf : m[n] * cf[n];
+            lds_o[wave][r16][D + 1] = lsum;
+        }
+        __syncthreads();
+        for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
+            const int col = i / (D / 4), d = 4 * (i % (D / 4));
+            float mw[kAttnWaves], mm = kNegInf, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, mw[w] = lds_o[w][col][D]);
+            f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) {
+                const float a = mw[w] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw[w] - mm);
+                v += a * *(const f32x4 *)&lds_o[w][col][d];
+                ll += a * lds_o[w][col][D + 1];
+            }
+            if (splits == 1) {
+                put_row(16 * n + col, d, ll > 0.0f || ll != ll ? v / ll : (f32x4){0, 0, 0, 0});
+            } else {
+                float *p = part + ((size_t)split * g.part_cols + 16 * n + col) * ROW;
+                part_put((uint64_t *)(p + d), v);
+                if (d == 0) part_put((uint64_t *)(p + D), (f32x4){mm, ll, 0, 0});
+            }
+        }
+    }
+    if (splits == 1) return;
+    if (!split_tile_last_atomic(g.counters + tile, splits)) return;
+#pragma unroll 1
+    for (int n = 0; n < NT; ++n) {
+        const int nc = min(16, ncols - 16 * n);
+        if (nc <= 0) break;
+        auto row_of = [&](int s, int col) { return (uint64_t *)(part + ((size_t)s * g.part_cols + 16 * n + col) * ROW); };
+        __syncthreads();
+        // the splits' sums, and their maxima and then weights
+        static_assert(2 * 16 * kKv4MaxSplits <= kAttnWaves * 16 * 68, "LDS of the joining");
+        float *sums = &lds_o[0][0][0], (*lds_w)[16] = (float(*)[16])(sums + 16 * kKv4MaxSplits);
+        for (int i = tid; i < splits * nc; i += 64 * kAttnWaves) {
+            const f32x4 ml = part_get<f32x4>(row_of(i / nc, i % nc) + D / 2);
+            lds_w[i / nc][i % nc] = ml[0];
+            sums[i] = ml[1];
+        }
+        __syncthreads();
+        if (tid < nc) {
+            float mm = kNegInf, ll = 0.0f;
+            for (int s = 0; s < splits; ++s) mm = fmaxf(mm, lds_w[s][tid]);
+            for (int s = 0; s < splits; ++s) {
+                const float ms = lds_w[s][tid];
+                const float a = ms == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms - mm);
+                lds_w[s][tid] = a;
+                ll += a * sums[s * nc + tid];
+            }
+            lds_l[tid] = ll;
+        }
+        __syncthreads();
+        for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
+            const int col = i / (D / 4), d = 4 * (i % (D / 4));
+            f32x4 v = {0, 0, 0, 0};
+            for (int s0 = 0; s0 < splits; s0 += 4) {
+                f32x4 w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = s0 + k < splits ? part_get<f32x4>(row_of(s0 + k, col) + d / 2) : (f32x4){0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v += (s0 + k < splits ? lds_w[s0 + k][col] : 0.0f) * w[k];
+            }
+            const float ll = lds_l[col];
+            put_row(16 * n + col, d, ll > 0.0f || ll != ll ? v / ll : (f32x4){0, 0, 0, 0});
+            for (int s = 0; s < splits; ++s) {
+                part_put(row_of(s, col) + d / 2, (f32x4){0, 0, 0, 0});
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < splits * nc; i += 64 * kAttnWaves)
+            part_put(row_of(i / nc, i % nc) + D / 2, (f32x4){0, 0, 0, 0});
+    }
+}
+
+template <int DT, int D, int NT>
+static hipError_t launch_attn(const Kv4AttnArgs &g, hipStream_t st) {
+    hipLaunchKernelGGL((kv4_attention_kernel<DT, D, NT>),
+                       dim3((unsigned)((int64_t)g.B * g.splits * g.Hkv * g.col_tiles)), dim3(64 * kAttnWaves), 0, st, g);
+    return hipGetLastError();
+}
+
+template <int DT, int D>
+static hipError_t launch_attn_nt(const Kv4AttnArgs &g, hipStream_t st) {
+    switch (g.nt) {
+        case 1: return launch_attn<DT, D, 1>(g, st);
+        case 2: return launch_attn<DT, D, 2>(g, st);
+        default: return launch_attn<DT, D, 4>(g, st);
+    }
+}
+
+hipError_t launch_kv4_attention(const Kv4AttnArgs &g, hipStream_t st) {
+    if (g.D == 128)
+        return g.dtype == DT_BF16 ? launch_attn_nt<DT_BF16, 128>(g, st) : launch_attn_nt<DT_F16, 128>(g, st);
+    return g.dtype == DT_BF16 ? launch_attn_nt<DT_BF16, 64>(g, st) : launch_attn_nt<DT_F16, 64>(g, st);
+}
+
+}  // namespace awq4

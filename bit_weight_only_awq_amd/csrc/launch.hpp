@@ -157,4 +157,53 @@ hipError_t launch_repack_v2(const int32_t *qweight_v2, const int32_t *qzeros_v2,
 hipError_t launch_unpack(const int32_t *packed, void *vals, int64_t rows, int64_t cols, int layout,
                          hipStream_t st);
 
+// Residual addition + RMS norm + 8-bit output (norm.hip).
+struct NormArgs {
+    const void *x, *residual, *weight;  // residual: nullptr = none
+    void *residual_out;                 // x + residual (nullptr iff residual is)
+    void *y;                            // the norm in the activation type, or nullptr
+    void *a;                            // codes [M, K], or nullptr (y alone)
+    float *s1, *asum;                   // asum: nullptr = int8 codes, else E4M3
+    int64_t M, K;
+    float eps;
+    int dtype;
+};
+hipError_t launch_rmsnorm(const NormArgs &n, hipStream_t st);
+
+// Rotary positions and the 4-bit paged cache (kv4.hpp has its layout).
+struct Kv4AppendArgs {
+    const void *q, *k, *v;  // q: nullptr iff Hq == 0
+    int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+    const float *rope;         // [max_pos, rot]: cos, then sin
+    const int32_t *positions;  // [T]
+    const int64_t *slots;      // [T]; outside 0 .. num_pages * P - 1: not stored
+    void *q_out;               // [T, Hq, D]
+    int32_t *cache;
+    int64_t T, num_pages;
+    int Hq, Hkv, D, P, rot, max_pos, interleaved, dtype;
+};
+hipError_t launch_kv4_append(const Kv4AppendArgs &g, hipStream_t st);
+
+struct Kv4AttnArgs {
+    const void *q;          // [total_q, Hq, D]
+    const int32_t *cache;
+    const int32_t *tables;  // [B, table_stride] page ids; outside 0 .. num_pages - 1: no page
+    const int32_t *lens;    // [B]
+    const int32_t *cu_q;    // [B + 1], or nullptr (one new token each)
+    void *out;              // [total_q, Hq, D]
+    int64_t num_pages;
+    int B, total_q, max_q, Hq, Hkv, D, P, table_stride, window, dtype;
+    float scale;
+    // the plan
+    int nt;         // 16-column tiles of query rows per workgroup (1, 2, 4)
+    int col_tiles;  // workgroups along the query rows of a sequence and key/value head
+    int splits;     // most workgroups along a sequence's tokens
+    int min_steps;  // 32-token steps that a workgroup takes at least, where there are more workgroups
+    int part_cols;  // query rows of a tile that the partial sums hold
+    uint32_t *counters;
+    float *partials;
+};
+constexpr int kKv4MaxSplits = 128;
+hipError_t launch_kv4_attention(const Kv4AttnArgs &g, hipStream_t st);
+
 }  // namespace awq4

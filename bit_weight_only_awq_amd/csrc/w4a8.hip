@@ -21,14 +21,9 @@
 // the i-th MFMA (output column = 4*j + i within a 64-column set).
 #include "device.hpp"
 #include "launch.hpp"
+#include "quant_ops.hpp"
 
 namespace awq4 {
-
-// Rounding an fp32 value to the activation type (nearest even) and back.
-template <int DT>
-__device__ __forceinline__ float round_to_act(float v) {
-    return DT == DT_F16 ? (float)(f16)v : (float)(__bf16)v;
-}
 
 // ---------------------------------------------------------------------------
 // Activation quantisation, general form (any K): one workgroup (256 threads)
@@ -81,50 +76,6 @@ __global__ __launch_bounds__(256) void w4a8_quant_kernel(const uint16_t *__restr
         if (s != 0.0f) r = fminf(fmaxf(rintf(act_bits_to_f32<DT>(row[k]) / s), -128.0f), 127.0f);
         out[k] = (int8_t)r;
     }
-}
-
-// int8 codes of 8 fp16 or bf16 values (one 16-byte chunk) for the scale s,
-// given r ~ 1/s: round half to even of x / s, clamped to int8, without a
-// divide.  For x and s of one 16-bit type the exact quotient is a half-integer
-// or at least 2^-12 (fp16) / 2^-9 (bf16) from one, and x * r (r within a few
-// ulps of 1/s) stays within 2^-15 of it.
-// One FMA adds 1536, which rounds x * r to a multiple of 2^-13 (the fp32
-// spacing in [1024, 2048)): exact ties land on the half-integer, every other
-// quotient stays on its own side of it.  The clamp is taken in that shifted
-// range; adding 1.5 * 2^23 - 1536 then rounds to an integer (half to even)
-// held in the low mantissa bits, so the low byte of the sum's bits is the
-// int8 code.  Checked exhaustively against the correctly rounded fp32 divide
-// for every reachable s (bf16: every s >= 2^-126, whose reciprocal is a normal
-// fp32 value; smaller scales take the divide), every x and reciprocals up to
-// 3 ulps off.
-template <int DT>
-__device__ __forceinline__ u32x2 quant8(u32x4 v, float r) {
-    uint32_t b[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float f = act_bits_to_f32<DT>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-        const float t = __builtin_amdgcn_fmed3f(__builtin_fmaf(f, r, 1536.0f), 1536.0f - 128.0f, 1536.0f + 127.0f);
-        b[e] = bit_as<uint32_t>(t + (12582912.0f - 1536.0f));
-    }
-    u32x2 o;
-#pragma unroll
-    for (int w = 0; w < 2; ++w)  // low bytes of b[4w .. 4w+3]
-        o[w] = perm_b32(b[4 * w + 1], b[4 * w], 0x0C0C0400u) | perm_b32(b[4 * w + 3], b[4 * w + 2], 0x04000C0Cu);
-    return o;
-}
-
-// The same codes through the correctly rounded fp32 divide (bf16 scales
-// below 2^-126, whose reciprocal is not a normal fp32 value).
-template <int DT>
-__device__ __forceinline__ u32x2 quant8_div(u32x4 v, float s) {
-    u32x2 o = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t h = (v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-        const float qf = fminf(fmaxf(rintf(act_bits_to_f32<DT>(h) / s), -128.0f), 127.0f);
-        o[e >> 2] |= ((uint32_t)(int32_t)qf & 0xFFu) << (8 * (e & 3));
-    }
-    return o;
 }
 
 // Register-resident quantisation: one workgroup of T threads per row, each

@@ -309,6 +309,186 @@ def linear_w4a8_fp8(x, b, s2, want_acc: bool = False, out=None, a=None, s1=None,
     return (out, s1, acc) if want_acc else out
 
 
+# ----------------------------------------------------------------------------- RMS norm
+
+def _norm_args(x, weight, residual, residual_out, *outs):
+    _need_cuda(x, weight, residual, residual_out, *outs)
+    if x.dtype not in _F16 or x.dim() != 2:
+        raise ValueError("x must be fp16 or bf16, [rows, columns]")
+    if weight.dtype != x.dtype or weight.shape != x.shape[1:]:
+        raise ValueError("weight must have x's type and one value per column")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        return None
+    if residual_out is None:
+        residual_out = torch.empty_like(x)
+    for t in (residual, residual_out):
+        if t.dtype != x.dtype or t.shape != x.shape:
+            raise ValueError("the residual must have x's type and shape")
+    return residual_out
+
+
+def _same(t, shape, dtype, what):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{what} must be {tuple(shape)}, {dtype}")
+
+
+def rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None):
+    """y = norm(x + residual) * weight in x's type, for the W4A16 layers.
+    Returns y, or (y, x + residual) with a residual (residual_out may be the
+    residual itself, out may be x)."""
+    _same(out, x.shape, x.dtype, "out")
+    residual_out = _norm_args(x, weight, residual, residual_out, out)
+    out = torch.empty_like(x) if out is None else out
+    M, K = x.shape
+    L.check("w4a8_rmsnorm_quant", L.lib().w4a8_rmsnorm_quant(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(out), None, None, M, K, eps, _F16[x.dtype],
+        _stream(x.device)))
+    return out if residual is None else (out, residual_out)
+
+
+def rmsnorm_quant(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None, a8=None, s1=None):
+    """norm(x + residual) * weight as int8 codes with one scale per token, the
+    input of w4a8_gemm: (a8, s1, x + residual or None).  The norm itself is
+    written to y where given."""
+    M, K = x.shape
+    _same(y, x.shape, x.dtype, "y")
+    _same(a8, (M, K), torch.int8, "a8")
+    _same(s1, (M,), torch.float32, "s1")
+    residual_out = _norm_args(x, weight, residual, residual_out, y, a8, s1)
+    a8 = torch.empty(M, K, dtype=torch.int8, device=x.device) if a8 is None else a8
+    s1 = torch.empty(M, dtype=torch.float32, device=x.device) if s1 is None else s1
+    L.check("w4a8_rmsnorm_quant", L.lib().w4a8_rmsnorm_quant(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(a8), _ptr(s1), M, K, eps,
+        _F16[x.dtype], _stream(x.device)))
+    return a8, s1, residual_out
+
+
+def rmsnorm_quant_fp8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None, a=None, s1=None,
+                      asum=None):
+    """The same as E4M3 codes, the input of w4a8_fp8_gemm: (codes uint8, s1,
+    asum, x + residual or None)."""
+    M, K = x.shape
+    _same(y, x.shape, x.dtype, "y")
+    _same(a, (M, K), torch.uint8, "a")
+    _same(s1, (M,), torch.float32, "s1")
+    _same(asum, (M,), torch.float32, "asum")
+    residual_out = _norm_args(x, weight, residual, residual_out, y, a, s1, asum)
+    a = torch.empty(M, K, dtype=torch.uint8, device=x.device) if a is None else a
+    s1 = torch.empty(M, dtype=torch.float32, device=x.device) if s1 is None else s1
+    asum = torch.empty(M, dtype=torch.float32, device=x.device) if asum is None else asum
+    L.check("w4a8_fp8_rmsnorm_quant", L.lib().w4a8_fp8_rmsnorm_quant(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(a), _ptr(s1), _ptr(asum), M, K, eps,
+        _F16[x.dtype], _stream(x.device)))
+    return a, s1, asum, residual_out
+
+
+# ----------------------------------------------------------------------------- attention over a 4-bit cache
+
+def kv4_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, device=None) -> torch.Tensor:
+    """A zeroed paged key/value cache in 4 bits (layout: awq4.h), int32
+    [num_pages, kv_heads, words of a page and head]."""
+    words = int(L.lib().awq_kv4_head_words(head_dim, page_size))
+    if words == 0:
+        raise ValueError("head_dim must be 64 or 128, page_size a power of two from 16 to 1024")
+    return torch.zeros(num_pages, kv_heads, words, dtype=torch.int32, device="cuda" if device is None else device)
+
+
+def _kv4_page_size(cache, head_dim: int) -> int:
+    if cache.dim() != 3 or cache.dtype != torch.int32:
+        raise ValueError("cache must be int32 [num_pages, kv_heads, words]")
+    page = cache.shape[2] // (head_dim // 4 + 2)
+    if page * (head_dim // 4 + 2) != cache.shape[2]:
+        raise ValueError("the cache's words do not fit this head dimension")
+    return page
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scale: float = 1.0, device=None) -> torch.Tensor:
+    """fp32 [positions, rot]: the cosines, then the sines, of p / scale *
+    base^(-2i / rot) (scale > 1 stretches the positions for longer contexts),
+    from angles in 64 bits."""
+    inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    ang = (torch.arange(positions, dtype=torch.float64) / scale)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), 1).float().to("cuda" if device is None else device)
+
+
+def _heads(t, name):
+    """(stride of a token in elements) of [T, H, D] with dense heads."""
+    if t.dim() != 3 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense heads")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def kv4_append(q, k, v, rope, positions, slots, cache, interleaved: bool = False, out=None):
+    """Rotary positions on q and k [T, H, D] (rope: fp32 [max_pos, rot], None =
+    no rotation), k and v quantised to 4 bits into the cache's slots; returns
+    the rotated q (None for q = None).  q, k and v may be views of one fused
+    QKV tensor."""
+    for t in (q, k, v, rope, positions, slots, cache):
+        if t is not None and not t.is_cuda:
+            raise ValueError("all tensors must be on a CUDA (HIP) device")
+    _need_cuda(rope, positions, slots, cache, out)
+    T, hkv, D = k.shape
+    if k.dtype not in _F16 or v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must be fp16 or bf16, of one type and shape")
+    if q is not None and (q.dtype != k.dtype or q.shape[0] != T or q.shape[2] != D):
+        raise ValueError("q must have k's type, tokens and head dimension")
+    if cache.shape[1] != hkv:
+        raise ValueError("the cache has another number of key/value heads")
+    _same(slots, (T,), torch.int64, "slots")
+    rot = max_pos = 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype != torch.float32:
+            raise ValueError("rope must be fp32 [max_pos, rot]")
+        max_pos, rot = rope.shape
+        if positions is None:
+            raise ValueError("rope without positions")
+        _same(positions, (T,), torch.int32, "positions")
+    hq = 0 if q is None else q.shape[1]
+    if q is not None:
+        _same(out, q.shape, q.dtype, "out")
+        out = torch.empty(T, hq, D, dtype=q.dtype, device=q.device) if out is None else out
+    page = _kv4_page_size(cache, D)
+    L.check("awq_kv4_append", L.lib().awq_kv4_append(
+        _ptr(q), _ptr(k), _ptr(v), 0 if q is None else _heads(q, "q"), _heads(k, "k"), _heads(v, "v"), _ptr(rope),
+        _ptr(positions) if rope is not None else None, _ptr(slots), _ptr(out), _ptr(cache), T, hq, hkv, D, page,
+        cache.shape[0], rot, max_pos, int(interleaved), _F16[k.dtype], _stream(k.device)))
+    return out
+
+
+def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None, max_q: int = 1,
+                  max_kv: int | None = None, window: int = 0, out=None):
+    """Causal attention of q [total_q, Hq, D] over the paged 4-bit cache.
+    tables int32 [B, pages of a sequence], lens int32 [B] (tokens with the new
+    ones); cu_q int32 [B + 1] and max_q where sequences have more than one new
+    token; max_kv: the longest sequence (default: what the tables can hold);
+    scale: default 1 / sqrt(D)."""
+    _need_cuda(q, cache, tables, lens, cu_q, out)
+    if q.dtype not in _F16 or q.dim() != 3:
+        raise ValueError("q must be fp16 or bf16 [tokens, heads, head_dim]")
+    total, hq, D = q.shape
+    B = lens.shape[0]
+    if tables.dim() != 2 or tables.shape[0] != B or tables.dtype != torch.int32:
+        raise ValueError("tables must be int32 [sequences, pages]")
+    _same(lens, (B,), torch.int32, "lens")
+    _same(cu_q, (B + 1,), torch.int32, "cu_q")
+    _same(out, q.shape, q.dtype, "out")
+    page = _kv4_page_size(cache, D)
+    hkv = cache.shape[1]
+    if max_kv is None:
+        max_kv = tables.shape[1] * page
+    out = torch.empty_like(q) if out is None else out
+    with torch.cuda.device(q.device):
+        need = int(L.lib().awq_kv4_attention_workspace_bytes(B, max_q, hq, hkv, D, max_kv))
+    ws = WORKSPACE.get(q.device, need)
+    L.check("awq_kv4_attention", L.lib().awq_kv4_attention(
+        _ptr(q), _ptr(cache), _ptr(tables), _ptr(lens), _ptr(cu_q), _ptr(out), B, total, max_q, max_kv, hq, hkv, D,
+        page, cache.shape[0], tables.shape[1], D ** -0.5 if scale is None else scale, window, _F16[q.dtype], _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(q.device)))
+    return out
+
+
 # ----------------------------------------------------------------------------- measurement helper
 
 STREAM_SINK_WORDS = 8192

@@ -7,6 +7,8 @@
  * M <= 8) and a prefill regime (GEMM, any M), plus the QQQ-style W4A8 variant
  * (per-token int8 activations x symmetric int4 weights, exact int32
  * accumulation, per-token and per-channel (optionally per-group) scales).
+ * Around those layers it has RMS norm with the residual's addition and an
+ * 8-bit output, and attention over a paged key/value cache in 4 bits.
  *
  * Sources (web pages, cited by title and passage):
  *  [P1] vLLM pull request "Speed up AWQ 2.5x with updated kernel": the list of
@@ -27,7 +29,9 @@
  *
  * Conventions for every entry point:
  *  - All tensors are dense, row-major and contiguous, in device memory owned
- *    by the caller.  Device pointers must be 16-byte aligned (AWQ_EALIGN).
+ *    by the caller (awq_kv4_append takes token strides).  Device pointers must
+ *    be 16-byte aligned (AWQ_EALIGN), those of the kv4 calls' index arrays
+ *    aligned to their type.
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *    Work is enqueued on it; no entry point synchronises or allocates device
  *    memory, so all of them are asynchronous and safe to call from several
@@ -386,6 +390,144 @@ int w4a8_fp8_gemm(const uint8_t *a, const int32_t *b_packed, const float *s1, co
 int w4a8_fp8_linear(const void *x, uint8_t *a, float *s1, float *asum, const int32_t *b_packed,
                     const void *s2, void *y, float *acc_out, int64_t M, int64_t N, int64_t K, int dtype,
                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The operators around the linear layers: RMS norm with an 8-bit output, and
+ * the attention block's cache in 4 bits.  fl32(v) is v rounded to binary32
+ * and act(v) v rounded to the activation type, both to nearest even; every
+ * rounding written below is part of the definition, so codes, scales and
+ * packed words are the same bits on every run, launch and machine.
+ *
+ * w4a8_rmsnorm_quant -- residual addition, root-mean-square norm and per-token
+ * int8 quantisation in one pass, the input of w4a8_gemm:
+ *   h[m,k]  = act( fl32( x + residual ) )            (no residual: h = x)
+ *   v[m]    = fl32( sum_k h^2 / K + eps )            (sum and quotient in binary64)
+ *   q[m]    = fl32( 1 / fl32( sqrt(v) ) )
+ *   y[m,k]  = act( fl32( fl32( h q ) weight[k] ) )
+ *   s1, a8  = w4a8_quant_act of y
+ *   x, residual: device fp16/bf16 [M, K] (dtype); residual NULL = none.
+ *   weight:      device [K], same type.
+ *   residual_out: device [M, K], h (written); NULL iff residual is.  May be
+ *                residual itself, or x.
+ *   y:           device [M, K], the norm in the activation type, or NULL.
+ *                May be x (where residual_out is not).
+ *   a8, s1:      device int8 [M, K] and fp32 [M]; both NULL for the norm alone
+ *                (then y must be given), the input of a W4A16 layer.
+ *   No other tensors may overlap.  A row whose h holds a NaN or an infinity,
+ *   or whose norm overflows the activation type, has an s1 that is not
+ *   finite; its codes mean nothing.  eps >= 0 and finite.
+ * Errors: AWQ_EINVAL (M, K < 1, K > 2^20, pointers, dtype, eps), AWQ_EALIGN,
+ * AWQ_EHIP.
+ */
+int w4a8_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *residual_out, void *y,
+                       int8_t *a8, float *s1, int64_t M, int64_t K, float eps, int dtype, void *stream);
+
+/*
+ * w4a8_fp8_rmsnorm_quant -- the same with E4M3 codes, the input of
+ * w4a8_fp8_gemm: s1, a, asum = w4a8_fp8_quant_act of y.  a, s1 and asum must
+ * be given.
+ */
+int w4a8_fp8_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *residual_out, void *y,
+                           uint8_t *a, float *s1, float *asum, int64_t M, int64_t K, float eps, int dtype,
+                           void *stream);
+
+/*
+ * The paged key/value cache in 4 bits: int32 [num_pages, Hkv, W] with
+ * W = awq_kv4_head_words(head_dim, page_size) = page_size (head_dim / 4 + 2).
+ * The words of one page and key/value head:
+ *   K words  [page_size][head_dim/8]       AWQ_LAYOUT_N8 along the dimensions
+ *   V words  [page_size/4][head_dim/8][4]  the same words, those of four
+ *                                          consecutive tokens side by side
+ *   K meta   [page_size], V meta [page_size]
+ *            bits 15..0 the scale s in the activation type, 31..16 the zero
+ *            point z (0..15), one pair per token and head
+ * and value = (code - z) s, as for the weights.  head_dim 64 or 128;
+ * page_size a power of two, 16..1024.  A page belongs to the sequences whose
+ * block tables name it; the library keeps no other state, and no word that is
+ * not read below need be initialised.
+ *
+ * awq_kv4_head_words -- W, or 0 for sizes the library does not take.
+ */
+int64_t awq_kv4_head_words(int64_t head_dim, int64_t page_size);
+
+/*
+ * awq_kv4_append -- rotary positions on the queries and keys of T tokens, and
+ * their keys and values quantised into the cache.
+ * Rotation of the pair (x1, x2) with the cosine c and sine s of its angle:
+ *   act( fl32( fl32(x1 c) - fl32(x2 s) ) ),  act( fl32( fl32(x2 c) + fl32(x1 s) ) )
+ * over the first `rot` dimensions of each head, pairs (i, i + rot/2), or
+ * (2i, 2i + 1) if interleaved; angle i of position p is row p of the table.
+ * Quantisation of one token and head x (keys after the rotation):
+ *   lo = min(0, min x), hi = max(0, max x), s = act( fl32( fl32(hi - lo) / 15 ) )
+ *   z = min( rint( fl32(-lo / s) ), 15 ),  code = clamp( rint( fl32(x / s) ) + z, 0, 15 )
+ * with rint to nearest even; s = 0 gives z = code = 0.  A head that holds a
+ * NaN or an infinity is stored as s = NaN, z = code = 0.
+ *   q, k, v:   device [T, Hq or Hkv, head_dim] (dtype), the heads of a token
+ *              dense, q_stride / k_stride / v_stride elements from one token
+ *              to the next (multiples of 8), so that a fused QKV product's
+ *              output serves as all three.  q NULL iff Hq == 0.
+ *   rope:      device fp32 [max_pos, rot]: rot/2 cosines, then rot/2 sines.
+ *              rot a multiple of 16, 0..head_dim; 0 = no rotation (rope and
+ *              positions may be NULL).
+ *   positions: device int32 [T].  A token whose position is outside
+ *              0..max_pos-1 is not stored and its rotated query dimensions
+ *              are NaN.
+ *   slots:     device int64 [T], page * page_size + place in the page; a slot
+ *              outside the cache (-1, say) stores nothing.  Two tokens with
+ *              one slot leave either's words.
+ *   q_out:     device [T, Hq, head_dim], dense; may be q where q is dense.
+ * T == 0 is a no-op that returns AWQ_OK.  Index arrays need the alignment of
+ * their type only.
+ * Errors: AWQ_EINVAL, AWQ_EUNSUPPORTED (head_dim, page_size), AWQ_EALIGN
+ * (strides too), AWQ_EHIP.
+ */
+int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   const float *rope, const int32_t *positions, const int64_t *slots, void *q_out, int32_t *cache,
+                   int64_t T, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t page_size, int64_t num_pages,
+                   int64_t rot, int64_t max_pos, int interleaved, int dtype, void *stream);
+
+/*
+ * awq_kv4_attention -- causal attention of B sequences' new tokens over the
+ * cache (which holds the new tokens' keys and values too: append first).
+ * Sequence b has n = cu_q[b+1] - cu_q[b] new tokens, rows cu_q[b].. of q, and
+ * L = lens[b] tokens in all; its new token i stands at p = L - n + i and sees
+ * the tokens j <= p, with a window w > 0 only j > p - w:
+ *   out = sum_j softmax_j( scale q . k_j ) v_j
+ * over the keys and values that the cache's words stand for.  Query head e
+ * reads key/value head e / (Hq / Hkv).  A row that sees nothing (p < 0,
+ * L = 0) is 0.
+ *   q, out:  device [total_q, Hq, head_dim], dense; out may be q.
+ *   tables:  device int32 [B, table_stride]: entry t / page_size names the
+ *            page of token t.  An entry that names no page of the cache (-1)
+ *            hides its tokens.
+ *   lens:    device int32 [B]; taken as 0 below 0 and as table_stride *
+ *            page_size above it.
+ *   cu_q:    device int32 [B + 1], rising from 0 to total_q; NULL = one new
+ *            token per sequence (total_q == B, max_q == 1).
+ *   max_q:   the most new tokens of a sequence (the rows of a sequence past
+ *            its first max_q are not written).
+ *   max_kv:  the longest sequence, or an upper bound: it sizes the launch and
+ *            the workspace, no result depends on it being close.
+ * Numerics: the codes enter the matrix cores exactly; scores, running maxima,
+ * sums and outputs are fp32; the softmax numerators times the values' scales
+ * are rounded once to 11 bits for the second product; out is rounded to
+ * nearest even.  A NaN or infinity in q, or a NaN scale in a token that a row
+ * sees, makes that row NaN; nothing that no row sees is used.
+ * Workspace: as for the GEMMs (shared, zero before and after each call).
+ * B == 0 or total_q == 0 is a no-op that returns AWQ_OK.
+ * Errors: AWQ_EINVAL (also scale <= 0), AWQ_EUNSUPPORTED (head_dim,
+ * page_size, more than 2^31 workgroups), AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
+ */
+int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables, const int32_t *lens,
+                      const int32_t *cu_q, void *out, int64_t B, int64_t total_q, int64_t max_q, int64_t max_kv,
+                      int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t page_size, int64_t num_pages,
+                      int64_t table_stride, float scale, int64_t window, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that awq_kv4_attention needs on the current device (0 if
+ * none, or for invalid arguments). */
+size_t awq_kv4_attention_workspace_bytes(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t head_dim,
+                                         int64_t max_kv);
 
 /*
  * awq_stream_read -- measurement helper, not a step of the method: reads
