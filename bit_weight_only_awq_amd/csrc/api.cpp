@@ -621,6 +621,7 @@ static int check_attention(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, in
     if (B < 0 || max_q < 1 || max_kv < 0 || B > kMaxDim || max_q > 16 * kMaxDim || max_kv > kMaxTokens)
         return AWQ_EINVAL;
     if (Hkv < 1 || Hq < 1 || Hq > kMaxHeads || Hkv > kMaxHeads || Hq % Hkv) return AWQ_EINVAL;
+    if (max_q * (Hq / Hkv) > (int64_t(1) << 31) - 64) return AWQ_EUNSUPPORTED;
     if (D != 64 && D != 128) return D < 1 ? AWQ_EINVAL : AWQ_EUNSUPPORTED;
     return AWQ_OK;
 }

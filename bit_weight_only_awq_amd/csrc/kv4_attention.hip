@@ -13,11 +13,17 @@
 // act on the fp32 scores, and on the value side the scale is folded into the
 // probabilities, whose one rounding (to fp16, the matrix cores' type; the
 // values' codes are exact in it) is the only one between q and the output's:
-//   P_j = fp16(softmax numerator * s'_j 2^(14 - E)),  O = sum P_j c'_j - sum P_j z'_j
-// E is the exponent of the largest s' met so far, raised together with the
-// running maximum: P then uses fp16's whole range (a probability 2^-28 times
-// the largest still has all 11 bits) whatever the scales' magnitude.  The sum
-// of z' takes the rounded P, so that a code and its zero point lose the same.
+//   p_j = 2^(t_j log2(e) - R),  P_j = fp16(p_j s'_j)
+//   O = (sum P_j c'_j - sum P_j z'_j) / sum p_j
+// The reference R of a row is raised when a P_j would pass 2^15 (or a p_j 2^100,
+// for values whose scale is next to nothing), to put the largest at 2^11: P
+// then uses fp16's whole range, and one 2^-25 times the largest still has all 11
+// bits, whatever the scales' magnitude.  Most steps find nothing to raise and
+// need no exchange between lanes.  The sum of z' takes the rounded P, so that
+// a code and its zero point lose the same, and it is taken off step by step:
+// codes average 7.5, and the sums of long contexts would otherwise lose what
+// is left after 7.5 has gone (131072 tokens: 8.4e-4 of the output against
+// 2.5e-4, the two roundings to 11 bits).  It costs matrix-core time only.
 // Queries are scaled by a power of two to just below 2^15 before they become
 // fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest.
 //
@@ -65,34 +71,34 @@ __device__ __forceinline__ u32x4 word_operand(uint32_t w) {
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    typedef float f32x2v __attribute__((ext_vector_type(2)));
-    return bit_as<uint32_t>(__builtin_convertvector((f32x2v){a, b}, f16x2));
+    return bit_as<uint32_t>(__builtin_convertvector((f32x2){a, b}, f16x2));
 }
 
 // What one wave reads for 32 tokens: two tiles of 16.
 template <int D>
 struct Kv4Step {
     static constexpr int KW = D / 32;  // words of a token in a lane
-    uint32_t k[2][KW];
+    typedef uint32_t Words __attribute__((ext_vector_type(KW)));
+    Words k[2];
     u32x4 v[2], km[2], vm[2];
 };
 
+constexpr float kNoRef = -1e30f;      // the reference of a row that has seen nothing
+constexpr float kMaxP = 0x1p15f, kMaxSum = 0x1p100f;
+
 template <int DT, int D, int NT>
-__global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnArgs g) {
+__global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) void kv4_attention_kernel(Kv4AttnArgs g) {
     using L = Kv4Layout<D>;
+    using Step = Kv4Step<D>;
     constexpr int COLS = 16 * NT, KW = D / 32, VM = D / 16, ROW = D + 4;
-    constexpr float kNegInf = -__builtin_inff();
-    __shared__ float lds_o[kAttnWaves][16][ROW];  // one 16-column tile of every wave; at D its m, at D + 1 its l
-    __shared__ float lds_l[16];
+    __shared__ float lds_o[kAttnWaves][16][ROW];  // one 16-column tile of every wave; at D its R, at D + 1 its sum of p
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, grp = lane >> 4;
-    // workgroup -> (sequence, split, head, column tile)
-    int id = blockIdx.x;
-    const int tile_h = id % (g.Hkv * g.col_tiles);
-    id /= g.Hkv * g.col_tiles;
-    const int split = id % g.splits, b = id / g.splits;
-    const int h = tile_h / g.col_tiles, ct = tile_h % g.col_tiles;
+    // workgroup -> (sequence, head, column tile), split
+    const int tile = blockIdx.x, split = blockIdx.y;
+    const int ct = tile % g.col_tiles, bh = tile / g.col_tiles;
+    const int h = bh % g.Hkv, b = bh / g.Hkv;
     const int G = g.Hq / g.Hkv;
 
     // the sequence's rows and length; whatever the arrays hold, no index
@@ -103,24 +109,61 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
         q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
     }
     const int nq = q1 - q0;
-    const int kv_len = (int)min((int64_t)max(g.lens[b], 0), (int64_t)g.table_stride * g.P);
-    const int64_t rows = (int64_t)min(nq, g.max_q) * G;
-    const int64_t c0 = (int64_t)ct * COLS;
+    const int kv_len = min(max(g.lens[b], 0), g.table_stride * g.P);
+    const int rows = min(nq, g.max_q) * G, c0 = ct * COLS;
     if (c0 >= rows) return;
-    const int ncols = (int)min((int64_t)COLS, rows - c0);
+    const int ncols = min(COLS, rows - c0);
 
     // tokens that any column of the tile sees: [kv_lo, kv_hi)
-    const int first_pos = kv_len - nq + (int)(c0 / G), last_pos = kv_len - nq + (int)((c0 + ncols - 1) / G);
+    const int first_pos = kv_len - nq + c0 / G, last_pos = kv_len - nq + (c0 + ncols - 1) / G;
     const int kv_hi = max(last_pos + 1, 0);
     const int kv_lo = g.window > 0 ? min(max(first_pos - g.window + 1, 0), kv_hi) : 0;
     // ... and that all of them see: [all_lo, all_hi)
     const int all_hi = first_pos + 1;
-    const int all_lo = g.window > 0 ? last_pos - g.window + 1 : 0;
+    const int all_lo = g.window > 0 ? max(last_pos - g.window + 1, 0) : 0;
     const int step0 = kv_lo >> 5, steps = kv_hi > kv_lo ? ((kv_hi + 31) >> 5) - step0 : 0;
     const int splits = max(1, min(g.splits, (steps + g.min_steps - 1) / g.min_steps));
     if (split >= splits) return;
     const int per = (steps + splits - 1) / splits;
     const int s_begin = step0 + split * per, s_end = min(step0 + steps, s_begin + per);
+
+    const int lgP = __builtin_ctz(g.P);
+    // (in the constant address space: no kernel of this call writes it, so it is
+    // read through the scalar cache)
+    const auto *table = (const __attribute__((address_space(4))) int32_t *)(g.tables + (size_t)b * g.table_stride);
+    const int64_t page_bytes = (int64_t)g.Hkv * L::head_words(g.P) * 4;
+    const char *head = (const char *)g.cache + (int64_t)h * L::head_words(g.P) * 4;
+    // this lane's place in a tile of 16 tokens, in bytes after the tile's first word
+    const uint32_t k_at = 4 * L::k_word(r16, KW * grp), m_at = 16 * grp;
+    const uint32_t v_at = 4 * L::v_word(g.P, 4 * grp, D == 128 ? r16 : (r16 & 7));
+    const uint32_t km_at = 4 * L::k_meta(g.P, 0) + m_at, vm_at = 4 * L::v_meta(g.P, 0) + m_at;
+    // the page that holds tokens t .. t + 15, or -1
+    auto page_of = [&](int t) -> int {
+        if (t >= kv_len) return -1;
+        const int p = __builtin_amdgcn_readfirstlane(table[t >> lgP]);
+        return p >= 0 && p < g.num_pages ? p : -1;
+    };
+    auto load = [&](Step &s, int p0, int p1, int t0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = (t0 + 16 * i) & (g.P - 1);
+            const char *base = head + max(i ? p1 : p0, 0) * page_bytes;
+            const char *words = base + t * (4 * L::kWords), *metas = base + 4 * t;
+            s.k[i] = *(const typename Step::Words *)(words + k_at);
+            s.v[i] = *(const u32x4 *)(words + v_at);
+            s.km[i] = *(const u32x4 *)(metas + km_at);
+            s.vm[i] = *(const u32x4 *)(metas + vm_at);
+        }
+    };
+
+    // the first step's loads before anything else
+    Step cur, nxt;
+    int st = s_begin + wave, p0 = -1, p1 = -1;
+    if (st < s_end) {
+        p0 = page_of(32 * st);
+        p1 = page_of(32 * st + 16);
+        load(cur, p0, p1, 32 * st);
+    }
 
     // this lane's columns: their rows of q as matrix-core operand, in fp16
     u32x4 qf[NT][KW];
@@ -130,8 +173,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
     for (int n = 0; n < NT; ++n) {
         const int col = 16 * n + r16;
         const bool live = col < ncols;
-        const int64_t row = c0 + (live ? col : 0);
-        const int qi = (int)(row / G), hg = (int)(row - (int64_t)qi * G);
+        const int row = c0 + (live ? col : 0);
+        const int qi = row / G, hg = row - qi * G;
         const int pos = kv_len - nq + qi;
         hi[n] = pos + 1;
         lo[n] = g.window > 0 ? pos - g.window + 1 : 0;
@@ -148,7 +191,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
         }
         mx = column_max(mx);
         const int ex = (int)(bit_as<uint32_t>(mx) >> 23);
-        const int up = ex == 255 ? 0 : 127 + 14 - ex;
+        const int up = ex == 255 || ex == 0 ? 0 : min(127 + 14 - ex, 100);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
@@ -165,51 +208,19 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
         cf[n] = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
     }
 
-    const int lgP = __builtin_ctz(g.P);
-    const int32_t *table = g.tables + (size_t)b * g.table_stride;
-    const int hw = L::head_words(g.P);
-    // the page that holds tokens t .. t + 15, or -1
-    auto page_of = [&](int t) -> int {
-        if (t >= kv_len) return -1;
-        const int p = table[t >> lgP];
-        return p >= 0 && p < g.num_pages ? p : -1;
-    };
-    auto load = [&](Kv4Step<D> &s, int p0, int p1, int t0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int page = max(i ? p1 : p0, 0), t = (t0 + 16 * i) & (g.P - 1);
-            const uint32_t *base = (const uint32_t *)g.cache + ((size_t)page * g.Hkv + h) * hw;
-            const uint32_t *kp = base + L::k_word(t + r16, KW * grp);
-            if (KW == 4) {
-                const u32x4 w = *(const u32x4 *)kp;
-#pragma unroll
-                for (int j = 0; j < KW; ++j) s.k[i][j] = w[j];
-            } else {
-                const u32x2 w = *(const u32x2 *)kp;
-#pragma unroll
-                for (int j = 0; j < KW; ++j) s.k[i][j] = w[j];
-            }
-            s.v[i] = *(const u32x4 *)(base + L::v_word(g.P, t + 4 * grp, D == 128 ? r16 : (r16 & 7)));
-            s.km[i] = *(const u32x4 *)(base + L::k_meta(g.P, t + 4 * grp));
-            s.vm[i] = *(const u32x4 *)(base + L::v_meta(g.P, t + 4 * grp));
-        }
-    };
-
-    f32x4 o[NT][VM], oz[NT];
-    float m[NT], l[NT];
-    int e_run = 27;  // exponent field of the largest value scale so far (from 2^-100 on)
+    f32x4 o[NT][VM];
+    float ref[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        m[n] = kNegInf;
+        ref[n] = kNoRef;
         l[n] = 0.0f;
-        oz[n] = (f32x4){0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < VM; ++t) o[n][t] = (f32x4){0, 0, 0, 0};
     }
     const uint32_t half_sel = (D == 128 || r16 < 8) ? 0x05040100u : 0x07060302u;
 
-    auto compute = [&](Kv4Step<D> &s, int p0, int p1, int t0) {
-        const bool plain = p0 >= 0 && p1 >= 0 && t0 >= all_lo && t0 + 32 <= all_hi && t0 >= kv_lo;
+    // One step.  plain: every token of it is there and every column sees it.
+    auto compute = [&](Step &s, bool plain, int p0, int p1, int t0) {
         if (!plain) {
             // tokens that no column sees, or without a page: whatever their
             // meta words hold must not reach the sums
@@ -223,84 +234,99 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
                     s.vm[i][r] = any ? s.vm[i][r] : 0u;
                 }
         }
-        float ks[2][4], kz[2][4], vs[2][4], top = 0.0f;
+        f32x4 x[NT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][i] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                const u32x4 a = word_operand(s.k[i][j]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[n][i] = mfma_f16(a, qf[n][j], x[n][i]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float vs[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                ks[i][r] = act_bits_to_f32<DT>(s.km[i][r] & 0xFFFFu);
-                kz[i][r] = (float)((s.km[i][r] >> 16) & 0xFFu);
+                const float ks = act_bits_to_f32<DT>(s.km[i][r] & 0xFFFFu);
+                const float kz = (float)((s.km[i][r] >> 16) & 0xFFu);
                 vs[i][r] = act_bits_to_f32<DT>(s.vm[i][r] & 0xFFFFu);
-                top = fmaxf(top, vs[i][r]);  // (a NaN scale does not count)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[n][i][r] = __builtin_fmaf(-kz, qz[n], x[n][i][r]) * ks;
             }
-        top = column_max(top);
-        const int e_now = max(e_run, min((int)(bit_as<uint32_t>(top) >> 23), 254));
-        const float down = __builtin_ldexpf(1.0f, e_run - e_now), vf = __builtin_ldexpf(1.0f, 127 + 14 - e_now);
-        const bool raised = e_now != e_run;
-        e_run = e_now;
-        u32x4 ko[2][KW];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < KW; ++j) ko[i][j] = word_operand(s.k[i][j]);
         u32x4 pf[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float x[2][4], mx = kNegInf;
+            auto seen = [&](int i, int r) {
+                const int j = t0 + 16 * i + 4 * grp + r;
+                return (i ? p1 : p0) >= 0 && j >= lo[n] && j < hi[n];
+            };
+            float p[2][4], w[2][4], top, sum;
+            auto numerators = [&] {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f32x4 a = {0, 0, 0, 0};
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < KW; ++j) a = mfma_f16(ko[i][j], qf[n][j], a);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[i][r] = __builtin_fmaf(-kz[i][r], qz[n], a[r]) * ks[i][r];
-                    if (!plain) {
-                        const int j = t0 + 16 * i + 4 * grp + r;
-                        const bool seen = (i ? p1 : p0) >= 0 && j >= lo[n] && j < hi[n];
-                        x[i][r] = seen ? x[i][r] : kNegInf;
+                    for (int r = 0; r < 4; ++r) {
+                        p[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][i][r], cf[n], -ref[n]));
+                        w[i][r] = p[i][r] * vs[i][r];
                     }
-                    mx = fmaxf(mx, x[i][r]);
+                if (!plain) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const bool on = seen(i, r);
+                            p[i][r] = on ? p[i][r] : 0.0f;
+                            w[i][r] = on ? w[i][r] : 0.0f;
+                        }
                 }
-            }
-            mx = fmaxf(m[n], column_max(mx));
-            if (__builtin_amdgcn_ballot_w64(mx > m[n]) != 0 || raised) {
-                const float alpha = m[n] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m[n] - mx) * cf[n]);
-                const float od = alpha * down;
-                l[n] *= alpha;
-                oz[n] *= od;
+                top = sum = 0.0f;
 #pragma unroll
-                for (int t = 0; t < VM; ++t) o[n][t] *= od;
-                m[n] = mx;
-            }
-            const float ref = mx == kNegInf ? 0.0f : mx * cf[n];
-            float p[2][4];
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], cf[n], -ref));
-                    float w = e * (vs[i][r] * vf);
-                    if (!plain) {
-                        const bool seen = x[i][r] != kNegInf;
-                        e = seen ? e : 0.0f;
-                        w = seen ? w : 0.0f;
+                    for (int r = 0; r < 4; ++r) {
+                        sum += p[i][r];
+                        top = fmaxf(top, w[i][r]);
                     }
-                    l[n] += e;
-                    p[i][r] = w;
-                }
-            pf[n] = (u32x4){pack_f16(p[0][0], p[0][1]), pack_f16(p[0][2], p[0][3]), pack_f16(p[1][0], p[1][1]),
-                            pack_f16(p[1][2], p[1][3])};
-        }
-        // the values' zero points as an operand with equal rows
-        u32x4 zo;
+            };
+            numerators();
+            if (__builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0) {
+                float t = ref[n];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            zo[2 * i] = perm_b32(s.vm[i][1], s.vm[i][0], 0x07060302u);
-            zo[2 * i + 1] = perm_b32(s.vm[i][3], s.vm[i][2], 0x07060302u);
-        }
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) oz[n] = mfma_f16(zo, pf[n], oz[n]);
+                    for (int r = 0; r < 4; ++r) {
+                        const float y = x[n][i][r] * cf[n];
+                        const float c = fmaxf(y + __builtin_amdgcn_logf(vs[i][r]) - 11.0f, y - 90.0f);
+                        t = plain || seen(i, r) ? fmaxf(t, c) : t;
+                    }
+                t = column_max(t);
+                const float f = __builtin_amdgcn_exp2f(ref[n] - t);
+                ref[n] = t;
+                l[n] *= f;
+#pragma unroll
+                for (int u = 0; u < VM; ++u) o[n][u] *= f;
+                numerators();
+            }
+            l[n] += sum;
+            pf[n] = (u32x4){pack_f16(w[0][0], w[0][1]), pack_f16(w[0][2], w[0][3]), pack_f16(w[1][0], w[1][1]),
+                            pack_f16(w[1][2], w[1][3])};
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // the values' zero points as an operand with equal rows, negative, for
+        // columns without and with the factor 16
+        u32x4 z1, z16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t z =
+                perm_b32(s.vm[i >> 1][2 * (i & 1) + 1], s.vm[i >> 1][2 * (i & 1)], 0x07060302u);
+            z1[i] = z | 0x80008000u;
+            z16[i] = (z << 4) | 0x80008000u;
+        }
         // the values' codes: consecutive tokens side by side, one column a mask
         uint32_t px[4], py[4];
 #pragma unroll
@@ -321,84 +347,73 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
                 a[i] = (pos & 2 ? w >> 8 : w) & mask;
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[n][t] = mfma_f16(a, pf[n], o[n][t]);
+            for (int n = 0; n < NT; ++n) o[n][t] = mfma_f16(a, pf[n], mfma_f16(pos & 1 ? z16 : z1, pf[n], o[n][t]));
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    {
-        int st = s_begin + wave;
-        if (st < s_end) {
-            Kv4Step<D> cur, nxt;
-            int p0 = page_of(32 * st), p1 = page_of(32 * st + 16);
-            load(cur, p0, p1, 32 * st);
-            while (true) {
-                const int sn = st + kAttnWaves;
-                const bool more = sn < s_end;
-                int n0 = -1, n1 = -1;
-                if (more) {
-                    n0 = page_of(32 * sn);
-                    n1 = page_of(32 * sn + 16);
-                    load(nxt, n0, n1, 32 * sn);
-                }
-                compute(cur, p0, p1, 32 * st);
-                if (!more) break;
-                cur = nxt;
-                st = sn;
-                p0 = n0;
-                p1 = n1;
-            }
+    while (st < s_end) {
+        const int sn = st + kAttnWaves;
+        int n0 = -1, n1 = -1;
+        if (sn < s_end) {
+            n0 = page_of(32 * sn);
+            n1 = page_of(32 * sn + 16);
+            load(nxt, n0, n1, 32 * sn);
         }
+        const int t0 = 32 * st;
+        compute(cur, p0 >= 0 && p1 >= 0 && t0 >= all_lo && t0 + 32 <= all_hi, p0, p1, t0);
+        cur = nxt;
+        st = sn;
+        p0 = n0;
+        p1 = n1;
     }
 
     // Join the four waves, 16 columns at a time; then write, or exchange with
     // the sequence's other workgroups.
-    const int64_t tile = ((int64_t)b * g.Hkv + h) * g.col_tiles + ct;
-    float *part = splits > 1 ? g.partials + tile * g.splits * (g.part_cols * ROW) : nullptr;
+    float *part = splits > 1 ? g.partials + (size_t)tile * g.splits * (g.part_cols * ROW) : nullptr;
     auto put_row = [&](int col, int d, f32x4 v) {
-        const int64_t row = c0 + col;
-        const int qi = (int)(row / G), hg = (int)(row - (int64_t)qi * G);
+        const int row = c0 + col, qi = row / G, hg = row - qi * G;
         *(uint2 *)((uint16_t *)g.out + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D + d) = quad_out_bits<DT>(v);
     };
+    // (a sum of p that is not a number shows in the row)
+    auto quotient = [](f32x4 v, float sum) { return sum == 0.0f ? (f32x4){0, 0, 0, 0} : v / sum; };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int nc = min(16, ncols - 16 * n);
         if (nc <= 0) break;
         if (n) __syncthreads();
         const float lsum = column_sum(l[n]);
-        const int back = e_run - 127 - 14 + 24;
 #pragma unroll
         for (int t = 0; t < VM; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 4 * grp + r;
                 const int d = D == 128 ? 8 * i + t : 8 * (i & 7) + 2 * t + (i >> 3);
-                const bool x16 = (D == 128 ? t >> 1 : t) & 1;
-                const float v = (x16 ? o[n][t][r] * 0.0625f : o[n][t][r]) - oz[n][r];
-                lds_o[wave][r16][d] = __builtin_ldexpf(v, back);
+                lds_o[wave][r16][d] = o[n][t][r] * ((D == 128 ? t >> 1 : t) & 1 ? 0x1p20f : 0x1p24f);
             }
         if (grp == 0) {
-            lds_o[wave][r16][D] = m[n] == kNegInf ? kNegInf : m[n] * cf[n];
+            lds_o[wave][r16][D] = ref[n];
             lds_o[wave][r16][D + 1] = lsum;
         }
         __syncthreads();
         for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
             const int col = i / (D / 4), d = 4 * (i % (D / 4));
-            float mw[kAttnWaves], mm = kNegInf, ll = 0.0f;
+            float rw[kAttnWaves], rr = kNoRef, ll = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, mw[w] = lds_o[w][col][D]);
+            for (int w = 0; w < kAttnWaves; ++w) rr = fmaxf(rr, rw[w] = lds_o[w][col][D]);
             f32x4 v = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kAttnWaves; ++w) {
-                const float a = mw[w] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw[w] - mm);
+                const float a = __builtin_amdgcn_exp2f(rw[w] - rr);
                 v += a * *(const f32x4 *)&lds_o[w][col][d];
                 ll += a * lds_o[w][col][D + 1];
             }
             if (splits == 1) {
-                put_row(16 * n + col, d, ll > 0.0f || ll != ll ? v / ll : (f32x4){0, 0, 0, 0});
+                put_row(16 * n + col, d, quotient(v, ll));
             } else {
                 float *p = part + ((size_t)split * g.part_cols + 16 * n + col) * ROW;
                 part_put((uint64_t *)(p + d), v);
-                if (d == 0) part_put((uint64_t *)(p + D), (f32x4){mm, ll, 0, 0});
+                if (d == 0) part_put((uint64_t *)(p + D), (f32x4){rr, ll, 0, 0});
             }
         }
     }
@@ -408,27 +423,28 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
     for (int n = 0; n < NT; ++n) {
         const int nc = min(16, ncols - 16 * n);
         if (nc <= 0) break;
-        auto row_of = [&](int s, int col) { return (uint64_t *)(part + ((size_t)s * g.part_cols + 16 * n + col) * ROW); };
+        auto row_of = [&](int s, int col) {
+            return (uint64_t *)(part + ((size_t)s * g.part_cols + 16 * n + col) * ROW);
+        };
         __syncthreads();
-        // the splits' sums, and their maxima and then weights
+        // the splits' sums, and their references and then weights
         static_assert(2 * 16 * kKv4MaxSplits <= kAttnWaves * 16 * 68, "LDS of the joining");
-        float *sums = &lds_o[0][0][0], (*lds_w)[16] = (float(*)[16])(sums + 16 * kKv4MaxSplits);
+        float *sums = &lds_o[0][0][0], (*weight)[16] = (float(*)[16])(sums + 16 * kKv4MaxSplits);
         for (int i = tid; i < splits * nc; i += 64 * kAttnWaves) {
-            const f32x4 ml = part_get<f32x4>(row_of(i / nc, i % nc) + D / 2);
-            lds_w[i / nc][i % nc] = ml[0];
-            sums[i] = ml[1];
+            const f32x4 rl = part_get<f32x4>(row_of(i / nc, i % nc) + D / 2);
+            weight[i / nc][i % nc] = rl[0];
+            sums[i] = rl[1];
         }
         __syncthreads();
         if (tid < nc) {
-            float mm = kNegInf, ll = 0.0f;
-            for (int s = 0; s < splits; ++s) mm = fmaxf(mm, lds_w[s][tid]);
+            float rr = kNoRef, ll = 0.0f;
+            for (int s = 0; s < splits; ++s) rr = fmaxf(rr, weight[s][tid]);
             for (int s = 0; s < splits; ++s) {
-                const float ms = lds_w[s][tid];
-                const float a = ms == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms - mm);
-                lds_w[s][tid] = a;
+                const float a = __builtin_amdgcn_exp2f(weight[s][tid] - rr);
+                weight[s][tid] = a;
                 ll += a * sums[s * nc + tid];
             }
-            lds_l[tid] = ll;
+            sums[tid] = ll;  // (split 0's, read already)
         }
         __syncthreads();
         for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
@@ -440,15 +456,11 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
                 for (int k = 0; k < 4; ++k)
                     w[k] = s0 + k < splits ? part_get<f32x4>(row_of(s0 + k, col) + d / 2) : (f32x4){0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v += (s0 + k < splits ? lds_w[s0 + k][col] : 0.0f) * w[k];
+                for (int k = 0; k < 4; ++k) v += (s0 + k < splits ? weight[s0 + k][col] : 0.0f) * w[k];
             }
-            const float ll = lds_l[col];
-            put_row(16 * n + col, d, ll > 0.0f || ll != ll ? v / ll : (f32x4){0, 0, 0, 0});
-            for (int s = 0; s < splits; ++s) {
-                part_put(row_of(s, col) + d / 2, (f32x4){0, 0, 0, 0});
-            }
+            put_row(16 * n + col, d, quotient(v, sums[col]));
+            for (int s = 0; s < splits; ++s) part_put(row_of(s, col) + d / 2, (f32x4){0, 0, 0, 0});
         }
-        __syncthreads();
         for (int i = tid; i < splits * nc; i += 64 * kAttnWaves)
             part_put(row_of(i / nc, i % nc) + D / 2, (f32x4){0, 0, 0, 0});
     }
@@ -457,7 +469,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void kv4_attention_kernel(Kv4AttnA
 template <int DT, int D, int NT>
 static hipError_t launch_attn(const Kv4AttnArgs &g, hipStream_t st) {
     hipLaunchKernelGGL((kv4_attention_kernel<DT, D, NT>),
-                       dim3((unsigned)((int64_t)g.B * g.splits * g.Hkv * g.col_tiles)), dim3(64 * kAttnWaves), 0, st, g);
+                       dim3((unsigned)((int64_t)g.B * g.Hkv * g.col_tiles), (unsigned)g.splits), dim3(64 * kAttnWaves),
+                       0, st, g);
     return hipGetLastError();
 }
 
