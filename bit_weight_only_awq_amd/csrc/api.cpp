@@ -604,14 +604,14 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
                         const DeviceProps &d) {
     Kv4Plan p{};
     const int64_t rows = max_q * (Hq / Hkv);
-    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.col_tiles = cdiv(rows, 16 * p.nt);
-    p.part_cols = (int)std::min<int64_t>(rows, 16 * p.nt);
+    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+    const int64_t tile_rows = p.nt ? 16 * p.nt : 128, step = p.nt ? 32 : 64;
+    p.col_tiles = cdiv(rows, tile_rows);
+    p.part_cols = (int)std::min<int64_t>(rows, tile_rows);
     p.min_steps = 4;
     p.tiles = B * Hkv * p.col_tiles;
-    const int64_t most = cdiv(cdiv(max_kv, 32), p.min_steps);
-    p.splits = (int)std::max<int64_t>(
-        1, std::min<int64_t>({cdiv(4 * (int64_t)d.cus, p.tiles), most, (int64_t)kKv4MaxSplits}));
+    const int64_t most = cdiv(cdiv(max_kv, step), p.min_steps), fill = (p.nt ? 4 : 2) * (int64_t)d.cus;
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(fill, p.tiles), most, (int64_t)kKv4MaxSplits}));
     if (p.splits > 1)
         p.workspace_bytes =
             (size_t)(split_counters_bytes(p.tiles) + p.tiles * p.splits * p.part_cols * (D + 4) * 4);
@@ -1001,7 +1001,8 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
         g.counters = static_cast<uint32_t *>(workspace);
         g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + split_counters_bytes(p.tiles));
     }
-    return hip_status(launch_kv4_attention(g, static_cast<hipStream_t>(stream)));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return hip_status(p.nt ? launch_kv4_attention(g, st) : launch_kv4_prefill(g, st));
 }
 
 }  // extern "C"
