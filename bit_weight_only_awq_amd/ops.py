@@ -24,6 +24,12 @@ def _stream(dev: torch.device):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+# The raw handle of a device's current stream: the call behind
+# torch.cuda.current_stream(dev).cuda_stream without building the Stream object
+# (0.1 us against 1.8; a small kernel takes 3).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None:
@@ -61,6 +67,13 @@ class Workspace:
                     buf = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", idx))
                 self._bufs[key] = buf
             return buf
+
+    def of_stream(self, index: int, stream: int, nbytes: int):
+        """(pointer, bytes) of the workspace of `stream`, the current stream of device `index`, at least nbytes."""
+        buf = self._bufs.get((index, stream))
+        if buf is None or buf.numel() < nbytes:
+            buf = self.get(torch.device("cuda", index), nbytes)
+        return buf.data_ptr(), buf.numel()
 
 
 WORKSPACE = Workspace()
@@ -311,40 +324,58 @@ def linear_w4a8_fp8(x, b, s2, want_acc: bool = False, out=None, a=None, s1=None,
 
 # ----------------------------------------------------------------------------- RMS norm
 
-def _norm_args(x, weight, residual, residual_out, *outs):
-    _need_cuda(x, weight, residual, residual_out, *outs)
-    if x.dtype not in _F16 or x.dim() != 2:
-        raise ValueError("x must be fp16 or bf16, [rows, columns]")
-    if weight.dtype != x.dtype or weight.shape != x.shape[1:]:
-        raise ValueError("weight must have x's type and one value per column")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-        return None
-    if residual_out is None:
-        residual_out = torch.empty_like(x)
-    for t in (residual, residual_out):
-        if t.dtype != x.dtype or t.shape != x.shape:
-            raise ValueError("the residual must have x's type and shape")
+def _tensor(t, shape, dtype, index, what):
+    """Refuse a tensor that is not contiguous, of this shape and type, on device `index`."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be {tuple(shape)}, {dtype}, contiguous, on CUDA (HIP) device {index}")
+
+
+def _rmsnorm(fn, x, weight, eps, residual, residual_out, y, codes):
+    """Checks and call of the norm entry points; codes: their code, scale and sum tensors."""
+    if not x.is_cuda:
+        raise ValueError("all tensors must be on a CUDA (HIP) device")
+    dt, dev, shape = x.dtype, x.get_device(), x.shape
+    if dt not in _F16 or len(shape) != 2 or not x.is_contiguous():
+        raise ValueError("x must be contiguous fp16 or bf16, [rows, columns]")
+    _tensor(weight, shape[1:], dt, dev, "weight")
+    if residual is not None:
+        _tensor(residual, shape, dt, dev, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        elif residual_out is not residual:
+            _tensor(residual_out, shape, dt, dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if y is not None and y is not x:
+        _tensor(y, shape, dt, dev, "y")
+    status = getattr(L.lib(), fn)(
+        x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(),
+        None if residual is None else residual_out.data_ptr(), None if y is None else y.data_ptr(),
+        *[None if c is None else c.data_ptr() for c in codes], shape[0], shape[1], eps, _F16[dt], _raw_stream(dev))
+    if status:
+        L.check(fn, status)
     return residual_out
 
 
-def _same(t, shape, dtype, what):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-        raise ValueError(f"{what} must be {tuple(shape)}, {dtype}")
+def _codes(x, given, fp8: bool):
+    """The code, scale (and sum) tensors of x's rows: those given, checked, or new ones."""
+    shape, dtype, out = x.shape, torch.uint8 if fp8 else torch.int8, []
+    for t in given:
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=x.device)
+        else:
+            _tensor(t, shape, dtype, x.get_device(), "codes, scales and sums")
+        out.append(t)
+        shape, dtype = shape[:1], torch.float32
+    return out
 
 
 def rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None):
     """y = norm(x + residual) * weight in x's type, for the W4A16 layers.
     Returns y, or (y, x + residual) with a residual (residual_out may be the
     residual itself, out may be x)."""
-    _same(out, x.shape, x.dtype, "out")
-    residual_out = _norm_args(x, weight, residual, residual_out, out)
     out = torch.empty_like(x) if out is None else out
-    M, K = x.shape
-    L.check("w4a8_rmsnorm_quant", L.lib().w4a8_rmsnorm_quant(
-        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(out), None, None, M, K, eps, _F16[x.dtype],
-        _stream(x.device)))
+    residual_out = _rmsnorm("w4a8_rmsnorm_quant", x, weight, eps, residual, residual_out, out, (None, None))
     return out if residual is None else (out, residual_out)
 
 
@@ -352,16 +383,8 @@ def rmsnorm_quant(x, weight, eps: float = 1e-6, residual=None, residual_out=None
     """norm(x + residual) * weight as int8 codes with one scale per token, the
     input of w4a8_gemm: (a8, s1, x + residual or None).  The norm itself is
     written to y where given."""
-    M, K = x.shape
-    _same(y, x.shape, x.dtype, "y")
-    _same(a8, (M, K), torch.int8, "a8")
-    _same(s1, (M,), torch.float32, "s1")
-    residual_out = _norm_args(x, weight, residual, residual_out, y, a8, s1)
-    a8 = torch.empty(M, K, dtype=torch.int8, device=x.device) if a8 is None else a8
-    s1 = torch.empty(M, dtype=torch.float32, device=x.device) if s1 is None else s1
-    L.check("w4a8_rmsnorm_quant", L.lib().w4a8_rmsnorm_quant(
-        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(a8), _ptr(s1), M, K, eps,
-        _F16[x.dtype], _stream(x.device)))
+    a8, s1 = _codes(x, (a8, s1), False)
+    residual_out = _rmsnorm("w4a8_rmsnorm_quant", x, weight, eps, residual, residual_out, y, (a8, s1))
     return a8, s1, residual_out
 
 
@@ -369,18 +392,8 @@ def rmsnorm_quant_fp8(x, weight, eps: float = 1e-6, residual=None, residual_out=
                       asum=None):
     """The same as E4M3 codes, the input of w4a8_fp8_gemm: (codes uint8, s1,
     asum, x + residual or None)."""
-    M, K = x.shape
-    _same(y, x.shape, x.dtype, "y")
-    _same(a, (M, K), torch.uint8, "a")
-    _same(s1, (M,), torch.float32, "s1")
-    _same(asum, (M,), torch.float32, "asum")
-    residual_out = _norm_args(x, weight, residual, residual_out, y, a, s1, asum)
-    a = torch.empty(M, K, dtype=torch.uint8, device=x.device) if a is None else a
-    s1 = torch.empty(M, dtype=torch.float32, device=x.device) if s1 is None else s1
-    asum = torch.empty(M, dtype=torch.float32, device=x.device) if asum is None else asum
-    L.check("w4a8_fp8_rmsnorm_quant", L.lib().w4a8_fp8_rmsnorm_quant(
-        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(a), _ptr(s1), _ptr(asum), M, K, eps,
-        _F16[x.dtype], _stream(x.device)))
+    a, s1, asum = _codes(x, (a, s1, asum), True)
+    residual_out = _rmsnorm("w4a8_fp8_rmsnorm_quant", x, weight, eps, residual, residual_out, y, (a, s1, asum))
     return a, s1, asum, residual_out
 
 
@@ -413,11 +426,15 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scale: float = 1
     return torch.cat((ang.cos(), ang.sin()), 1).float().to("cuda" if device is None else device)
 
 
-def _heads(t, name):
-    """(stride of a token in elements) of [T, H, D] with dense heads."""
-    if t.dim() != 3 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense heads")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+def _heads(t, shape, dtype, index, what):
+    """Elements from one token to the next of [T, H, D] with dense heads."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{what} must be {tuple(shape)}, {dtype}, on CUDA (HIP) device {index}")
+    T, H, D = shape
+    step, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError(f"{what} must have dense heads")
+    return step if T > 1 else max(step, H * D)
 
 
 def kv4_append(q, k, v, rope, positions, slots, cache, interleaved: bool = False, out=None):
@@ -425,35 +442,41 @@ def kv4_append(q, k, v, rope, positions, slots, cache, interleaved: bool = False
     no rotation), k and v quantised to 4 bits into the cache's slots; returns
     the rotated q (None for q = None).  q, k and v may be views of one fused
     QKV tensor."""
-    for t in (q, k, v, rope, positions, slots, cache):
-        if t is not None and not t.is_cuda:
-            raise ValueError("all tensors must be on a CUDA (HIP) device")
-    _need_cuda(rope, positions, slots, cache, out)
-    T, hkv, D = k.shape
-    if k.dtype not in _F16 or v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("k and v must be fp16 or bf16, of one type and shape")
-    if q is not None and (q.dtype != k.dtype or q.shape[0] != T or q.shape[2] != D):
-        raise ValueError("q must have k's type, tokens and head dimension")
+    if not k.is_cuda:
+        raise ValueError("all tensors must be on a CUDA (HIP) device")
+    dt, dev, shape = k.dtype, k.get_device(), k.shape
+    if dt not in _F16 or len(shape) != 3:
+        raise ValueError("k must be fp16 or bf16 [tokens, heads, head_dim]")
+    T, hkv, D = shape
+    k_step, v_step = _heads(k, shape, dt, dev, "k"), _heads(v, shape, dt, dev, "v")
+    hq = q_step = rot = max_pos = 0
+    q_ptr = out_ptr = rope_ptr = pos_ptr = None
+    if q is not None:
+        hq = q.shape[1]
+        q_shape = torch.Size((T, hq, D))
+        q_step = _heads(q, q_shape, dt, dev, "q")
+        if out is None:
+            out = torch.empty(q_shape, dtype=dt, device=k.device)
+        else:
+            _tensor(out, q_shape, dt, dev, "out")
+        q_ptr, out_ptr = q.data_ptr(), out.data_ptr()
+    if rope is not None:
+        _tensor(rope, rope.shape, torch.float32, dev, "rope")
+        if positions is None or rope.dim() != 2:
+            raise ValueError("rope must be [max_pos, rot] and come with positions")
+        _tensor(positions, shape[:1], torch.int32, dev, "positions")
+        max_pos, rot = rope.shape
+        rope_ptr, pos_ptr = rope.data_ptr(), positions.data_ptr()
+    _tensor(slots, shape[:1], torch.int64, dev, "slots")
+    _tensor(cache, cache.shape, torch.int32, dev, "cache")
+    page = _kv4_page_size(cache, D)
     if cache.shape[1] != hkv:
         raise ValueError("the cache has another number of key/value heads")
-    _same(slots, (T,), torch.int64, "slots")
-    rot = max_pos = 0
-    if rope is not None:
-        if rope.dim() != 2 or rope.dtype != torch.float32:
-            raise ValueError("rope must be fp32 [max_pos, rot]")
-        max_pos, rot = rope.shape
-        if positions is None:
-            raise ValueError("rope without positions")
-        _same(positions, (T,), torch.int32, "positions")
-    hq = 0 if q is None else q.shape[1]
-    if q is not None:
-        _same(out, q.shape, q.dtype, "out")
-        out = torch.empty(T, hq, D, dtype=q.dtype, device=q.device) if out is None else out
-    page = _kv4_page_size(cache, D)
-    L.check("awq_kv4_append", L.lib().awq_kv4_append(
-        _ptr(q), _ptr(k), _ptr(v), 0 if q is None else _heads(q, "q"), _heads(k, "k"), _heads(v, "v"), _ptr(rope),
-        _ptr(positions) if rope is not None else None, _ptr(slots), _ptr(out), _ptr(cache), T, hq, hkv, D, page,
-        cache.shape[0], rot, max_pos, int(interleaved), _F16[k.dtype], _stream(k.device)))
+    status = L.lib().awq_kv4_append(q_ptr, k.data_ptr(), v.data_ptr(), q_step, k_step, v_step, rope_ptr, pos_ptr,
+                                    slots.data_ptr(), out_ptr, cache.data_ptr(), T, hq, hkv, D, page, cache.shape[0],
+                                    rot, max_pos, int(interleaved), _F16[dt], _raw_stream(dev))
+    if status:
+        L.check("awq_kv4_append", status)
     return out
 
 
@@ -464,28 +487,41 @@ def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None,
     ones); cu_q int32 [B + 1] and max_q where sequences have more than one new
     token; max_kv: the longest sequence (default: what the tables can hold);
     scale: default 1 / sqrt(D)."""
-    _need_cuda(q, cache, tables, lens, cu_q, out)
-    if q.dtype not in _F16 or q.dim() != 3:
-        raise ValueError("q must be fp16 or bf16 [tokens, heads, head_dim]")
-    total, hq, D = q.shape
+    if not q.is_cuda:
+        raise ValueError("all tensors must be on a CUDA (HIP) device")
+    dt, dev, shape = q.dtype, q.get_device(), q.shape
+    if dt not in _F16 or len(shape) != 3 or not q.is_contiguous():
+        raise ValueError("q must be contiguous fp16 or bf16 [tokens, heads, head_dim]")
+    total, hq, D = shape
     B = lens.shape[0]
-    if tables.dim() != 2 or tables.shape[0] != B or tables.dtype != torch.int32:
-        raise ValueError("tables must be int32 [sequences, pages]")
-    _same(lens, (B,), torch.int32, "lens")
-    _same(cu_q, (B + 1,), torch.int32, "cu_q")
-    _same(out, q.shape, q.dtype, "out")
+    _tensor(lens, lens.shape[:1], torch.int32, dev, "lens")
+    _tensor(tables, torch.Size((B, tables.shape[-1])), torch.int32, dev, "tables")
+    if cu_q is not None:
+        _tensor(cu_q, torch.Size((B + 1,)), torch.int32, dev, "cu_q")
+    _tensor(cache, cache.shape, torch.int32, dev, "cache")
     page = _kv4_page_size(cache, D)
-    hkv = cache.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    elif out is not q:
+        _tensor(out, shape, dt, dev, "out")
+    pages, hkv, _ = cache.shape
+    width = tables.shape[1]
     if max_kv is None:
-        max_kv = tables.shape[1] * page
-    out = torch.empty_like(q) if out is None else out
-    with torch.cuda.device(q.device):
-        need = int(L.lib().awq_kv4_attention_workspace_bytes(B, max_q, hq, hkv, D, max_kv))
-    ws = WORKSPACE.get(q.device, need)
-    L.check("awq_kv4_attention", L.lib().awq_kv4_attention(
-        _ptr(q), _ptr(cache), _ptr(tables), _ptr(lens), _ptr(cu_q), _ptr(out), B, total, max_q, max_kv, hq, hkv, D,
-        page, cache.shape[0], tables.shape[1], D ** -0.5 if scale is None else scale, window, _F16[q.dtype], _ptr(ws),
-        0 if ws is None else ws.numel(), _stream(q.device)))
+        max_kv = width * page
+    lib = L.lib()
+    if torch._C._cuda_getDevice() == dev:
+        need = lib.awq_kv4_attention_workspace_bytes(B, max_q, hq, hkv, D, max_kv)
+    else:
+        with torch.cuda.device(dev):
+            need = lib.awq_kv4_attention_workspace_bytes(B, max_q, hq, hkv, D, max_kv)
+    stream = _raw_stream(dev)
+    ws, ws_bytes = WORKSPACE.of_stream(dev, stream, need) if need else (None, 0)
+    status = lib.awq_kv4_attention(q.data_ptr(), cache.data_ptr(), tables.data_ptr(), lens.data_ptr(),
+                                   None if cu_q is None else cu_q.data_ptr(), out.data_ptr(), B, total, max_q, max_kv,
+                                   hq, hkv, D, page, pages, width, D ** -0.5 if scale is None else scale, window,
+                                   _F16[dt], ws, ws_bytes, stream)
+    if status:
+        L.check("awq_kv4_attention", status)
     return out
 
 
