@@ -593,7 +593,7 @@ static int check_kv4(int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t num_
 }
 
 struct Kv4Plan {
-    int nt, splits, min_steps, part_cols;
+    int kind, splits, min_steps, part_cols;
     int64_t col_tiles, tiles;
     size_t workspace_bytes;
 };
@@ -604,13 +604,13 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
                         const DeviceProps &d) {
     Kv4Plan p{};
     const int64_t rows = max_q * (Hq / Hkv);
-    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
-    const int64_t tile_rows = p.nt ? 16 * p.nt : 128, step = p.nt ? 32 : 64;
-    p.col_tiles = cdiv(rows, tile_rows);
-    p.part_cols = (int)std::min<int64_t>(rows, tile_rows);
-    p.min_steps = 4;
+    p.kind = rows <= 4 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
+    const int64_t tile_rows[] = {4, 16, 32, 128}, step[] = {64, 32, 32, 64};
+    p.col_tiles = cdiv(rows, tile_rows[p.kind]);
+    p.part_cols = (int)std::min<int64_t>(rows, tile_rows[p.kind]);
+    p.min_steps = p.kind == 0 || p.kind == 3 ? 4 : 8;
     p.tiles = B * Hkv * p.col_tiles;
-    const int64_t most = cdiv(cdiv(max_kv, step), p.min_steps), fill = (p.nt ? 4 : 2) * (int64_t)d.cus;
+    const int64_t most = cdiv(cdiv(max_kv, step[p.kind]), p.min_steps), fill = 2 * (int64_t)d.cus;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(fill, p.tiles), most, (int64_t)kKv4MaxSplits}));
     if (p.splits > 1)
         p.workspace_bytes =
@@ -996,13 +996,15 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
     if (rc != AWQ_OK) return rc;
     Kv4AttnArgs g{q, cache, tables, lens, cu_q, out, num_pages, (int)B, (int)total_q, (int)max_q, (int)Hq, (int)Hkv,
                   (int)head_dim, (int)page_size, (int)table_stride, (int)std::min<int64_t>(window, kMaxTokens), dtype,
-                  scale, p.nt, (int)p.col_tiles, p.splits, p.min_steps, p.part_cols, nullptr, nullptr};
+                  scale, p.kind, (int)p.col_tiles, p.splits, p.min_steps, p.part_cols, nullptr, nullptr};
     if (p.workspace_bytes) {
         g.counters = static_cast<uint32_t *>(workspace);
         g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + split_counters_bytes(p.tiles));
     }
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return hip_status(p.nt ? launch_kv4_attention(g, st) : launch_kv4_prefill(g, st));
+    return hip_status(p.kind == 0   ? launch_kv4_decode(g, st)
+                      : p.kind == 3 ? launch_kv4_prefill(g, st)
+                                    : launch_kv4_attention(g, st));
 }
 
 }  // extern "C"

@@ -23,6 +23,15 @@
 
 namespace awq4 {
 
+// 8 or 16 bytes of a buffer: lane offset plus scalar offset.
+template <typename T>
+__device__ __forceinline__ T buf_get(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t scalar) {
+    if constexpr (sizeof(T) == 8)
+        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)scalar, 0));
+    else
+        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)scalar, 0));
+}
+
 template <int D>
 struct Kv4Layout {
     static constexpr int kWords = D / 8;  // packed words of one token and head

@@ -38,41 +38,9 @@
 // join their sums through LDS, and the workgroups of a sequence (as many as
 // its length asks for, known only on the device) join theirs through the
 // workspace: the last to arrive adds them in order, writes and clears.
-#include "kv4.hpp"
-#include "launch.hpp"
+#include "kv4_ops.hpp"
 
 namespace awq4 {
-
-constexpr int kAttnWaves = 4;
-
-// The larger of the values of the four lanes of a column (lanes l, l ^ 16, l ^
-// 32, l ^ 48), in each of them.
-__device__ __forceinline__ float column_max(float v) {
-    const uint32_t b = bit_as<uint32_t>(v);
-    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const float m = fmaxf(bit_as<float>((uint32_t)h[0]), bit_as<float>((uint32_t)h[1]));
-    const uint32_t c = bit_as<uint32_t>(m);
-    const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
-    return fmaxf(bit_as<float>((uint32_t)q[0]), bit_as<float>((uint32_t)q[1]));
-}
-__device__ __forceinline__ float column_sum(float v) {
-    const uint32_t b = bit_as<uint32_t>(v);
-    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const float m = bit_as<float>((uint32_t)h[0]) + bit_as<float>((uint32_t)h[1]);
-    const uint32_t c = bit_as<uint32_t>(m);
-    const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
-    return bit_as<float>((uint32_t)q[0]) + bit_as<float>((uint32_t)q[1]);
-}
-
-// The eight codes of a word as matrix-core operand (fp16 subnormals), columns
-// 0..7 in order; columns 2, 3, 6, 7 carry a factor 16.
-__device__ __forceinline__ u32x4 word_operand(uint32_t w) {
-    return (u32x4){w & 0x000F000Fu, w & 0x00F000F0u, (w >> 8) & 0x000F000Fu, (w >> 8) & 0x00F000F0u};
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    return bit_as<uint32_t>(__builtin_convertvector((f32x2){a, b}, f16x2));
-}
 
 // What one wave reads for 32 tokens: two tiles of 16.
 template <int D>
@@ -83,14 +51,11 @@ struct Kv4Step {
     u32x4 v[2], km[2], vm[2];
 };
 
-constexpr float kNoRef = -1e30f;      // the reference of a row that has seen nothing
-constexpr float kMaxP = 0x1p15f, kMaxSum = 0x1p100f;
-
 template <int DT, int D, int NT>
-__global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) void kv4_attention_kernel(Kv4AttnArgs g) {
+__global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attention_kernel(Kv4AttnArgs g) {
     using L = Kv4Layout<D>;
     using Step = Kv4Step<D>;
-    constexpr int COLS = 16 * NT, KW = D / 32, VM = D / 16, ROW = D + 4;
+    constexpr int COLS = 16 * NT, KW = D / 32, VM = D / 16, ROW = AttnRows<DT, D>::kRow;
     __shared__ float lds_o[kAttnWaves][16][ROW];  // one 16-column tile of every wave; at D its R, at D + 1 its sum of p
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -131,38 +96,43 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
     // (in the constant address space: no kernel of this call writes it, so it is
     // read through the scalar cache)
     const auto *table = (const __attribute__((address_space(4))) int32_t *)(g.tables + (size_t)b * g.table_stride);
-    const int64_t page_bytes = (int64_t)g.Hkv * L::head_words(g.P) * 4;
-    const char *head = (const char *)g.cache + (int64_t)h * L::head_words(g.P) * 4;
+    const uint32_t num_pages = (uint32_t)min(g.num_pages, (int64_t)0x7FFFFFFF);
+    const uint32_t page_bytes = (uint32_t)g.Hkv * L::head_words(g.P) * 4;
+    const uint32_t head_bytes = L::head_words(g.P) * 4;
+    const char *head = (const char *)g.cache + (size_t)h * head_bytes;
     // this lane's place in a tile of 16 tokens, in bytes after the tile's first word
     const uint32_t k_at = 4 * L::k_word(r16, KW * grp), m_at = 16 * grp;
     const uint32_t v_at = 4 * L::v_word(g.P, 4 * grp, D == 128 ? r16 : (r16 & 7));
     const uint32_t km_at = 4 * L::k_meta(g.P, 0) + m_at, vm_at = 4 * L::v_meta(g.P, 0) + m_at;
-    // the page that holds tokens t .. t + 15, or -1
-    auto page_of = [&](int t) -> int {
-        if (t >= kv_len) return -1;
-        const int p = __builtin_amdgcn_readfirstlane(table[t >> lgP]);
-        return p >= 0 && p < g.num_pages ? p : -1;
-    };
-    auto load = [&](Step &s, int p0, int p1, int t0) {
+    // the table's entries for the two tiles of a step (past the end: the last
+    // token's), and whether a tile's first token is there and has a page
+    const int last = max(kv_len - 1, 0) >> lgP;
+    auto entry = [&](int t) { return (uint32_t)table[min(t >> lgP, last)]; };
+    auto there = [&](uint32_t e, int t) { return e < num_pages && t < kv_len; };
+    auto load = [&](Step &s, uint32_t e0, uint32_t e1, int t0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = (t0 + 16 * i) & (g.P - 1);
-            const char *base = head + max(i ? p1 : p0, 0) * page_bytes;
-            const char *words = base + t * (4 * L::kWords), *metas = base + 4 * t;
-            s.k[i] = *(const typename Step::Words *)(words + k_at);
-            s.v[i] = *(const u32x4 *)(words + v_at);
-            s.km[i] = *(const u32x4 *)(metas + km_at);
-            s.vm[i] = *(const u32x4 *)(metas + vm_at);
+            const uint32_t e = i ? e1 : e0, t = (uint32_t)(t0 + 16 * i) & (uint32_t)(g.P - 1);
+            // (a buffer descriptor a tile: scalar base and offset plus a 32-bit
+            // lane offset, no 64-bit sums per lane)
+            const auto page = buf_rsrc(head + (uint64_t)(e < num_pages ? e : 0u) * page_bytes, head_bytes);
+            s.k[i] = buf_get<typename Step::Words>(page, k_at, t * (4 * L::kWords));
+            s.v[i] = buf_get<u32x4>(page, v_at, t * (4 * L::kWords));
+            s.km[i] = buf_get<u32x4>(page, km_at, 4 * t);
+            s.vm[i] = buf_get<u32x4>(page, vm_at, 4 * t);
         }
     };
 
     // the first step's loads before anything else
     Step cur, nxt;
-    int st = s_begin + wave, p0 = -1, p1 = -1;
+    int st = s_begin + wave;
+    uint32_t e0 = 0, e1 = 0, n0 = 0, n1 = 0;  // this step's entries, the next one's
     if (st < s_end) {
-        p0 = page_of(32 * st);
-        p1 = page_of(32 * st + 16);
-        load(cur, p0, p1, 32 * st);
+        e0 = entry(32 * st);
+        e1 = entry(32 * st + 16);
+        n0 = entry(32 * (st + kAttnWaves));
+        n1 = entry(32 * (st + kAttnWaves) + 16);
+        load(cur, e0, e1, 32 * st);
     }
 
     // this lane's columns: their rows of q as matrix-core operand, in fp16
@@ -190,8 +160,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
             }
         }
         mx = column_max(mx);
-        const int ex = (int)(bit_as<uint32_t>(mx) >> 23);
-        const int up = ex == 255 || ex == 0 ? 0 : min(127 + 14 - ex, 100);
+        const int up = query_shift(mx);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
@@ -200,9 +169,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
                 f[i][e] = __builtin_ldexpf(f[i][e], up);
                 sum += f[i][e];
             }
-            // columns 2, 3, 6, 7 meet codes times 16
-            qf[n][i] = (u32x4){pack_f16(f[i][0], f[i][1]), pack_f16(f[i][2] * 0.0625f, f[i][3] * 0.0625f),
-                               pack_f16(f[i][4], f[i][5]), pack_f16(f[i][6] * 0.0625f, f[i][7] * 0.0625f)};
+            qf[n][i] = query_operand(f[i]);
         }
         qz[n] = column_sum(sum) * 0x1p-24f;
         cf[n] = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
@@ -217,10 +184,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
 #pragma unroll
         for (int t = 0; t < VM; ++t) o[n][t] = (f32x4){0, 0, 0, 0};
     }
-    const uint32_t half_sel = (D == 128 || r16 < 8) ? 0x05040100u : 0x07060302u;
-
     // One step.  plain: every token of it is there and every column sees it.
-    auto compute = [&](Step &s, bool plain, int p0, int p1, int t0) {
+    auto compute = [&](Step &s, bool plain, bool in0, bool in1, int t0) {
         if (!plain) {
             // tokens that no column sees, or without a page: whatever their
             // meta words hold must not reach the sums
@@ -229,7 +194,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = t0 + 16 * i + 4 * grp + r;
-                    const bool any = (i ? p1 : p0) >= 0 && j >= kv_lo && j < kv_hi;
+                    const bool any = (i ? in1 : in0) && j >= kv_lo && j < kv_hi;
                     s.km[i][r] = any ? s.km[i][r] : 0u;
                     s.vm[i][r] = any ? s.vm[i][r] : 0u;
                 }
@@ -263,7 +228,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
         for (int n = 0; n < NT; ++n) {
             auto seen = [&](int i, int r) {
                 const int j = t0 + 16 * i + 4 * grp + r;
-                return (i ? p1 : p0) >= 0 && j >= lo[n] && j < hi[n];
+                return (i ? in1 : in0) && j >= lo[n] && j < hi[n];
             };
             float p[2][4], w[2][4], top, sum;
             auto numerators = [&] {
@@ -327,143 +292,63 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : NT == 2 ? 2 : 1) voi
             z1[i] = z | 0x80008000u;
             z16[i] = (z << 4) | 0x80008000u;
         }
-        // the values' codes: consecutive tokens side by side, one column a mask
-        uint32_t px[4], py[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w0 = s.v[i >> 1][2 * (i & 1)], w1 = s.v[i >> 1][2 * (i & 1) + 1];
-            px[i] = perm_b32(w1, w0, half_sel);
-            py[i] = D == 128 ? pair_y(w0, w1) : 0u;
-        }
+        const ValuePairs<D> pairs(s.v[0], s.v[1], r16);
 #pragma unroll
         for (int t = 0; t < VM; ++t) {
-            // D = 128: column t of the word; D = 64: position t of the lane's half
-            const int pos = D == 128 ? t >> 1 : t;
-            const uint32_t mask = pos & 1 ? 0x00F000F0u : 0x000F000Fu;
-            u32x4 a;
+            const u32x4 a = pairs.operand(t);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w = D == 128 && (t & 1) ? py[i] : px[i];
-                a[i] = (pos & 2 ? w >> 8 : w) & mask;
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) o[n][t] = mfma_f16(a, pf[n], mfma_f16(pos & 1 ? z16 : z1, pf[n], o[n][t]));
+            for (int n = 0; n < NT; ++n)
+                o[n][t] = mfma_f16(a, pf[n], mfma_f16(value_pos<D>(t) & 1 ? z16 : z1, pf[n], o[n][t]));
             if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    while (st < s_end) {
-        const int sn = st + kAttnWaves;
-        int n0 = -1, n1 = -1;
-        if (sn < s_end) {
-            n0 = page_of(32 * sn);
-            n1 = page_of(32 * sn + 16);
-            load(nxt, n0, n1, 32 * sn);
-        }
+    // Two steps in turn, each with registers of its own: the loads of one are
+    // in flight while the other is computed (a copy from one to the other would
+    // wait for them).
+    auto run = [&](Step &now, Step &next) {
         const int t0 = 32 * st;
-        compute(cur, p0 >= 0 && p1 >= 0 && t0 >= all_lo && t0 + 32 <= all_hi, p0, p1, t0);
-        cur = nxt;
-        st = sn;
-        p0 = n0;
-        p1 = n1;
+        const bool in0 = there(e0, t0), in1 = there(e1, t0 + 16);
+        const bool plain = in0 && in1 && t0 >= all_lo && t0 + 32 <= all_hi;
+        st += kAttnWaves;
+        e0 = n0;
+        e1 = n1;
+        if (st < s_end) {
+            load(next, e0, e1, 32 * st);
+            n0 = entry(32 * (st + kAttnWaves));
+            n1 = entry(32 * (st + kAttnWaves) + 16);
+        }
+        compute(now, plain, in0, in1, t0);
+    };
+    while (st < s_end) {
+        run(cur, nxt);
+        if (st >= s_end) break;
+        run(nxt, cur);
     }
 
     // Join the four waves, 16 columns at a time; then write, or exchange with
     // the sequence's other workgroups.
-    float *part = splits > 1 ? g.partials + (size_t)tile * g.splits * (g.part_cols * ROW) : nullptr;
-    auto put_row = [&](int col, int d, f32x4 v) {
-        const int row = c0 + col, qi = row / G, hg = row - qi * G;
-        *(uint2 *)((uint16_t *)g.out + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D + d) = quad_out_bits<DT>(v);
-    };
-    // (a sum of p that is not a number shows in the row)
-    auto quotient = [](f32x4 v, float sum) { return sum == 0.0f ? (f32x4){0, 0, 0, 0} : v / sum; };
+    const AttnRows<DT, D> out{g, tile, splits, split, c0, q0, h, G};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int nc = min(16, ncols - 16 * n);
         if (nc <= 0) break;
         if (n) __syncthreads();
         const float lsum = column_sum(l[n]);
+        float *mine = &lds_o[wave][r16][0];
 #pragma unroll
         for (int t = 0; t < VM; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 4 * grp + r;
-                const int d = D == 128 ? 8 * i + t : 8 * (i & 7) + 2 * t + (i >> 3);
-                lds_o[wave][r16][d] = o[n][t][r] * ((D == 128 ? t >> 1 : t) & 1 ? 0x1p20f : 0x1p24f);
-            }
+            for (int r = 0; r < 4; ++r) mine[value_dim<D>(t, 4 * grp + r)] = o[n][t][r] * value_unit<D>(t);
         if (grp == 0) {
-            lds_o[wave][r16][D] = ref[n];
-            lds_o[wave][r16][D + 1] = lsum;
+            mine[D] = ref[n];
+            mine[D + 1] = lsum;
         }
         __syncthreads();
-        for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
-            const int col = i / (D / 4), d = 4 * (i % (D / 4));
-            float rw[kAttnWaves], rr = kNoRef, ll = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w) rr = fmaxf(rr, rw[w] = lds_o[w][col][D]);
-            f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w) {
-                const float a = __builtin_amdgcn_exp2f(rw[w] - rr);
-                v += a * *(const f32x4 *)&lds_o[w][col][d];
-                ll += a * lds_o[w][col][D + 1];
-            }
-            if (splits == 1) {
-                put_row(16 * n + col, d, quotient(v, ll));
-            } else {
-                float *p = part + ((size_t)split * g.part_cols + 16 * n + col) * ROW;
-                part_put((uint64_t *)(p + d), v);
-                if (d == 0) part_put((uint64_t *)(p + D), (f32x4){rr, ll, 0, 0});
-            }
-        }
+        out.template join<kAttnWaves>(&lds_o[0][0][0], [](int w, int col) { return 16 * w + col; }, 16 * n, nc);
     }
-    if (splits == 1) return;
-    if (!split_tile_last_atomic(g.counters + tile, splits)) return;
-#pragma unroll 1
-    for (int n = 0; n < NT; ++n) {
-        const int nc = min(16, ncols - 16 * n);
-        if (nc <= 0) break;
-        auto row_of = [&](int s, int col) {
-            return (uint64_t *)(part + ((size_t)s * g.part_cols + 16 * n + col) * ROW);
-        };
-        __syncthreads();
-        // the splits' sums, and their references and then weights
-        static_assert(2 * 16 * kKv4MaxSplits <= kAttnWaves * 16 * 68, "LDS of the joining");
-        float *sums = &lds_o[0][0][0], (*weight)[16] = (float(*)[16])(sums + 16 * kKv4MaxSplits);
-        for (int i = tid; i < splits * nc; i += 64 * kAttnWaves) {
-            const f32x4 rl = part_get<f32x4>(row_of(i / nc, i % nc) + D / 2);
-            weight[i / nc][i % nc] = rl[0];
-            sums[i] = rl[1];
-        }
-        __syncthreads();
-        if (tid < nc) {
-            float rr = kNoRef, ll = 0.0f;
-            for (int s = 0; s < splits; ++s) rr = fmaxf(rr, weight[s][tid]);
-            for (int s = 0; s < splits; ++s) {
-                const float a = __builtin_amdgcn_exp2f(weight[s][tid] - rr);
-                weight[s][tid] = a;
-                ll += a * sums[s * nc + tid];
-            }
-            sums[tid] = ll;  // (split 0's, read already)
-        }
-        __syncthreads();
-        for (int i = tid; i < nc * (D / 4); i += 64 * kAttnWaves) {
-            const int col = i / (D / 4), d = 4 * (i % (D / 4));
-            f32x4 v = {0, 0, 0, 0};
-            for (int s0 = 0; s0 < splits; s0 += 4) {
-                f32x4 w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = s0 + k < splits ? part_get<f32x4>(row_of(s0 + k, col) + d / 2) : (f32x4){0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v += (s0 + k < splits ? weight[s0 + k][col] : 0.0f) * w[k];
-            }
-            put_row(16 * n + col, d, quotient(v, sums[col]));
-            for (int s = 0; s < splits; ++s) part_put(row_of(s, col) + d / 2, (f32x4){0, 0, 0, 0});
-        }
-        for (int i = tid; i < splits * nc; i += 64 * kAttnWaves)
-            part_put(row_of(i / nc, i % nc) + D / 2, (f32x4){0, 0, 0, 0});
-    }
+    if (splits > 1 && split_tile_last_atomic(g.counters + tile, splits))
+        out.exchange(&lds_o[0][0][0], ncols);
 }
 
 template <int DT, int D, int NT>
@@ -476,11 +361,7 @@ static hipError_t launch_attn(const Kv4AttnArgs &g, hipStream_t st) {
 
 template <int DT, int D>
 static hipError_t launch_attn_nt(const Kv4AttnArgs &g, hipStream_t st) {
-    switch (g.nt) {
-        case 1: return launch_attn<DT, D, 1>(g, st);
-        case 2: return launch_attn<DT, D, 2>(g, st);
-        default: return launch_attn<DT, D, 4>(g, st);
-    }
+    return g.kind == 1 ? launch_attn<DT, D, 1>(g, st) : launch_attn<DT, D, 2>(g, st);
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs &g, hipStream_t st) {

@@ -1,0 +1,340 @@
+// kv4_decode.hip -- attention over the paged 4-bit cache for at most four query
+// rows per key/value head: the answer's next token with groups of up to four
+// heads.  Mathematics, masks, splits and reference R as in kv4_attention.hip.
+//
+// Sixteen columns of a 16 x 16 tile would be twelve or more empty ones, and
+// with them most of the exponentials and the arithmetic beside the matrix
+// cores, which then bound the kernel (4.3 of the 5.9 TB/s that reading reaches
+// here, whatever the number of waves).  So the columns hold four runs of 16
+// tokens for four rows: column 4 s + j is row j against the tokens of run s.
+// A product's sum over k runs over the four lane groups; the key operand gives
+// group g the tokens of run g (eight of their dimensions a product, sixteen
+// products for D = 128, as many as before), and the query operand is zero in
+// column (s, j) for every group but g = s: each column sums over its own run.
+// 64 tokens x 4 rows make one score register quad instead of four.
+//
+// Loads stay whole lines (a lane reads a quarter of the words of one token in
+// each run); a 4 x 4 transpose between lane groups and runs (sixteen lane
+// swaps for 64 tokens) puts the tokens of run g into group g.  The scales lie
+// where the scores do; the values' zero points move from there to their
+// operand by a broadcast along the 16 lanes of a group.  The second product
+// takes 32 tokens at a time, two runs, with the probabilities of the other
+// columns cleared; its columns stay apart by run until the end, where the
+// sixteen partial rows (four waves, four runs) of each row are joined.
+#include "kv4_ops.hpp"
+
+namespace awq4 {
+
+// What one wave reads for 64 tokens.
+template <int D>
+struct Kv4Quad {
+    static constexpr int KW = D / 32;
+    typedef uint32_t Words __attribute__((ext_vector_type(KW)));
+    Words k[4];    // run i: token 16 i + lane % 16, words KW (lane / 16) ..
+    u32x4 v[4];    // run i: tokens 4 (lane / 16) .., one word column
+    u32x4 km, vm;  // run (lane % 16) / 4: tokens 4 (lane / 16) ..
+};
+
+// Registers a and b between the halves (32 lanes) or odd and even rows (16
+// lanes) of the wave: a keeps its lower (even) part and takes b's there, b
+// takes a's upper (odd) part.
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = (uint32_t)r[0];
+    b = (uint32_t)r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = (uint32_t)r[0];
+    b = (uint32_t)r[1];
+}
+// Lane 4 N of each row of 16 lanes, in all of them.
+template <int N>
+__device__ __forceinline__ uint32_t row_broadcast(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + 4 * N, 0xF, 0xF, false);
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnArgs g) {
+    using L = Kv4Layout<D>;
+    using Quad = Kv4Quad<D>;
+    constexpr int KW = D / 32, VM = D / 16, ROW = AttnRows<DT, D>::kRow;
+    __shared__ float lds_o[kAttnWaves][16][ROW];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, grp = lane >> 4, run = r16 >> 2, j = r16 & 3;
+    // workgroup -> (sequence, head), split
+    const int tile = blockIdx.x, split = blockIdx.y;
+    const int h = tile % g.Hkv, b = tile / g.Hkv;
+    const int G = g.Hq / g.Hkv;
+
+    int q0 = b, q1 = b + 1;
+    if (g.cu_q) {
+        q0 = min(max(g.cu_q[b], 0), g.total_q);
+        q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
+    }
+    const int nq = q1 - q0;
+    const int kv_len = min(max(g.lens[b], 0), g.table_stride * g.P);
+    const int ncols = min(nq, g.max_q) * G;  // 1 .. 4
+    if (ncols == 0) return;
+
+    // tokens that any row sees: [kv_lo, kv_hi), and that all of them see
+    const int base_pos = kv_len - nq, last_pos = base_pos + (ncols - 1) / G;
+    const int kv_hi = max(last_pos + 1, 0);
+    const int kv_lo = g.window > 0 ? min(max(base_pos - g.window + 1, 0), kv_hi) : 0;
+    const int all_hi = base_pos + 1, all_lo = g.window > 0 ? max(last_pos - g.window + 1, 0) : 0;
+    const int step0 = kv_lo >> 6, steps = kv_hi > kv_lo ? ((kv_hi + 63) >> 6) - step0 : 0;
+    const int splits = max(1, min(g.splits, (steps + g.min_steps - 1) / g.min_steps));
+    if (split >= splits) return;
+    const int per = (steps + splits - 1) / splits;
+    const int s_begin = step0 + split * per, s_end = min(step0 + steps, s_begin + per);
+
+    const int lgP = __builtin_ctz(g.P);
+    const auto *table = (const __attribute__((address_space(4))) int32_t *)(g.tables + (size_t)b * g.table_stride);
+    const uint32_t num_pages = (uint32_t)min(g.num_pages, (int64_t)0x7FFFFFFF);
+    const uint32_t head_bytes = L::head_words(g.P) * 4, page_bytes = (uint32_t)g.Hkv * head_bytes;
+    const char *head = (const char *)g.cache + (size_t)h * head_bytes;
+    // this lane's place in a run, in bytes after the run's first word
+    const uint32_t k_at = 4 * L::k_word(r16, KW * grp);
+    const uint32_t v_at = 4 * L::v_word(g.P, 4 * grp, D == 128 ? r16 : (r16 & 7));
+    const uint32_t km_at = 4 * L::k_meta(g.P, 4 * grp), vm_at = 4 * g.P;
+    const int last = max(kv_len - 1, 0) >> lgP;
+    // the table's entries of the four runs of a step
+    struct Entries {
+        uint32_t e[4];
+    };
+    auto entries = [&](int t0) {
+        Entries r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.e[i] = (uint32_t)table[min((t0 + 16 * i) >> lgP, last)];
+        return r;
+    };
+    auto load = [&](Quad &s, const Entries &e, int t0) {
+        uint32_t mine = 0;  // the page of this lane's scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p = e.e[i] < num_pages ? e.e[i] : 0u, t = (uint32_t)(t0 + 16 * i) & (uint32_t)(g.P - 1);
+            const auto page = buf_rsrc(head + (uint64_t)p * page_bytes, head_bytes);
+            s.k[i] = buf_get<typename Quad::Words>(page, k_at, t * (4 * L::kWords));
+            s.v[i] = buf_get<u32x4>(page, v_at, t * (4 * L::kWords));
+            mine = run == i ? p : mine;
+        }
+        const char *metas = head + (uint64_t)mine * page_bytes + (km_at + 4 * ((uint32_t)(t0 + 16 * run) & (g.P - 1)));
+        s.km = *(const u32x4 *)metas;
+        s.vm = *(const u32x4 *)(metas + vm_at);
+    };
+
+    Quad cur, nxt;
+    int st = s_begin + wave;
+    Entries now_e{}, next_e{};
+    if (st < s_end) {
+        now_e = entries(64 * st);
+        next_e = entries(64 * (st + kAttnWaves));
+        load(cur, now_e, 64 * st);
+    }
+
+    // the row of this lane's column, zero but in the lane group of its run
+    u32x4 qf[4 * KW];
+    float qz, cf;
+    int lo, hi;
+    {
+        const int row = j < ncols ? j : 0, qi = row / G, hg = row - qi * G;
+        const int pos = base_pos + qi;
+        hi = pos + 1;
+        lo = g.window > 0 ? pos - g.window + 1 : 0;
+        const uint16_t *src = (const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D;
+        // every lane reads its row's whole q (its four groups and runs the same): no exchange for the
+        // largest value and the sum
+        float mx = 0.0f, sum = 0.0f;
+        u32x4 w[4 * KW];
+#pragma unroll
+        for (int i = 0; i < 4 * KW; ++i) {
+            w[i] = *(const u32x4 *)(src + 8 * i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                mx = fmaxf(mx, fabsf(act_bits_to_f32<DT>((w[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
+        }
+        const int up = query_shift(mx);
+#pragma unroll
+        for (int i = 0; i < 4 * KW; ++i) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] = __builtin_ldexpf(act_bits_to_f32<DT>((w[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu), up);
+                sum += f[e];
+            }
+            const u32x4 op = query_operand(f);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) qf[i][p] = grp == run ? op[p] : 0u;
+        }
+        qz = sum * 0x1p-24f;
+        cf = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
+    }
+    uint32_t mine[4];  // all ones where this lane's column is of run i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i] = run == i ? 0xFFFFFFFFu : 0u;
+
+    f32x4 o[VM];
+    float ref = kNoRef, l = 0.0f;
+#pragma unroll
+    for (int t = 0; t < VM; ++t) o[t] = (f32x4){0, 0, 0, 0};
+
+    // One step.  there: bit i, run i starts before the end and has a page;
+    // plain: all four do, and every row sees every token.
+    auto compute = [&](Quad &s, uint32_t there, bool plain, int t0) {
+        const int at = t0 + 16 * run + 4 * grp;  // this lane's four tokens
+        if (!plain) {
+            // tokens that no row sees, or without a page: whatever their meta
+            // words hold must not reach the sums
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool any = ((there >> run) & 1) && at + r >= kv_lo && at + r < kv_hi;
+                s.km[r] = any ? s.km[r] : 0u;
+                s.vm[r] = any ? s.vm[r] : 0u;
+            }
+        }
+        // tokens of run g into lane group g: register i of a word from run i to quarter i
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            uint32_t a = s.k[0][w], b = s.k[1][w], c = s.k[2][w], d = s.k[3][w];
+            swap32(a, c);
+            swap32(b, d);
+            swap16(a, b);
+            swap16(c, d);
+            s.k[0][w] = a;
+            s.k[1][w] = b;
+            s.k[2][w] = c;
+            s.k[3][w] = d;
+        }
+        f32x4 x = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < KW; w += 2) {
+                x = mfma_f16(word_operand(s.k[i][w]), qf[KW * i + w], x);
+                x1 = mfma_f16(word_operand(s.k[i][w + 1]), qf[KW * i + w + 1], x1);
+            }
+        x += x1;
+        __builtin_amdgcn_sched_barrier(0);
+        float vs[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float ks = act_bits_to_f32<DT>(s.km[r] & 0xFFFFu);
+            const float kz = (float)((s.km[r] >> 16) & 0xFFu);
+            vs[r] = act_bits_to_f32<DT>(s.vm[r] & 0xFFFFu);
+            x[r] = __builtin_fmaf(-kz, qz, x[r]) * ks;
+        }
+        auto seen = [&](int r) { return ((there >> run) & 1) && at + r >= lo && at + r < hi; };
+        float p[4], w[4], top, sum;
+        auto numerators = [&] {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], cf, -ref));
+                w[r] = p[r] * vs[r];
+            }
+            if (!plain) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool on = seen(r);
+                    p[r] = on ? p[r] : 0.0f;
+                    w[r] = on ? w[r] : 0.0f;
+                }
+            }
+            sum = (p[0] + p[1]) + (p[2] + p[3]);
+            top = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+        };
+        numerators();
+        if (__builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0) {
+            float t = ref;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float y = x[r] * cf;
+                const float c = fmaxf(y + __builtin_amdgcn_logf(vs[r]) - 11.0f, y - 90.0f);
+                t = plain || seen(r) ? fmaxf(t, c) : t;
+            }
+            t = column_max(t);
+            const float f = __builtin_amdgcn_exp2f(ref - t);
+            ref = t;
+            l *= f;
+#pragma unroll
+            for (int u = 0; u < VM; ++u) o[u] *= f;
+            numerators();
+        }
+        l += sum;
+        const uint32_t p01 = pack_f16(w[0], w[1]), p23 = pack_f16(w[2], w[3]);
+        const uint32_t z01 = perm_b32(s.vm[1], s.vm[0], 0x07060302u), z23 = perm_b32(s.vm[3], s.vm[2], 0x07060302u);
+        __builtin_amdgcn_sched_barrier(0);
+        // runs 0 and 1, then 2 and 3
+        static_for<2>([&](auto pair) {
+            constexpr int P = 2 * decltype(pair)::value;
+            const u32x4 bop = {p01 & mine[P], p23 & mine[P], p01 & mine[P + 1], p23 & mine[P + 1]};
+            // the zero points as an operand with equal rows, negative, for
+            // operands without and with the factor 16
+            const u32x4 z = {row_broadcast<P>(z01), row_broadcast<P>(z23), row_broadcast<P + 1>(z01),
+                             row_broadcast<P + 1>(z23)};
+            u32x4 z1, z16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                z1[i] = z[i] | 0x80008000u;
+                z16[i] = (z[i] << 4) | 0x80008000u;
+            }
+            const ValuePairs<D> pairs(s.v[P], s.v[P + 1], r16);
+#pragma unroll
+            for (int t = 0; t < VM; ++t) {
+                o[t] = mfma_f16(pairs.operand(t), bop, mfma_f16(value_pos<D>(t) & 1 ? z16 : z1, bop, o[t]));
+                if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        });
+    };
+
+    auto step = [&](Quad &now, Quad &next) {
+        const int t0 = 64 * st;
+        uint32_t there = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) there |= (uint32_t)(now_e.e[i] < num_pages && t0 + 16 * i < kv_len) << i;
+        const bool plain = there == 15 && t0 >= all_lo && t0 + 64 <= all_hi;
+        st += kAttnWaves;
+        now_e = next_e;
+        if (st < s_end) {
+            load(next, now_e, 64 * st);
+            next_e = entries(64 * (st + kAttnWaves));
+        }
+        compute(now, there, plain, t0);
+    };
+    while (st < s_end) {
+        step(cur, nxt);
+        if (st >= s_end) break;
+        step(nxt, cur);
+    }
+
+    const AttnRows<DT, D> out{g, tile, splits, split, 0, q0, h, G};
+    const float lsum = column_sum(l);
+    float *part = &lds_o[wave][r16][0];
+#pragma unroll
+    for (int t = 0; t < VM; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[value_dim<D>(t, 4 * grp + r)] = o[t][r] * value_unit<D>(t);
+    if (grp == 0) {
+        part[D] = ref;
+        part[D + 1] = lsum;
+    }
+    __syncthreads();
+    // (partial 4 w + s of row j: wave w, column 4 s + j)
+    out.template join<4 * kAttnWaves>(&lds_o[0][0][0], [](int p, int col) { return 4 * p + col; }, 0, ncols);
+    if (splits > 1 && split_tile_last_atomic(g.counters + tile, splits)) out.exchange(&lds_o[0][0][0], ncols);
+}
+
+template <int DT, int D>
+static hipError_t launch_decode(const Kv4AttnArgs &g, hipStream_t st) {
+    hipLaunchKernelGGL((kv4_decode_kernel<DT, D>), dim3((unsigned)((int64_t)g.B * g.Hkv), (unsigned)g.splits),
+                       dim3(64 * kAttnWaves), 0, st, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_decode(const Kv4AttnArgs &g, hipStream_t st) {
+    if (g.D == 128)
+        return g.dtype == DT_BF16 ? launch_decode<DT_BF16, 128>(g, st) : launch_decode<DT_F16, 128>(g, st);
+    return g.dtype == DT_BF16 ? launch_decode<DT_BF16, 64>(g, st) : launch_decode<DT_F16, 64>(g, st);
+}
+
+}  // namespace awq4

@@ -195,15 +195,16 @@ struct Kv4AttnArgs {
     int B, total_q, max_q, Hq, Hkv, D, P, table_stride, window, dtype;
     float scale;
     // the plan
-    int nt;         // 16-column tiles of query rows per workgroup (1, 2, 4); 0: the prefill kernel (128 rows)
+    int kind;       // kernel: 0 at most four rows, 1 and 2 tiles of 16 and 32 rows, 3 the prefill kernel (128 rows)
     int col_tiles;  // workgroups along the query rows of a sequence and key/value head
     int splits;     // most workgroups along a sequence's tokens
-    int min_steps;  // steps (32 tokens; prefill: tiles of 64) that a workgroup takes at least, where there are more
+    int min_steps;  // steps (64 tokens; kinds 1, 2: 32) that a workgroup takes at least, where there are more
     int part_cols;  // query rows of a tile that the partial sums hold
     uint32_t *counters;
     float *partials;
 };
 constexpr int kKv4MaxSplits = 128;
+hipError_t launch_kv4_decode(const Kv4AttnArgs &g, hipStream_t st);
 hipError_t launch_kv4_attention(const Kv4AttnArgs &g, hipStream_t st);
 hipError_t launch_kv4_prefill(const Kv4AttnArgs &g, hipStream_t st);
 
