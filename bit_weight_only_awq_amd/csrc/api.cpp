@@ -592,8 +592,9 @@ static int check_kv4(int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t num_
     return AWQ_OK;
 }
 
+static constexpr int kKv4Apart = 8;
 struct Kv4Plan {
-    int kind, splits, min_steps, part_cols;
+    int kind, splits, chunk, part_cols, apart;
     int64_t col_tiles, tiles;
     size_t workspace_bytes;
 };
@@ -608,10 +609,14 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
     const int64_t tile_rows[] = {4, 16, 32, 128}, step[] = {64, 32, 32, 64};
     p.col_tiles = cdiv(rows, tile_rows[p.kind]);
     p.part_cols = (int)std::min<int64_t>(rows, tile_rows[p.kind]);
-    p.min_steps = p.kind == 0 || p.kind == 3 ? 4 : 8;
     p.tiles = B * Hkv * p.col_tiles;
-    const int64_t most = cdiv(cdiv(max_kv, step[p.kind]), p.min_steps), fill = 2 * (int64_t)d.cus;
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(fill, p.tiles), most, (int64_t)kKv4MaxSplits}));
+    // workgroups to fill the device, each with `least` steps at least
+    const int64_t steps = std::max<int64_t>(1, cdiv(max_kv, step[p.kind])), fill = 2 * (int64_t)d.cus;
+    const int64_t least = p.kind == 0 || p.kind == 3 ? 4 : 8;
+    const int64_t splits = std::min<int64_t>(cdiv(fill, p.tiles), kKv4MaxSplits);
+    p.chunk = (int)std::max(least, cdiv(steps, splits));
+    p.splits = (int)cdiv(steps, p.chunk);
+    p.apart = p.splits >= kKv4Apart;
     if (p.splits > 1)
         p.workspace_bytes =
             (size_t)(split_counters_bytes(p.tiles) + p.tiles * p.splits * p.part_cols * (D + 4) * 4);
@@ -996,15 +1001,17 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
     if (rc != AWQ_OK) return rc;
     Kv4AttnArgs g{q, cache, tables, lens, cu_q, out, num_pages, (int)B, (int)total_q, (int)max_q, (int)Hq, (int)Hkv,
                   (int)head_dim, (int)page_size, (int)table_stride, (int)std::min<int64_t>(window, kMaxTokens), dtype,
-                  scale, p.kind, (int)p.col_tiles, p.splits, p.min_steps, p.part_cols, nullptr, nullptr};
+                  scale, p.kind, (int)p.col_tiles, p.splits, p.chunk, p.part_cols, p.apart, nullptr, nullptr};
     if (p.workspace_bytes) {
         g.counters = static_cast<uint32_t *>(workspace);
         g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + split_counters_bytes(p.tiles));
     }
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return hip_status(p.kind == 0   ? launch_kv4_decode(g, st)
-                      : p.kind == 3 ? launch_kv4_prefill(g, st)
-                                    : launch_kv4_attention(g, st));
+    rc = hip_status(p.kind == 0   ? launch_kv4_decode(g, st)
+                    : p.kind == 3 ? launch_kv4_prefill(g, st)
+                                  : launch_kv4_attention(g, st));
+    if (rc != AWQ_OK || !p.apart) return rc;
+    return hip_status(launch_kv4_reduce(g, st));
 }
 
 }  // extern "C"

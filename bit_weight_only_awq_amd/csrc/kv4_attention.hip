@@ -66,31 +66,14 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
     const int h = bh % g.Hkv, b = bh / g.Hkv;
     const int G = g.Hq / g.Hkv;
 
-    // the sequence's rows and length; whatever the arrays hold, no index
-    // leaves the tensors
-    int q0 = b, q1 = b + 1;
-    if (g.cu_q) {
-        q0 = min(max(g.cu_q[b], 0), g.total_q);
-        q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
-    }
-    const int nq = q1 - q0;
-    const int kv_len = min(max(g.lens[b], 0), g.table_stride * g.P);
-    const int rows = min(nq, g.max_q) * G, c0 = ct * COLS;
-    if (c0 >= rows) return;
-    const int ncols = min(COLS, rows - c0);
-
-    // tokens that any column of the tile sees: [kv_lo, kv_hi)
-    const int first_pos = kv_len - nq + c0 / G, last_pos = kv_len - nq + (c0 + ncols - 1) / G;
-    const int kv_hi = max(last_pos + 1, 0);
-    const int kv_lo = g.window > 0 ? min(max(first_pos - g.window + 1, 0), kv_hi) : 0;
-    // ... and that all of them see: [all_lo, all_hi)
-    const int all_hi = first_pos + 1;
-    const int all_lo = g.window > 0 ? max(last_pos - g.window + 1, 0) : 0;
-    const int step0 = kv_lo >> 5, steps = kv_hi > kv_lo ? ((kv_hi + 31) >> 5) - step0 : 0;
-    const int splits = max(1, min(g.splits, (steps + g.min_steps - 1) / g.min_steps));
-    if (split >= splits) return;
-    const int per = (steps + splits - 1) / splits;
-    const int s_begin = step0 + split * per, s_end = min(step0 + steps, s_begin + per);
+    const Kv4Span<COLS, 32> span(g, b, ct, G);
+    const int q0 = span.q0, kv_len = span.kv_len, c0 = span.c0, ncols = span.ncols, splits = span.splits;
+    if (ncols <= 0 || split >= splits) return;
+    const int s_begin = span.first(split), s_end = span.first(split + 1);
+    const int kv_lo = span.kv_lo, kv_hi = span.kv_hi;
+    // tokens that all of the tile's rows see: [all_lo, all_hi)
+    const int all_hi = span.pos_of(c0, G) + 1;
+    const int all_lo = g.window > 0 ? max(span.pos_of(c0 + ncols - 1, G) - g.window + 1, 0) : 0;
 
     const int lgP = __builtin_ctz(g.P);
     // (in the constant address space: no kernel of this call writes it, so it is
@@ -145,7 +128,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
         const bool live = col < ncols;
         const int row = c0 + (live ? col : 0);
         const int qi = row / G, hg = row - qi * G;
-        const int pos = kv_len - nq + qi;
+        const int pos = span.pos_of(row, G);
         hi[n] = pos + 1;
         lo[n] = g.window > 0 ? pos - g.window + 1 : 0;
         const uint16_t *src = (const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D + 8 * KW * grp;
@@ -347,7 +330,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
         __syncthreads();
         out.template join<kAttnWaves>(&lds_o[0][0][0], [](int w, int col) { return 16 * w + col; }, 16 * n, nc);
     }
-    if (splits > 1 && split_tile_last_atomic(g.counters + tile, splits))
+    if (splits > 1 && !g.apart && split_tile_last_atomic(g.counters + tile, splits))
         out.exchange(&lds_o[0][0][0], ncols);
 }
 

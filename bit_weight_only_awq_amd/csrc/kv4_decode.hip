@@ -68,26 +68,14 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnA
     const int h = tile % g.Hkv, b = tile / g.Hkv;
     const int G = g.Hq / g.Hkv;
 
-    int q0 = b, q1 = b + 1;
-    if (g.cu_q) {
-        q0 = min(max(g.cu_q[b], 0), g.total_q);
-        q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
-    }
-    const int nq = q1 - q0;
-    const int kv_len = min(max(g.lens[b], 0), g.table_stride * g.P);
-    const int ncols = min(nq, g.max_q) * G;  // 1 .. 4
-    if (ncols == 0) return;
-
-    // tokens that any row sees: [kv_lo, kv_hi), and that all of them see
-    const int base_pos = kv_len - nq, last_pos = base_pos + (ncols - 1) / G;
-    const int kv_hi = max(last_pos + 1, 0);
-    const int kv_lo = g.window > 0 ? min(max(base_pos - g.window + 1, 0), kv_hi) : 0;
-    const int all_hi = base_pos + 1, all_lo = g.window > 0 ? max(last_pos - g.window + 1, 0) : 0;
-    const int step0 = kv_lo >> 6, steps = kv_hi > kv_lo ? ((kv_hi + 63) >> 6) - step0 : 0;
-    const int splits = max(1, min(g.splits, (steps + g.min_steps - 1) / g.min_steps));
-    if (split >= splits) return;
-    const int per = (steps + splits - 1) / splits;
-    const int s_begin = step0 + split * per, s_end = min(step0 + steps, s_begin + per);
+    const Kv4Span<4, 64> span(g, b, 0, G);
+    const int q0 = span.q0, kv_len = span.kv_len, ncols = span.ncols, splits = span.splits;
+    if (ncols <= 0 || split >= splits) return;
+    const int s_begin = span.first(split), s_end = span.first(split + 1);
+    const int kv_lo = span.kv_lo, kv_hi = span.kv_hi;
+    // tokens that all rows see: [all_lo, all_hi)
+    const int all_hi = span.pos_of(0, G) + 1;
+    const int all_lo = g.window > 0 ? max(span.pos_of(ncols - 1, G) - g.window + 1, 0) : 0;
 
     const int lgP = __builtin_ctz(g.P);
     const auto *table = (const __attribute__((address_space(4))) int32_t *)(g.tables + (size_t)b * g.table_stride);
@@ -139,7 +127,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnA
     int lo, hi;
     {
         const int row = j < ncols ? j : 0, qi = row / G, hg = row - qi * G;
-        const int pos = base_pos + qi;
+        const int pos = span.pos_of(row, G);
         hi = pos + 1;
         lo = g.window > 0 ? pos - g.window + 1 : 0;
         const uint16_t *src = (const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D;
@@ -321,7 +309,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnA
     __syncthreads();
     // (partial 4 w + s of row j: wave w, column 4 s + j)
     out.template join<4 * kAttnWaves>(&lds_o[0][0][0], [](int p, int col) { return 4 * p + col; }, 0, ncols);
-    if (splits > 1 && split_tile_last_atomic(g.counters + tile, splits)) out.exchange(&lds_o[0][0][0], ncols);
+    if (splits > 1 && !g.apart && split_tile_last_atomic(g.counters + tile, splits)) out.exchange(&lds_o[0][0][0], ncols);
 }
 
 template <int DT, int D>

@@ -20,15 +20,13 @@
 // two tiles ahead and unpacked one ahead, one barrier a tile.  Two workgroups
 // (64 KB each at D = 128) share a CU, out of step, so that one's exponentials
 // run beside the other's matrix products.
-#include "kv4.hpp"
-#include "launch.hpp"
+#include "kv4_ops.hpp"
 
 namespace awq4 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kPreWaves = 4, kPreTile = 64;  // waves (32 rows each) and tokens of a tile
-constexpr float kPreNoRef = -1e30f, kPreMaxP = 0x1p15f, kPreMaxSum = 0x1p100f;
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
@@ -44,10 +42,6 @@ __device__ __forceinline__ float pair_max(float v) {
 __device__ __forceinline__ float pair_sum(float v) {
     const auto h = __builtin_amdgcn_permlane32_swap(bit_as<uint32_t>(v), bit_as<uint32_t>(v), false, false);
     return bit_as<float>((uint32_t)h[0]) + bit_as<float>((uint32_t)h[1]);
-}
-
-__device__ __forceinline__ uint32_t pre_pack_f16(float a, float b) {
-    return bit_as<uint32_t>(__builtin_convertvector((f32x2){a, b}, f16x2));
 }
 
 // One tile in LDS, in bytes: keys [64][D] and values [D][64] as 16-bit
@@ -98,35 +92,20 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
     const int h = bh % g.Hkv, b = bh / g.Hkv, split = blockIdx.y;
     const int G = g.Hq / g.Hkv;
 
-    int q0 = b, q1 = b + 1;
-    if (g.cu_q) {
-        q0 = min(max(g.cu_q[b], 0), g.total_q);
-        q1 = min(max(g.cu_q[b + 1], q0), g.total_q);
-    }
-    const int nq = q1 - q0;
-    const int kv_len = min(max(g.lens[b], 0), g.table_stride * g.P);
-    const int rows = min(nq, g.max_q) * G, c0 = ct * COLS;
-    if (c0 >= rows) return;
-    const int ncols = min(COLS, rows - c0);
-
-    // tokens that any row of the workgroup sees: [kv_lo, kv_hi)
-    const int base = kv_len - nq;
-    const int kv_hi = max(base + (c0 + ncols - 1) / G + 1, 0);
-    const int kv_lo = g.window > 0 ? min(max(base + c0 / G - g.window + 1, 0), kv_hi) : 0;
-    const int tile0 = kv_lo / kPreTile, tiles = kv_hi > kv_lo ? (kv_hi + kPreTile - 1) / kPreTile - tile0 : 0;
-    const int splits = max(1, min(g.splits, tiles / g.min_steps));
-    if (split >= splits) return;
-    const int per = (tiles + splits - 1) / splits;
-    const int t_begin = tile0 + split * per, t_end = min(tile0 + tiles, t_begin + per);
-    // ... that any row of this wave sees, and that all of them see
+    const Kv4Span<COLS, kPreTile> span(g, b, ct, G);
+    const int q0 = span.q0, kv_len = span.kv_len, c0 = span.c0, ncols = span.ncols, splits = span.splits;
+    if (ncols <= 0 || split >= splits) return;
+    const int t_begin = span.first(split), t_end = span.first(split + 1);
+    const int kv_lo = span.kv_lo, kv_hi = span.kv_hi;
+    // tokens that any row of this wave sees, and that all of them see
     const int w0 = c0 + 32 * wave, w1 = min(w0 + 32, c0 + ncols);  // w1 <= w0: no rows
-    const int first_pos = base + w0 / G, last_pos = base + (max(w1, w0 + 1) - 1) / G;
+    const int first_pos = span.pos_of(w0, G), last_pos = span.pos_of(max(w1, w0 + 1) - 1, G);
     const int wave_hi = w1 > w0 ? last_pos + 1 : 0, wave_lo = g.window > 0 ? first_pos - g.window + 1 : 0;
     const int all_hi = first_pos + 1, all_lo = g.window > 0 ? last_pos - g.window + 1 : 0;
 
     // this lane's row
     const int row = min(w0 + c32, c0 + ncols - 1), qi = row / G, hg = row - qi * G;
-    const int hi = base + qi + 1, lo = g.window > 0 ? base + qi - g.window + 1 : 0;
+    const int hi = span.pos_of(row, G) + 1, lo = g.window > 0 ? hi - g.window : 0;
     const size_t row_at = ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D;
     u32x4 qf[KS];
 #pragma unroll
@@ -251,7 +230,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
     };
 
     f32x16 o[DTL];
-    float ref = kPreNoRef, l = 0.0f;
+    float ref = kNoRef, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < DTL; ++i)
 #pragma unroll
@@ -278,9 +257,9 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
         f32x16 x[2];
         uint32_t pf[2][8];
         float sum;
-        bool raise = __builtin_amdgcn_ballot_w64(ref == kPreNoRef) != 0;  // rows that have seen nothing yet
+        bool raise = __builtin_amdgcn_ballot_w64(ref == kNoRef) != 0;  // rows that have seen nothing yet
         while (true) {
-            const float from_ref = ref == kPreNoRef ? 0.0f : ref;
+            const float from_ref = ref == kNoRef ? 0.0f : ref;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -300,7 +279,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
                 }
             __builtin_amdgcn_sched_barrier(0);
             if (raise) {
-                float m = ref == kPreNoRef ? kPreNoRef : 0.0f;
+                float m = ref == kNoRef ? kNoRef : 0.0f;
                 const int from = opaque(at);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -316,7 +295,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
                     }
                 m = pair_max(m);
                 const float f = m > 0.0f ? __builtin_amdgcn_exp2f(-m) : 1.0f;  // (a first reference: o and l are 0)
-                ref = m == kPreNoRef ? kPreNoRef : from_ref + m;
+                ref = m == kNoRef ? kNoRef : from_ref + m;
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < DTL; ++i) o[i] *= f;
@@ -348,11 +327,11 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
                         sum += x[u][4 * a + r];
                         top = fmaxf(top, w[r]);
                     }
-                    pf[u][2 * a] = pre_pack_f16(w[0], w[1]);
-                    pf[u][2 * a + 1] = pre_pack_f16(w[2], w[3]);
+                    pf[u][2 * a] = pack_f16(w[0], w[1]);
+                    pf[u][2 * a + 1] = pack_f16(w[2], w[3]);
                 }
             if (raise) break;
-            raise = __builtin_amdgcn_ballot_w64(!(top <= kPreMaxP && sum <= kPreMaxSum)) != 0;
+            raise = __builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0;
             if (!raise) break;
         }
         l += sum;
@@ -407,36 +386,51 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
     // arrive adds them in order, writes and clears
     const size_t tile_at = (size_t)ct * (g.B * g.Hkv) + bh;
     float *part = g.partials + tile_at * g.splits * (size_t)(g.part_cols * ROW);
-    auto row_of = [&](int s) { return part + ((size_t)s * g.part_cols + (32 * wave + c32)) * ROW; };
+    const auto rows_at = buf_rsrc(part, (int64_t)splits * g.part_cols * ROW * 4);
+    const uint32_t mine = ((32 * wave + c32) * ROW + 4 * half) * 4;  // this lane's quads: + 8 dimensions each
+    auto at = [&](int s, int d) { return (int)(mine + (uint32_t)(s * g.part_cols * ROW + d) * 4); };
+    auto put_part = [&](int o, f32x4 v) {
+        __builtin_amdgcn_raw_buffer_store_b128(bit_as<u32x4>(v), rows_at, o, 0, kPartCoherent);
+    };
+    auto get_part = [&](int o) { return bit_as<f32x4>(__builtin_amdgcn_raw_buffer_load_b128(rows_at, o, 0, kPartCoherent)); };
+    const int ref_at = D - 4 * half;  // (past the sums, for either half)
     if (live) {
 #pragma unroll
-        for (int i = 0; i < DTL; ++i)
-#pragma unroll
-            for (int a = 0; a < 4; ++a) part_put((uint64_t *)(row_of(split) + 32 * i + 8 * a + 4 * half), quad(i, a));
-        if (half == 0) part_put((uint64_t *)(row_of(split) + D), (f32x4){ref, lsum, 0, 0});
+        for (int q = 0; q < 4 * DTL; ++q) put_part(at(split, 8 * q), quad(q / 4, q % 4));
+        if (half == 0) put_part(at(split, ref_at), (f32x4){ref, lsum, 0, 0});
     }
-    if (!split_tile_last_atomic(g.counters + tile_at, splits)) return;
+    if (g.apart || !split_tile_last_atomic(g.counters + tile_at, splits)) return;
     if (!live) return;
-    float rr = kPreNoRef, ll = 0.0f;
-    for (int s = 0; s < splits; ++s) rr = fmaxf(rr, part_get<f32x4>((uint64_t *)(row_of(s) + D))[0]);
+    // (one split's quads in flight while the one before is added)
+    f32x4 now[4 * DTL], next[4 * DTL], rl, rl_next;
+    auto fetch = [&](f32x4 (&w)[4 * DTL], f32x4 &r, int s) {
+        r = get_part(at(s, ref_at));
+#pragma unroll
+        for (int q = 0; q < 4 * DTL; ++q) w[q] = get_part(at(s, 8 * q));
+    };
+    float rr = kNoRef, ll = 0.0f;
 #pragma unroll
     for (int i = 0; i < DTL; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+    fetch(now, rl, 0);
     for (int s = 0; s < splits; ++s) {
-        const f32x4 rl = part_get<f32x4>((uint64_t *)(row_of(s) + D));
-        const float f = __builtin_amdgcn_exp2f(rl[0] - rr);
-        ll += f * rl[1];
+        if (s + 1 < splits) fetch(next, rl_next, s + 1);
+        const float top = fmaxf(rr, rl[0]);
+        const float old = __builtin_amdgcn_exp2f(rr - top), f = __builtin_amdgcn_exp2f(rl[0] - top);
+        rr = top;
+        ll = ll * old + f * rl[1];
 #pragma unroll
-        for (int i = 0; i < DTL; ++i)
+        for (int q = 0; q < 4 * DTL; ++q) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                uint64_t *p = (uint64_t *)(row_of(s) + 32 * i + 8 * a + 4 * half);
-                const f32x4 v = part_get<f32x4>(p);
-                part_put(p, (f32x4){0, 0, 0, 0});
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[i][4 * a + r] = __builtin_fmaf(f, v[r], o[i][4 * a + r]);
+            for (int r = 0; r < 4; ++r) {
+                const int e = 4 * (q % 4) + r;
+                o[q / 4][e] = __builtin_fmaf(f, now[q][r], o[q / 4][e] * old);
             }
+            now[q] = next[q];
+            put_part(at(s, 8 * q), (f32x4){0, 0, 0, 0});
+        }
+        rl = rl_next;
     }
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
@@ -445,7 +439,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 2) void kv4_prefill_kernel(Kv4AttnA
         for (int a = 0; a < 4; ++a) put(row_at, 32 * i + 8 * a + 4 * half, quad(i, a) * inv);
     // (both lanes of a row have read its references by now: they run together)
     if (half == 0)
-        for (int s = 0; s < splits; ++s) part_put((uint64_t *)(row_of(s) + D), (f32x4){0, 0, 0, 0});
+        for (int s = 0; s < splits; ++s) put_part(at(s, ref_at), (f32x4){0, 0, 0, 0});
 }
 
 template <int DT, int D>

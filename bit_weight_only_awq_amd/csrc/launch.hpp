@@ -198,8 +198,9 @@ struct Kv4AttnArgs {
     int kind;       // kernel: 0 at most four rows, 1 and 2 tiles of 16 and 32 rows, 3 the prefill kernel (128 rows)
     int col_tiles;  // workgroups along the query rows of a sequence and key/value head
     int splits;     // most workgroups along a sequence's tokens
-    int min_steps;  // steps (64 tokens; kinds 1, 2: 32) that a workgroup takes at least, where there are more
+    int chunk;      // steps (64 tokens; kinds 1, 2: 32) that a workgroup takes
     int part_cols;  // query rows of a tile that the partial sums hold
+    int apart;      // the workgroups' sums are added by a second kernel, not by the last of them
     uint32_t *counters;
     float *partials;
 };
@@ -207,5 +208,6 @@ constexpr int kKv4MaxSplits = 128;
 hipError_t launch_kv4_decode(const Kv4AttnArgs &g, hipStream_t st);
 hipError_t launch_kv4_attention(const Kv4AttnArgs &g, hipStream_t st);
 hipError_t launch_kv4_prefill(const Kv4AttnArgs &g, hipStream_t st);
+hipError_t launch_kv4_reduce(const Kv4AttnArgs &g, hipStream_t st);
 
 }  // namespace awq4
