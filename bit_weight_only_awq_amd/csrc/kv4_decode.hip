@@ -55,11 +55,13 @@ __device__ __forceinline__ uint32_t row_broadcast(uint32_t v) {
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnArgs g) {
+__global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnArgs g) {
     using L = Kv4Layout<D>;
     using Quad = Kv4Quad<D>;
     constexpr int KW = D / 32, VM = D / 16, ROW = AttnRows<DT, D>::kRow;
     __shared__ float lds_o[kAttnWaves][16][ROW];
+    __shared__ __attribute__((aligned(16))) uint32_t lds_q[5][D / 2 + 4];  // (rows four banks apart)
+    __shared__ float lds_row[4][2];  // sum of q, factor of the scores
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, grp = lane >> 4, run = r16 >> 2, j = r16 & 3;
@@ -121,43 +123,37 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnA
         load(cur, now_e, 64 * st);
     }
 
-    // the row of this lane's column, zero but in the lane group of its run
-    u32x4 qf[4 * KW];
-    float qz, cf;
-    int lo, hi;
+    // The rows of q, in fp16 and in the order of the operands, in LDS: wave w
+    // takes row w, a lane two dimensions (D = 64: the upper lanes none).  A lane
+    // reads its column's row in the lane group of its run, and zeros elsewhere.
     {
-        const int row = j < ncols ? j : 0, qi = row / G, hg = row - qi * G;
-        const int pos = span.pos_of(row, G);
-        hi = pos + 1;
-        lo = g.window > 0 ? pos - g.window + 1 : 0;
-        const uint16_t *src = (const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D;
-        // every lane reads its row's whole q (its four groups and runs the same): no exchange for the
-        // largest value and the sum
-        float mx = 0.0f, sum = 0.0f;
-        u32x4 w[4 * KW];
+        const int row = wave < ncols ? wave : 0, qi = row / G, hg = row - qi * G;
+        const bool holds = 2 * lane < D;
+        const uint32_t *src = (const uint32_t *)((const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D);
+        const uint32_t w = holds ? src[lane] : 0u;
+        float f[2] = {act_bits_to_f32<DT>(w & 0xFFFFu), act_bits_to_f32<DT>(w >> 16)};
+        float mx = fmaxf(fabsf(f[0]), fabsf(f[1]));
 #pragma unroll
-        for (int i = 0; i < 4 * KW; ++i) {
-            w[i] = *(const u32x4 *)(src + 8 * i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                mx = fmaxf(mx, fabsf(act_bits_to_f32<DT>((w[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
-        }
+        for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
         const int up = query_shift(mx);
+        f[0] = __builtin_ldexpf(f[0], up);
+        f[1] = __builtin_ldexpf(f[1], up);
+        float sum = f[0] + f[1];
 #pragma unroll
-        for (int i = 0; i < 4 * KW; ++i) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = __builtin_ldexpf(act_bits_to_f32<DT>((w[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu), up);
-                sum += f[e];
-            }
-            const u32x4 op = query_operand(f);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) qf[i][p] = grp == run ? op[p] : 0u;
+        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        const float down = lane & 1 ? 0.0625f : 1.0f;  // columns 2, 3, 6, 7 of a word meet codes times 16
+        if (holds) lds_q[wave][lane] = pack_f16(f[0] * down, f[1] * down);
+        if (lane == 0) {
+            lds_row[wave][0] = sum * 0x1p-24f;
+            lds_row[wave][1] = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
         }
-        qz = sum * 0x1p-24f;
-        cf = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
+        if (tid < D / 2) lds_q[4][tid] = 0u;
     }
+    __syncthreads();
+    const u32x4 *q_from = (const u32x4 *)lds_q[grp == run ? j : 4];
+    const float qz = lds_row[j][0], cf = lds_row[j][1];
+    const int pos = span.pos_of(j < ncols ? j : 0, G);
+    const int hi = pos + 1, lo = g.window > 0 ? pos - g.window + 1 : 0;
     uint32_t mine[4];  // all ones where this lane's column is of run i
 #pragma unroll
     for (int i = 0; i < 4; ++i) mine[i] = run == i ? 0xFFFFFFFFu : 0u;
@@ -199,8 +195,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void kv4_decode_kernel(Kv4AttnA
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int w = 0; w < KW; w += 2) {
-                x = mfma_f16(word_operand(s.k[i][w]), qf[KW * i + w], x);
-                x1 = mfma_f16(word_operand(s.k[i][w + 1]), qf[KW * i + w + 1], x1);
+                x = mfma_f16(word_operand(s.k[i][w]), q_from[KW * i + w], x);
+                x1 = mfma_f16(word_operand(s.k[i][w + 1]), q_from[KW * i + w + 1], x1);
             }
         x += x1;
         __builtin_amdgcn_sched_barrier(0);
