@@ -126,7 +126,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
     // The rows of q, in fp16 and in the order of the operands, in LDS: wave w
     // takes row w, a lane two dimensions (D = 64: the upper lanes none).  A lane
     // reads its column's row in the lane group of its run, and zeros elsewhere.
-    {
+    if (tid < D / 2) lds_q[4][tid] = 0u;
+    if (wave < 4) {
         const int row = wave < ncols ? wave : 0, qi = row / G, hg = row - qi * G;
         const bool holds = 2 * lane < D;
         const uint32_t *src = (const uint32_t *)((const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D);
@@ -147,7 +148,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
             lds_row[wave][0] = sum * 0x1p-24f;
             lds_row[wave][1] = __builtin_ldexpf(g.scale * 1.4426950408889634f, 24 - up);
         }
-        if (tid < D / 2) lds_q[4][tid] = 0u;
     }
     __syncthreads();
     const u32x4 *q_from = (const u32x4 *)lds_q[grp == run ? j : 4];
