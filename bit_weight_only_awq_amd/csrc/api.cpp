@@ -606,15 +606,17 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
     Kv4Plan p{};
     const int64_t rows = max_q * (Hq / Hkv);
     p.kind = rows <= 4 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
-    const int64_t tile_rows[] = {4, 16, 32, 128}, step[] = {64, 32, 32, 64};
+    const int64_t tile_rows[] = {4, 16, 32, 256}, step[] = {64, 32, 32, 128};
     p.col_tiles = cdiv(rows, tile_rows[p.kind]);
     p.part_cols = (int)std::min<int64_t>(rows, tile_rows[p.kind]);
     p.tiles = B * Hkv * p.col_tiles;
-    // workgroups to fill the device, each with `least` steps at least
-    const int64_t steps = std::max<int64_t>(1, cdiv(max_kv, step[p.kind])), fill = 2 * (int64_t)d.cus;
-    const int64_t least = p.kind == 0 || p.kind == 3 ? 4 : 8;
+    // workgroups to fill the device (a prompt's takes a whole CU, two of the
+    // others go to one at least), each with `least` steps at least
+    const int64_t steps = std::max<int64_t>(1, cdiv(max_kv, step[p.kind]));
+    const int64_t fill = (p.kind == 3 ? 1 : 2) * (int64_t)d.cus;
+    const int64_t least[] = {4, 8, 8, 2};
     const int64_t splits = std::min<int64_t>(cdiv(fill, p.tiles), kKv4MaxSplits);
-    p.chunk = (int)std::max(least, cdiv(steps, splits));
+    p.chunk = (int)std::max(least[p.kind], cdiv(steps, splits));
     p.splits = (int)cdiv(steps, p.chunk);
     p.apart = p.splits >= kKv4Apart;
     if (p.splits > 1)

@@ -29,12 +29,12 @@ namespace awq4 {
 // 131072 63 -> 56 us; caches small enough to stay in the memory-side cache
 // from call to call read up to 8 % slower).
 constexpr int kStreamOnce = 2;
-template <typename T>
+template <typename T, int POLICY = kStreamOnce>
 __device__ __forceinline__ T buf_get(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t scalar) {
     if constexpr (sizeof(T) == 8)
-        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)scalar, kStreamOnce));
+        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b64(r, (int)lane, (int)scalar, POLICY));
     else
-        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)scalar, kStreamOnce));
+        return bit_as<T>(__builtin_amdgcn_raw_buffer_load_b128(r, (int)lane, (int)scalar, POLICY));
 }
 
 template <int D>

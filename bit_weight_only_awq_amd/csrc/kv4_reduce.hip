@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256) void kv4_reduce_kernel(Kv4AttnArgs g) {
     const int G = g.Hq / g.Hkv;
     // the attention kernels' order of tiles
     const int bhs = g.B * g.Hkv;
-    const int ct = TILE == 128 ? tile / bhs : tile % g.col_tiles, bh = TILE == 128 ? tile % bhs : tile / g.col_tiles;
+    const int ct = TILE == 256 ? tile / bhs : tile % g.col_tiles, bh = TILE == 256 ? tile % bhs : tile / g.col_tiles;
     const int h = bh % g.Hkv, b = bh / g.Hkv;
     const Kv4Span<TILE, STEP> span(g, b, ct, G);
     if (col >= span.ncols || span.splits == 1) return;
@@ -82,7 +82,7 @@ static hipError_t launch_reduce_kind(const Kv4AttnArgs &g, hipStream_t st) {
         case 0: return launch_reduce<DT, D, 4, 64>(g, st);
         case 1: return launch_reduce<DT, D, 16, 32>(g, st);
         case 2: return launch_reduce<DT, D, 32, 32>(g, st);
-        default: return launch_reduce<DT, D, 128, 64>(g, st);
+        default: return launch_reduce<DT, D, 256, 128>(g, st);
     }
 }
 
