@@ -592,12 +592,28 @@ static int check_kv4(int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t num_
     return AWQ_OK;
 }
 
-static constexpr int kKv4Apart = 8;
 struct Kv4Plan {
-    int kind, splits, chunk, part_cols, apart;
+    int kind, splits, chunk, part_cols;
     int64_t col_tiles, tiles;
     size_t workspace_bytes;
 };
+// Which attention kernel (heads: sequences times key/value heads; times of
+// 32 query heads over 8, D = 128, bf16, pages of 16):
+//  - at most four rows: kv4_decode.hip.  64 sequences of about 4900 tokens 81 us,
+//    tiles of 16 rows 89.
+//  - the prefill kernel where every CU gets four of its steps or more and a tile
+//    more than half its rows: 16 x 192 rows over 4096 tokens 88 us, tiles of 16
+//    and 32 rows 110 and 104; four prompts of 512 tokens 32, 44 and 51.  Less
+//    work leaves it waiting: 256 rows of one sequence over 8192 tokens 40 us
+//    against 35 and 32, four times 256 over 1024 27 against 18 and 25; 16 x 128
+//    rows over 4096 tokens 84 against 85 and 65.
+//  - tiles of 32 rows where they fill the device, as in that last case; a prompt
+//    of 128 tokens 10 us, in tiles of 16 rows 7.
+static int kv4_kind(int64_t rows, int64_t heads, int64_t max_kv, int64_t cus) {
+    if (rows <= 4) return 0;
+    if (rows > 128 && heads * cdiv(rows, 256) * cdiv(max_kv, 128) >= 4 * cus) return 3;
+    return heads * cdiv(rows, 32) >= 2 * cus ? 2 : 1;
+}
 // How an attention call is launched (pure function of the shape; the lengths
 // themselves are known on the device only, where a sequence takes as many of
 // its workgroups as it has steps for).
@@ -605,23 +621,20 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
                         const DeviceProps &d) {
     Kv4Plan p{};
     const int64_t rows = max_q * (Hq / Hkv);
-    p.kind = rows <= 4 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
+    p.kind = kv4_kind(rows, B * Hkv, max_kv, d.cus);
     const int64_t tile_rows[] = {4, 16, 32, 256}, step[] = {64, 32, 32, 128};
     p.col_tiles = cdiv(rows, tile_rows[p.kind]);
     p.part_cols = (int)std::min<int64_t>(rows, tile_rows[p.kind]);
     p.tiles = B * Hkv * p.col_tiles;
-    // workgroups to fill the device (a prompt's takes a whole CU, two of the
-    // others go to one at least), each with `least` steps at least
+    // workgroups to fill the device, each with `least` steps at least: of the
+    // prefill kernel one goes to a CU, so no more than CUs; of the others two at least
     const int64_t steps = std::max<int64_t>(1, cdiv(max_kv, step[p.kind]));
-    const int64_t fill = (p.kind == 3 ? 1 : 2) * (int64_t)d.cus;
     const int64_t least[] = {4, 8, 8, 2};
-    const int64_t splits = std::min<int64_t>(cdiv(fill, p.tiles), kKv4MaxSplits);
+    const int64_t fill = p.kind == 3 ? std::max<int64_t>(1, d.cus / p.tiles) : cdiv(2 * (int64_t)d.cus, p.tiles);
+    const int64_t splits = std::min<int64_t>(fill, kKv4MaxSplits);
     p.chunk = (int)std::max(least[p.kind], cdiv(steps, splits));
     p.splits = (int)cdiv(steps, p.chunk);
-    p.apart = p.splits >= kKv4Apart;
-    if (p.splits > 1)
-        p.workspace_bytes =
-            (size_t)(split_counters_bytes(p.tiles) + p.tiles * p.splits * p.part_cols * (D + 4) * 4);
+    if (p.splits > 1) p.workspace_bytes = (size_t)(p.tiles * p.splits * p.part_cols * (D + 4) * 4);
     return p;
 }
 static int check_attention(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_kv) {
@@ -1003,16 +1016,12 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
     if (rc != AWQ_OK) return rc;
     Kv4AttnArgs g{q, cache, tables, lens, cu_q, out, num_pages, (int)B, (int)total_q, (int)max_q, (int)Hq, (int)Hkv,
                   (int)head_dim, (int)page_size, (int)table_stride, (int)std::min<int64_t>(window, kMaxTokens), dtype,
-                  scale, p.kind, (int)p.col_tiles, p.splits, p.chunk, p.part_cols, p.apart, nullptr, nullptr};
-    if (p.workspace_bytes) {
-        g.counters = static_cast<uint32_t *>(workspace);
-        g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + split_counters_bytes(p.tiles));
-    }
+                  scale, p.kind, (int)p.col_tiles, p.splits, p.chunk, p.part_cols, static_cast<float *>(workspace)};
     hipStream_t st = static_cast<hipStream_t>(stream);
     rc = hip_status(p.kind == 0   ? launch_kv4_decode(g, st)
                     : p.kind == 3 ? launch_kv4_prefill(g, st)
                                   : launch_kv4_attention(g, st));
-    if (rc != AWQ_OK || !p.apart) return rc;
+    if (rc != AWQ_OK || p.splits == 1) return rc;
     return hip_status(launch_kv4_reduce(g, st));
 }
 

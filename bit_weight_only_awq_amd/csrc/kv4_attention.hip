@@ -36,8 +36,8 @@
 // Bound: device memory (D + 8 bytes a token and head, read once).  A workgroup
 // of four waves takes a run of tokens, each wave 32 of every 128; the four
 // join their sums through LDS, and the workgroups of a sequence (as many as
-// its length asks for, known only on the device) join theirs through the
-// workspace: the last to arrive adds them in order, writes and clears.
+// its length asks for, known only on the device) leave theirs in the workspace
+// for kv4_reduce.hip.
 #include "kv4_ops.hpp"
 
 namespace awq4 {
@@ -309,8 +309,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
         run(nxt, cur);
     }
 
-    // Join the four waves, 16 columns at a time; then write, or exchange with
-    // the sequence's other workgroups.
+    // Join the four waves, 16 columns at a time.
     const AttnRows<DT, D> out{g, tile, splits, split, c0, q0, h, G};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -330,8 +329,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
         __syncthreads();
         out.template join<kAttnWaves>(&lds_o[0][0][0], [](int w, int col) { return 16 * w + col; }, 16 * n, nc);
     }
-    if (splits > 1 && !g.apart && split_tile_last_atomic(g.counters + tile, splits))
-        out.exchange(&lds_o[0][0][0], ncols);
 }
 
 template <int DT, int D, int NT>

@@ -305,7 +305,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
     __syncthreads();
     // (partial 4 w + s of row j: wave w, column 4 s + j)
     out.template join<4 * kAttnWaves>(&lds_o[0][0][0], [](int p, int col) { return 4 * p + col; }, 0, ncols);
-    if (splits > 1 && !g.apart && split_tile_last_atomic(g.counters + tile, splits)) out.exchange(&lds_o[0][0][0], ncols);
 }
 
 template <int DT, int D>

@@ -133,7 +133,7 @@ struct Kv4Span {
 };
 
 // The rows of one workgroup's tile: partial sums joined in LDS, then written,
-// or exchanged through the workspace and written by the last workgroup.
+// or left in the workspace for kv4_reduce.hip.
 template <int DT, int D>
 struct AttnRows {
     static constexpr int kRow = D + 4;  // floats of a partial row: D sums, reference, sum of p, two unused
@@ -170,105 +170,10 @@ struct AttnRows {
             if (splits == 1) {
                 put(col0 + col, d, quotient(v, ll));
             } else {
-                const auto row = buf_rsrc(row_of(split, col0), (int64_t)nc * kRow * 4);
-                auto store = [&](int at, f32x4 x) {
-                    __builtin_amdgcn_raw_buffer_store_b128(bit_as<u32x4>(x), row, 4 * (col * kRow + at), 0, kPartCoherent);
-                };
-                store(d, v);
-                if (d == 0) store(D, (f32x4){rr, ll, 0, 0});
+                float *row = row_of(split, col0 + col);
+                *(f32x4 *)(row + d) = v;
+                if (d == 0) *(f32x4 *)(row + D) = (f32x4){rr, ll, 0, 0};
             }
-        }
-    }
-    // The last workgroup of the tile: every split's rows added, written and
-    // cleared.  What it costs is the way to the device-wide coherence point and
-    // back, so that is made as few times as possible: the threads left over by
-    // the rows' quads take the splits in parallel, eight quads in flight each,
-    // and the references come with the first of them.  The order of the sums is
-    // fixed by the splits' number.  (A loop over the splits, four at a time,
-    // took 12 us of 23 for 32 splits.)
-    __device__ __forceinline__ void exchange(float *lds, int ncols) const {
-        constexpr int T = 64 * kAttnWaves, Q = D / 4, B = 8;
-        float *sums = lds, *refs = lds + 16 * kKv4MaxSplits;
-        static_assert(2 * 16 * kKv4MaxSplits <= kAttnWaves * 16 * kRow, "LDS of the exchange");
-#pragma unroll 1
-        for (int n = 0; n < ncols; n += 16) {
-            const int nc = min(16, ncols - n), slots = nc * Q, groups = max(1, T / slots);
-            // quad i of a group's thread: row i / Q, dimensions 4 (i % Q) ..
-            const int group = min((int)threadIdx.x / slots, groups), first = threadIdx.x - group * slots;
-            const int share = (splits + groups - 1) / groups;
-            const int sb = groups == 1 ? 0 : min(splits, group * share), se = groups == 1 ? splits : min(splits, sb + share);
-            const auto rows = buf_rsrc(row_of(0, n), (int64_t)splits * g.part_cols * kRow * 4);
-            auto at = [&](int s, int col, int d) { return (uint32_t)(((s * g.part_cols + col) * kRow + d) * 4); };
-            auto get = [&](uint32_t o) { return bit_as<f32x4>(__builtin_amdgcn_raw_buffer_load_b128(rows, (int)o, 0, kPartCoherent)); };
-            auto clear = [&](uint32_t o) {
-                __builtin_amdgcn_raw_buffer_store_b128((u32x4){0, 0, 0, 0}, rows, (int)o, 0, kPartCoherent);
-            };
-            const bool active = groups == 1 || group < groups;
-            __syncthreads();
-            // one quad (several where the rows outnumber the threads)
-            for (int i0 = groups == 1 ? (int)threadIdx.x : first, pass = 0; pass < (groups == 1 ? (slots + T - 1) / T : 1);
-                 ++pass, i0 += T) {
-                const bool on = active && i0 < slots;
-                const int col = on ? i0 / Q : 0, d = 4 * (i0 % Q);
-                f32x4 w[B];
-#pragma unroll
-                for (int k = 0; k < B; ++k)
-                    w[k] = on && sb + k < se ? get(at(sb + k, col, d)) : (f32x4){0, 0, 0, 0};
-                if (pass == 0) {
-                    for (int i = threadIdx.x; i < splits * nc; i += T) {
-                        const f32x4 rl = get(at(i / nc, i % nc, D));
-                        refs[i] = rl[0];
-                        sums[i] = rl[1];
-                    }
-                    __syncthreads();
-                }
-                float rr = kNoRef, ll = 0.0f;
-                for (int s0 = 0; s0 < splits; s0 += 16) {  // (sixteen reads in flight)
-                    float r[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) r[k] = refs[min(s0 + k, splits - 1) * nc + col];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) rr = fmaxf(rr, r[k]);
-                }
-                f32x4 v = {0, 0, 0, 0};
-                for (int s0 = sb; s0 < se; s0 += B) {
-#pragma unroll
-                    for (int k = 0; k < B; ++k) {
-                        const int s = min(s0 + k, se - 1);
-                        const float a = s0 + k < se ? __builtin_amdgcn_exp2f(refs[s * nc + col] - rr) : 0.0f;
-                        v += a * w[k];
-                        ll += a * sums[s * nc + col];
-                    }
-#pragma unroll
-                    for (int k = 0; k < B; ++k) {
-                        if (on && s0 + k < se) clear(at(s0 + k, col, d));
-                        w[k] = on && s0 + B + k < se ? get(at(s0 + B + k, col, d)) : (f32x4){0, 0, 0, 0};
-                    }
-                }
-                if (groups > 1) {
-                    // the groups' sums through LDS, in order
-                    __syncthreads();
-                    float *mine = lds + 8 * ((size_t)(active ? group : 0) * slots + first);
-                    if (active && first < slots) {
-                        *(f32x4 *)mine = v;
-                        mine[4] = ll;
-                    }
-                    __syncthreads();
-                    if (group == 0 && first < slots) {
-                        v = (f32x4){0, 0, 0, 0};
-                        ll = 0.0f;
-                        for (int k = 0; k < groups; ++k) {
-                            const float *other = lds + 8 * ((size_t)k * slots + first);
-                            v += *(const f32x4 *)other;
-                            ll += other[4];
-                        }
-                        put(n + col, d, quotient(v, ll));
-                    }
-                } else if (on) {
-                    put(n + col, d, quotient(v, ll));
-                }
-            }
-            for (int i = threadIdx.x; i < splits * nc; i += T) clear(at(i / nc, i % nc, D));
         }
     }
 };

@@ -29,9 +29,9 @@
 // registers of two waves a SIMD: a single spilled one waits for the cache
 // words in flight, which are ahead of it in the queue.
 //
-// Measured (32 heads over 8, D = 128, bf16): a prompt of 4096 tokens 165 us, 835
+// Measured (32 heads over 8, D = 128, bf16): a prompt of 4096 tokens 163 us, 846
 // TFLOP/s; five chunks of 700 tokens behind 3000 others with a window of 1000,
-// 110 us.  128 rows a workgroup, two of them a CU, a barrier every 64 tokens:
+// 105 us.  128 rows a workgroup, two of them a CU, a barrier every 64 tokens:
 // 225 and 125.  One wave a SIMD with 64 rows: over 600 (the sums alone are 128
 // registers, and queries spill).  The two waves of a SIMD made to take turns
 // between products and scores by barriers: 223 and 175 (a wave alone issues a
@@ -393,7 +393,10 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             asm("" : "+v"(pf[c / 4][2 * (c % 4)]), "+v"(pf[c / 4][2 * (c % 4) + 1]));
         };
         // The reference: no product of p (a lane's sum bounds it) with a scale of
-        // the tile may pass 2^15; raised, the largest p times the largest scale is 2^9.
+        // the tile may pass 2^15; raised, the largest p times the largest scale is
+        // 2^5, which leaves normal fp16 numbers down to 2^-19 of it and an
+        // absolute 2^-30 of it below.  (2^9, and a window's rows raise theirs so
+        // often that the five chunks named above take 130 us.)
         const f32x4 tops = lds_get<f32x4>(lds0 + Lds::kTop + Lds::slot(tile) * 16);
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         auto all_numerators = [&](bool masked) {
@@ -412,7 +415,8 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             all_numerators(false);
         else
             all_numerators(true);
-        if (__builtin_amdgcn_ballot_w64(!(sum * top <= kMaxP && sum <= kMaxSum)) != 0) {
+        const bool raise = !(sum * top <= kMaxP && sum <= kMaxSum);
+        if (__builtin_amdgcn_ballot_w64(raise) != 0) {
             products(tile - 1, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{}, nothing);
             float m = kNoRef;
 #pragma unroll
@@ -426,7 +430,10 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
                 }
                 chunk_end();
             }
-            m = fmaxf(ref, pair_max(m) - fminf(9.0f - __builtin_amdgcn_logf(top), 90.0f));
+            // (rows that need not stay as they are, so that no row's result depends on another's)
+            const bool either = pair_max(raise ? 1.0f : 0.0f) != 0.0f;
+            m = fmaxf(ref, pair_max(m) - fminf(5.0f - __builtin_amdgcn_logf(top), 90.0f));
+            m = either ? m : ref;
             const float f = __builtin_amdgcn_exp2f(ref - m);
             ref = m;
             l *= f;
@@ -513,60 +520,12 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
         }
         return;
     }
-    // partial sums through the workspace; a second kernel, or the last workgroup
-    // of the tile to arrive, adds them in order, writes and clears
-    const size_t tile_at = (size_t)ct * (g.B * g.Hkv) + bh;
-    float *part = g.partials + tile_at * g.splits * (size_t)(g.part_cols * ROW);
-    const auto rows_at = buf_rsrc(part, (int64_t)splits * g.part_cols * ROW * 4);
-    // this lane's quads of its row: + 8 dimensions each
-    auto at = [&](int s, int d) {
-        return (int)((uint32_t)((s * g.part_cols + 32 * wave + c32) * ROW + 4 * half + d) * 4);
-    };
-    auto put_part = [&](int to, f32x4 v) {
-        __builtin_amdgcn_raw_buffer_store_b128(bit_as<u32x4>(v), rows_at, to, 0, kPartCoherent);
-    };
-    auto get_part = [&](int from) {
-        return bit_as<f32x4>(__builtin_amdgcn_raw_buffer_load_b128(rows_at, from, 0, kPartCoherent));
-    };
-    const int ref_at = D - 4 * half;  // (past the sums, for either half of the lanes)
-    if (live) {
-#pragma unroll
-        for (int q = 0; q < 4 * DTL; ++q) put_part(at(split, 8 * q), quad(q));
-        if (half == 0) put_part(at(split, ref_at), (f32x4){ref, l, 0, 0});
-    }
-    if (g.apart || !split_tile_last_atomic(g.counters + tile_at, splits)) return;
+    // partial sums through the workspace, which a second kernel adds
     if (!live) return;
-    float rr = kNoRef, ll = 0.0f;
+    float *part = g.partials + ((((size_t)ct * (g.B * g.Hkv) + bh) * g.splits + split) * g.part_cols + 32 * wave + c32) * ROW;
 #pragma unroll
-    for (int i = 0; i < DTL; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-#pragma unroll 1
-    for (int s = 0; s < splits; ++s) {
-        const f32x4 rl = get_part(at(s, ref_at));
-        f32x4 w[4 * DTL];
-#pragma unroll
-        for (int q = 0; q < 4 * DTL; ++q) w[q] = get_part(at(s, 8 * q));
-        const float most = fmaxf(rr, rl[0]);
-        const float old = __builtin_amdgcn_exp2f(rr - most), f = __builtin_amdgcn_exp2f(rl[0] - most);
-        rr = most;
-        ll = ll * old + f * rl[1];
-#pragma unroll
-        for (int q = 0; q < 4 * DTL; ++q) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int e = 4 * (q % 4) + r;
-                o[q / 4][e] = __builtin_fmaf(f, w[q][r], o[q / 4][e] * old);
-            }
-            put_part(at(s, 8 * q), (f32x4){0, 0, 0, 0});
-        }
-    }
-    const float inv = inverse(ll);
-#pragma unroll
-    for (int q = 0; q < 4 * DTL; ++q) put(row_at, 8 * q + 4 * half, quad(q) * inv);
-    // (both lanes of a row have read its references by now: they run together)
-    if (half == 0)
-        for (int s = 0; s < splits; ++s) put_part(at(s, ref_at), (f32x4){0, 0, 0, 0});
+    for (int q = 0; q < 4 * DTL; ++q) *(f32x4 *)(part + 8 * q + 4 * half) = quad(q);
+    if (half == 0) *(f32x4 *)(part + D) = (f32x4){ref, l, 0, 0};
 }
 
 template <int DT, int D>

@@ -195,13 +195,11 @@ struct Kv4AttnArgs {
     int B, total_q, max_q, Hq, Hkv, D, P, table_stride, window, dtype;
     float scale;
     // the plan
-    int kind;       // kernel: 0 at most four rows, 1 and 2 tiles of 16 and 32 rows, 3 the prefill kernel (128 rows)
+    int kind;       // kernel: 0 at most four rows, 1 and 2 tiles of 16 and 32 rows, 3 the prefill kernel (256 rows)
     int col_tiles;  // workgroups along the query rows of a sequence and key/value head
     int splits;     // most workgroups along a sequence's tokens
-    int chunk;      // steps (64 tokens; kinds 1, 2: 32) that a workgroup takes
+    int chunk;      // steps (64 tokens; kinds 1, 2: 32, kind 3: 128) that a workgroup takes
     int part_cols;  // query rows of a tile that the partial sums hold
-    int apart;      // the workgroups' sums are added by a second kernel, not by the last of them
-    uint32_t *counters;
     float *partials;
 };
 constexpr int kKv4MaxSplits = 128;

@@ -510,9 +510,10 @@ int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride
  *            the workspace, no result depends on it being close.
  * Numerics: the codes enter the matrix cores exactly; scores, running maxima,
  * sums and outputs are fp32; the softmax numerators times the values' scales
- * are rounded once to 11 bits for the second product; out is rounded to
- * nearest even.  A NaN or infinity in q, or a NaN scale in a token that a row
- * sees, makes that row NaN; nothing that no row sees is used.
+ * are rounded once to 11 bits for the second product (those below 2^-19 of a
+ * row's largest to 2^-30 of it); out is rounded to nearest even.  A NaN or
+ * infinity in q, or a NaN scale in a token that a row sees, makes that row NaN;
+ * nothing that a row does not see changes it by more than its rounding.
  * Workspace: as for the GEMMs (shared, zero before and after each call).
  * B == 0 or total_q == 0 is a no-op that returns AWQ_OK.
  * Errors: AWQ_EINVAL (also scale <= 0), AWQ_EUNSUPPORTED (head_dim,
