@@ -14,7 +14,9 @@
 //
 // Bound: device memory.  A row is read once (x, r, w), held in registers as h
 // and then y, and written once (h, codes, s1, y if asked for): 7 bytes a value
-// with the residual against 13 in two launches (norm, then quantiser).
+// with the residual against 13 in two launches (norm, then quantiser).  4096
+// rows of 4096 values, fp16, int8 codes: 21.5 us, 5.5 TB/s.  One row takes 2.6 us:
+// a memory round trip and two sums over the workgroup.
 #include "device.hpp"
 #include "launch.hpp"
 #include "quant_ops.hpp"
@@ -260,13 +262,18 @@ static hipError_t launch_rows(const NormArgs &n, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Threads for a row: 8 values each up to 512 threads, then two chunks each up
+// to 8192 values, then 1024 threads (bf16, fp8 codes, residual: 777 rows of 8192
+// in 512 threads 14.7 us, in 1024 15.4, in 256 14.1; of 5120, int8, 10.4, 13.1,
+// 10.1; 4096 rows of 4096, fp16, int8: 512 threads 21.5, 256 22.8; 2048 rows of
+// 14336, fp8: 1024 threads 44, 512 49, 256 49).
 template <int DT, int OUT>
 static hipError_t launch_norm(const NormArgs &n, hipStream_t st) {
     if (n.K % 8 == 0 && n.K <= 8 * 1024 * 4) {
         if (n.K <= 8 * 128) return launch_rows<DT, OUT, 1, 128>(n, st);
         if (n.K <= 8 * 256) return launch_rows<DT, OUT, 1, 256>(n, st);
         if (n.K <= 8 * 512) return launch_rows<DT, OUT, 1, 512>(n, st);
-        if (n.K <= 8 * 1024) return launch_rows<DT, OUT, 1, 1024>(n, st);
+        if (n.K <= 8 * 1024) return launch_rows<DT, OUT, 2, 512>(n, st);
         if (n.K <= 8 * 1024 * 2) return launch_rows<DT, OUT, 2, 1024>(n, st);
         return launch_rows<DT, OUT, 4, 1024>(n, st);
     }

@@ -507,7 +507,7 @@ int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride
  *   max_q:   the most new tokens of a sequence (the rows of a sequence past
  *            its first max_q are not written).
  *   max_kv:  the longest sequence, or an upper bound: it sizes the launch and
- *            the workspace, no result depends on it being close.
+ *            the workspace, results depend on it by their rounding only.
  * Numerics: the codes enter the matrix cores exactly; scores, running maxima,
  * sums and outputs are fp32; the softmax numerators times the values' scales
  * are rounded once to 11 bits for the second product (those below 2^-19 of a
