@@ -21,9 +21,12 @@
 // bits, whatever the scales' magnitude.  Most steps find nothing to raise and
 // need no exchange between lanes.  The sum of z' takes the rounded P, so that
 // a code and its zero point lose the same, and it is taken off step by step:
-// codes average 7.5, and the sums of long contexts would otherwise lose what
-// is left after 7.5 has gone (131072 tokens: 8.4e-4 of the output against
-// 2.5e-4, the two roundings to 11 bits).  It costs matrix-core time only.
+// codes average 7.5, and of the sums of long contexts little is left after 7.5
+// has gone.  For the same reason it shows that the matrix cores drop the bits
+// of a product far below the largest of its sum, always downwards: every other
+// wave sums negated probabilities, whose loss is upwards.  (Error of the output
+// for 131072 tokens, its own rounding to 11 bits 2.0e-4: zero points taken off
+// at the end 8.4e-4, step by step 5.6e-4, with half the waves negated 2.3e-4.)
 // Queries are scaled by a power of two to just below 2^15 before they become
 // fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest.
 //
@@ -159,6 +162,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
     }
 
     f32x4 o[NT][VM];
+    // (odd waves sum negated probabilities: see above)
+    const uint32_t odd = wave & 1 ? 0x80008000u : 0u;
     float ref[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -261,8 +266,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
                 numerators();
             }
             l[n] += sum;
-            pf[n] = (u32x4){pack_f16(w[0][0], w[0][1]), pack_f16(w[0][2], w[0][3]), pack_f16(w[1][0], w[1][1]),
-                            pack_f16(w[1][2], w[1][3])};
+            pf[n] = (u32x4){pack_f16(w[0][0], w[0][1]) ^ odd, pack_f16(w[0][2], w[0][3]) ^ odd,
+                            pack_f16(w[1][0], w[1][1]) ^ odd, pack_f16(w[1][2], w[1][3]) ^ odd};
         }
         __builtin_amdgcn_sched_barrier(0);
         // the values' zero points as an operand with equal rows, negative, for
@@ -321,7 +326,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
 #pragma unroll
         for (int t = 0; t < VM; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) mine[value_dim<D>(t, 4 * grp + r)] = o[n][t][r] * value_unit<D>(t);
+            for (int r = 0; r < 4; ++r) mine[value_dim<D>(t, 4 * grp + r)] = o[n][t][r] * (odd ? -value_unit<D>(t) : value_unit<D>(t));
         if (grp == 0) {
             mine[D] = ref[n];
             mine[D + 1] = lsum;

@@ -159,6 +159,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
     for (int i = 0; i < 4; ++i) mine[i] = run == i ? 0xFFFFFFFFu : 0u;
 
     f32x4 o[VM];
+    // (odd waves sum negated probabilities: see kv4_attention.hip)
+    const uint32_t odd = wave & 1 ? 0x80008000u : 0u;
     float ref = kNoRef, l = 0.0f;
 #pragma unroll
     for (int t = 0; t < VM; ++t) o[t] = (f32x4){0, 0, 0, 0};
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
             numerators();
         }
         l += sum;
-        const uint32_t p01 = pack_f16(w[0], w[1]), p23 = pack_f16(w[2], w[3]);
+        const uint32_t p01 = pack_f16(w[0], w[1]) ^ odd, p23 = pack_f16(w[2], w[3]) ^ odd;
         const uint32_t z01 = perm_b32(s.vm[1], s.vm[0], 0x07060302u), z23 = perm_b32(s.vm[3], s.vm[2], 0x07060302u);
         __builtin_amdgcn_sched_barrier(0);
         // runs 0 and 1, then 2 and 3
@@ -297,7 +299,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
 #pragma unroll
     for (int t = 0; t < VM; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) part[value_dim<D>(t, 4 * grp + r)] = o[t][r] * value_unit<D>(t);
+        for (int r = 0; r < 4; ++r) part[value_dim<D>(t, 4 * grp + r)] = o[t][r] * (odd ? -value_unit<D>(t) : value_unit<D>(t));
     if (grp == 0) {
         part[D] = ref;
         part[D + 1] = lsum;
