@@ -626,8 +626,13 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
     p.col_tiles = cdiv(rows, tile_rows[p.kind]);
     p.part_cols = (int)std::min<int64_t>(rows, tile_rows[p.kind]);
     p.tiles = B * Hkv * p.col_tiles;
-    // workgroups to fill the device, each with `least` steps at least: of the
-    // prefill kernel one goes to a CU, so no more than CUs; of the others two at least
+    // Workgroups to fill the device, each with `least` steps at least.  Of the
+    // prefill kernel one goes to a CU, so no more than CUs (24 tiles, 10 splits
+    // against 11: 87 -> 70 us); of the others two a CU or a few more (one / two /
+    // three: two sequences of 131072 tokens 65 / 56 / 57 us, 64 of 4096 to 8192
+    // 84 / 84 / 92, 16 of 2050 with 32 heads 27 / 27 / 33).  `least` halved: 137
+    // tokens 9.0 us instead of 6.6, for the second launch; doubled: one sequence of
+    // 4096 11.9 instead of 11.2.
     const int64_t steps = std::max<int64_t>(1, cdiv(max_kv, step[p.kind]));
     const int64_t least[] = {4, 8, 8, 2};
     const int64_t fill = p.kind == 3 ? std::max<int64_t>(1, d.cus / p.tiles) : cdiv(2 * (int64_t)d.cus, p.tiles);

@@ -28,10 +28,13 @@ namespace awq4 {
 
 typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 
-// The quotient of two fp32 numbers, correctly rounded, from r = RN(1 / s):
-// q0 = RN(x r) is off by at most one unit, its remainder is exact in one FMA,
-// and q0 + e r rounds to RN(x / s) (Markstein).  s in the normal range, and
-// far enough from its ends that neither e nor q0 leaves it.
+// x / s correctly rounded to fp32, from r = RN(1 / s), for x and s of at most
+// 11 bits (16-bit types): q0 = RN(x r) is off by less than two units, its
+// remainder e is exact in one FMA (a multiple of a unit times s's last bit, of
+// 13 bits at most), and q0 + e r is off by 2^-22 of a unit before its rounding,
+// where x / s is never nearer than 2^-12 of one to a boundary between two
+// results.  s in the normal range, and far enough from its ends that neither e
+// nor q0 leaves it.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
     const float q0 = x * r;
     return __builtin_fmaf(__builtin_fmaf(-q0, s, x), r, q0);
