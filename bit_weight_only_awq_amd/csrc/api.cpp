@@ -611,7 +611,8 @@ struct Kv4Plan {
 //    of 128 tokens 10 us, in tiles of 16 rows 7.
 static int kv4_kind(int64_t rows, int64_t heads, int64_t max_kv, int64_t cus) {
     if (rows <= 4) return 0;
-    if (rows > 128 && heads * cdiv(rows, 256) * cdiv(max_kv, 128) >= 4 * cus) return 3;
+    const int64_t tiles = heads * cdiv(rows, 256);  // (a product of all three may pass 64 bits)
+    if (rows > 128 && (tiles >= 4 * cus || tiles * cdiv(max_kv, 128) >= 4 * cus)) return 3;
     return heads * cdiv(rows, 32) >= 2 * cus ? 2 : 1;
 }
 // How an attention call is launched (pure function of the shape; the lengths

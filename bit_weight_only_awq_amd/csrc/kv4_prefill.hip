@@ -454,7 +454,9 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
 #pragma unroll
             for (int i = 0; i < 4; ++i) all[i] = entry(kPreTile * tile + 16 * i);
         };
-        entries(2 * t_begin);
+        // (the first and the last tile may hold nothing that a row sees)
+        const int first = 2 * t_begin + (kPreTile * (2 * t_begin + 1) <= kv_lo);
+        entries(first);
         PreKeys<D> keys;
         PreValues values;
         auto unpack_meta = [&](int step) {
@@ -487,10 +489,13 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
         own1 = own2;
         own2 = own(t_begin + 2);
         __syncthreads();
-        products(2 * t_begin - 1, C4{}, C8{}, nothing);
+        products(first - 1, C4{}, C8{}, nothing);
         for (int step = t_begin; step < t_end; ++step) {
-            softmax(2 * step);
-            products(2 * step, C0{}, C8{}, nothing);
+            if (2 * step >= first) {
+                softmax(2 * step);
+                products(2 * step, C0{}, C8{}, nothing);
+            }
+            if (step + 1 == t_end) break;
             softmax(2 * step + 1);
             unpack_meta(step + 1);
             products(2 * step + 1, C0{}, C4{}, [&](auto n) { unpack_piece(step + 1, n); });
@@ -500,6 +505,10 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             own2 = own(step + 3);
             __syncthreads();
             products(2 * step + 1, C4{}, C8{}, nothing);
+        }
+        if (kPreTile * (2 * t_end - 1) < kv_hi) {
+            softmax(2 * t_end - 1);
+            products(2 * t_end - 1, C0{}, C4{}, nothing);
         }
     }
 
