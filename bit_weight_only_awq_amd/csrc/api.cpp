@@ -603,7 +603,7 @@ struct Kv4Plan {
 //    tiles of 16 rows 89.
 //  - the prefill kernel where every CU gets four of its steps or more and a tile
 //    more than half its rows: 16 x 192 rows over 4096 tokens 88 us, tiles of 16
-//    and 32 rows 110 and 104; four prompts of 512 tokens 32, 44 and 51.  Less
+//    and 32 rows 110 and 104; four prompts of 512 tokens 28, 44 and 51.  Less
 //    work leaves it waiting: 256 rows of one sequence over 8192 tokens 40 us
 //    against 35 and 32, four times 256 over 1024 27 against 18 and 25; 16 x 128
 //    rows over 4096 tokens 84 against 85 and 65.
