@@ -27,7 +27,8 @@ namespace awq4 {
 // non-temporal: a decode step reads a layer's cache once, and the next step
 // comes after all the other layers' (64 x 4096-8192 tokens 94 -> 85 us, 2 x
 // 131072 63 -> 56 us; caches small enough to stay in the memory-side cache
-// from call to call read up to 8 % slower).
+// from call to call read up to 8 % slower).  Policy 0 for prompts, whose
+// workgroups read the same words one after another.
 constexpr int kStreamOnce = 2;
 template <typename T, int POLICY = kStreamOnce>
 __device__ __forceinline__ T buf_get(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t scalar) {
