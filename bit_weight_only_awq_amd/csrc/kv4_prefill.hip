@@ -64,15 +64,17 @@ __device__ __forceinline__ float pair_sum(float v) {
 
 // LDS, in bytes: for each of four tiles (two steps) keys [64][D] and values
 // [D][64] as 16-bit integers, the keys' scales times scale log2(e), the values'
-// scales, and the largest of those in each run of 16 tokens.  Rows are 128 or
-// 256 bytes, so their 16-byte chunks are permuted by the row's number:
+// scales, the logarithms of those as a reference takes them, and the largest
+// scale of each run of 16 tokens.  Rows are 128 or 256 bytes, so their 16-byte
+// chunks are permuted by the row's number:
 // the lanes that an access serves at once read rows one apart and write rows
 // one or eight apart.  Chunk c of row r is at row(r) ^ (c << 4): one
 // instruction from a per-lane base.
 template <int D>
 struct PreLds {
     static constexpr uint32_t kSlots = 2 * kPreStep / kPreTile, kTile = 2 * kPreTile * D, kK = 0, kV = kSlots * kTile,
-                              kKs = 2 * kV, kVs = kKs + 4 * kSlots * kPreTile, kTop = kVs + 4 * kSlots * kPreTile,
+                              kKs = 2 * kV, kVs = kKs + 4 * kSlots * kPreTile, kTo = kVs + 4 * kSlots * kPreTile,
+                              kTop = kTo + 4 * kSlots * kPreTile,
                               kBytes = kTop + 16 * kSlots;
     __device__ static uint32_t slot(int tile) { return (uint32_t)tile & (kSlots - 1); }
     __device__ static uint32_t mix(uint32_t r) { return (r ^ (r >> 3)) & 7; }
@@ -206,8 +208,10 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             // that do not see the token clear the score's exponential, and 0
             // times the scale would bring it back
             const float vs = act_bits_to_f32<DT>(r.vm & 0xFFFFu);
-            lds_put(lds0 + Lds::kKs + Lds::slot(tile) * (4 * kPreTile) + 4 * (16 * run + kt),
-                    vs - vs == 0.0f ? act_bits_to_f32<DT>(r.km & 0xFFFFu) * score_scale : vs - vs);
+            const uint32_t to = lds0 + Lds::slot(tile) * (4 * kPreTile) + 4 * (16 * run + kt);
+            lds_put(to + Lds::kKs, vs - vs == 0.0f ? act_bits_to_f32<DT>(r.km & 0xFFFFu) * score_scale : vs - vs);
+            // (2^-90: a p stays in range itself beside scales of next to nothing)
+            lds_put(to + Lds::kTo, fmaxf(__builtin_amdgcn_logf(fabsf(vs)) - 5.0f, -90.0f));
         }
         r.km = (r.km >> 16) & 15u;  // the zero point from here on
     };
@@ -354,7 +358,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
     auto exponentials = [&](int tile, const bool (&there)[4], bool plain) {
         const int t0 = kPreTile * tile;
         uint32_t ks_from = lds0 + Lds::kKs + Lds::slot(tile) * (4 * kPreTile) + 16 * half;
-        constexpr uint32_t kVs = Lds::kVs - Lds::kKs;
+        constexpr uint32_t kVs = Lds::kVs - Lds::kKs, kTo = Lds::kTo - Lds::kKs;
         asm("" : "+v"(ks_from));  // (so that the reads' offsets stay constants)
         float sum;
         // Chunk c = 4 u + a has the tokens 32 u + 8 a + 4 half + r of the tile, in
@@ -392,11 +396,15 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             // (packed here, not where the branches join: 16 registers less)
             asm("" : "+v"(pf[c / 4][2 * (c % 4)]), "+v"(pf[c / 4][2 * (c % 4) + 1]));
         };
-        // The reference: no product of p (a lane's sum bounds it) with a scale of
-        // the tile may pass 2^15; raised, the largest p times the largest scale is
-        // 2^5, which leaves normal fp16 numbers down to 2^-19 of it and an
-        // absolute 2^-30 of it below.  (2^9, and a window's rows raise theirs so
-        // often that the five chunks named above take 130 us.)
+        // The reference: no product of p with its token's scale may pass 2^15;
+        // raised, the row's largest is 2^5, which leaves normal fp16 numbers down to
+        // 2^-19 of it and an absolute 2^-30 of it below.  A lane's sum of p times the
+        // tile's largest scale bounds its products and costs two instructions.  That
+        // scale may be of a token that the row does not see, or gives next to no
+        // probability, so past the bound the products themselves decide, and the new
+        // reference is that of the tokens seen: nothing else costs the row bits.
+        // (Raised to 2^9 instead, a window's rows raise theirs so often that the five
+        // chunks named above take 130 us.)
         const f32x4 tops = lds_get<f32x4>(lds0 + Lds::kTop + Lds::slot(tile) * 16);
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         auto all_numerators = [&](bool masked) {
@@ -415,25 +423,36 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             all_numerators(false);
         else
             all_numerators(true);
-        const bool raise = !(sum * top <= kMaxP && sum <= kMaxSum);
+        bool raise = !(sum * top <= kMaxP && sum <= kMaxSum);
+        if (__builtin_amdgcn_ballot_w64(raise) != 0) {
+            // (fp16 magnitudes are in the order of their patterns.  From 0x6000, 2^9,
+            // not only past 2^15: a row whose sum passes the bound here does so again
+            // in the next tiles.)
+            typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 most = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                most = __builtin_elementwise_max(most, bit_as<u16x2>(pf[i / 8][i % 8] & 0x7FFF7FFFu));
+            raise = !(sum <= kMaxSum) || max(most[0], most[1]) > 0x6000;
+        }
         if (__builtin_amdgcn_ballot_w64(raise) != 0) {
             products(tile - 1, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{}, nothing);
             float m = kNoRef;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const f32x4 ks = lds_get<f32x4>(ks_from + 32 * c);
+                const f32x4 ks = lds_get<f32x4>(ks_from + 32 * c), to = lds_get<f32x4>(ks_from + kTo + 32 * c);
                 const int from = opaque(at);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float y = x[c / 4][4 * (c % 4) + r] * ks[r];
-                    m = plain | seen(c, r, from) ? fmaxf(m, y) : m;
+                    const float y = __builtin_fmaf(x[c / 4][4 * (c % 4) + r], ks[r], to[r]);
+                    m = seen(c, r, from) ? fmaxf(m, y) : m;
                 }
                 chunk_end();
             }
             // (rows that need not stay as they are, so that no row's result depends on another's)
             const bool either = pair_max(raise ? 1.0f : 0.0f) != 0.0f;
-            m = fmaxf(ref, pair_max(m) - fminf(5.0f - __builtin_amdgcn_logf(top), 90.0f));
-            m = either ? m : ref;
+            m = pair_max(m);
+            m = either ? fmaxf(ref, m) : ref;
             const float f = __builtin_amdgcn_exp2f(ref - m);
             ref = m;
             l *= f;

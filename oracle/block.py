@@ -173,16 +173,13 @@ def page_values(cache, P: int, D: int, page: int, h: int, dtype: str):
 
 # ------------------------------------------------------------------ attention
 
-def attention(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
-    """(out, spread, unit): out [T, Hq, D] in binary64, and what an error bound needs: sum of p |v| (spread), and per row
-    (sum of p s', scale * largest s * sum |q|, largest s' of the sequence), from the words of the cache."""
+def _rows(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
+    """For every row of q that sees anything: (row, query head, the row's values, softmax weights of the tokens it sees,
+    their values, key scales and value scales)."""
     T, hq, D = q.shape
     pages, hkv, _ = cache.shape
     G = hq // hkv
     qv = decode(q, dtype)
-    out = np.zeros((T, hq, D))
-    spread = np.zeros((T, hq, D))
-    unit = np.zeros((T, hq, 3))
     for b in range(len(lens)):
         r0, r1 = int(cu_q[b]), int(cu_q[b + 1])
         n = r1 - r0
@@ -214,7 +211,23 @@ def attention(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, d
                     t = scale * (K[seen] @ row)
                     w = np.exp(t - t.max())
                     w /= w.sum()
-                    out[r0 + i, e] = w @ V[seen]
-                    spread[r0 + i, e] = w @ np.abs(V[seen])
-                    unit[r0 + i, e] = (w @ vs[seen], scale * ks[seen].max() * np.abs(row).sum(), np.nanmax(vs))
+                    yield r0 + i, e, row, w, V[seen], ks[seen], vs[seen]
+
+
+def attention(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
+    """(out, spread, unit): out [T, Hq, D] in binary64, and what an error bound needs: sum of p |v| (spread), and per row
+    (sum of p s', scale * largest |s| * sum |q|, largest s') over the tokens that it sees, from the words of the cache."""
+    out, spread, unit = np.zeros(q.shape), np.zeros(q.shape), np.zeros((*q.shape[:2], 3))
+    for r, e, row, w, V, ks, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
+        out[r, e] = w @ V
+        spread[r, e] = w @ np.abs(V)
+        unit[r, e] = (w @ vs, scale * np.abs(ks).max() * np.abs(row).sum(), np.nanmax(vs))
     return out, spread, unit
+
+
+def products(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
+    """[T, Hq, 3]: over the tokens that a row sees, the largest p |s'|, their number, and the sum of p |s'|."""
+    top = np.zeros((*q.shape[:2], 3))
+    for r, e, _, w, _, _, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
+        top[r, e] = (w * np.abs(vs)).max(), len(w), w @ np.abs(vs)
+    return top
