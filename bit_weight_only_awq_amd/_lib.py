@@ -76,6 +76,8 @@ def lib() -> ctypes.CDLL:
     L.w4a8_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
     L.awq_stream_read.argtypes = [vp, i64, vp, vp]
     L.awq_plan_info.argtypes = [i32, i64, i64, i64, i32, i32, i32, ctypes.POINTER(PlanInfo)]
+    L.awq_stream_capture_id.argtypes = [vp, ctypes.POINTER(ctypes.c_uint64)]
+    L.awq_stream_capture_id.restype = i32
     f32 = ctypes.c_float
     L.w4a8_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
     L.w4a8_fp8_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]

@@ -739,6 +739,17 @@ size_t awq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int group_si
     return 0;
 }
 
+int awq_stream_capture_id(void *stream, uint64_t *id) {
+    if (!id) return AWQ_EINVAL;
+    *id = 0;
+    if (!stream) return AWQ_OK;  // (the null stream cannot be captured)
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    unsigned long long number = 0;
+    const hipError_t e = hipStreamGetCaptureInfo(static_cast<hipStream_t>(stream), &status, &number);
+    if (e == hipSuccess && status != hipStreamCaptureStatusNone) *id = number;
+    return hip_status(e);
+}
+
 int awq_plan_info(int op, int64_t M, int64_t N, int64_t K, int group_size, int split_k, int cu_count,
                   awq_plan_t *out) {
     if (!out || cu_count < 0) return AWQ_EINVAL;

@@ -41,39 +41,73 @@ def _need_cuda(*ts):
 
 # ----------------------------------------------------------------------------- workspace
 
+def _zeros(index: int, nbytes: int) -> torch.Tensor:
+    """Zero bytes on device `index`, filled on its current stream."""
+    return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+
+
+def _capture_id(stream: int) -> int:
+    """Number of the graph capture that `stream` is recording, 0 if none."""
+    number = ctypes.c_uint64()
+    L.check("awq_stream_capture_id", L.lib().awq_stream_capture_id(stream, ctypes.byref(number)))
+    return number.value
+
+
 class Workspace:
     """One zero-initialised workspace per (device, stream), grown on demand and
     shared by every call ordered on that stream (the library leaves its
     counters zero after each call).  Calls on different streams may overlap in
-    time, so each stream gets its own buffer; a grown buffer is zero-filled on
-    the stream that will use it, and the caching allocator keeps the old one
-    alive until the work queued on that stream before the swap has run."""
+    time, so each stream gets its own buffer, zero-filled on that stream.  A
+    buffer that has been replaced by a larger one is kept, since a graph
+    captured earlier may hold its address (sizes at least double, so the kept
+    ones together are smaller than the current one).
+
+    A call that is being recorded into a graph takes the stream's buffer where
+    it is large enough.  Where it is not, the capture gets one of its own, from
+    the graph's memory and with its zero-fill recorded: that one is zero in
+    replays of this graph only, so no eager call and no other capture takes
+    it."""
 
     def __init__(self):
         self._bufs: dict[tuple[int, int], torch.Tensor] = {}
+        self._kept: list[torch.Tensor] = []
+        self._recorded: dict[tuple[int, int], tuple[int, torch.Tensor]] = {}  # (capture, its buffer)
         self._lock = threading.Lock()
 
     def get(self, device: torch.device, nbytes: int) -> torch.Tensor | None:
         if nbytes == 0:
             return None
         idx = device.index if device.index is not None else torch.cuda.current_device()
-        stream = torch.cuda.current_stream(idx)
-        key = (idx, stream.cuda_stream)
-        with self._lock:
-            buf = self._bufs.get(key)
-            if buf is None or buf.numel() < nbytes:
-                size = max(nbytes, 2 * (buf.numel() if buf is not None else 0), 1 << 20)
-                with torch.cuda.stream(stream):
-                    buf = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", idx))
-                self._bufs[key] = buf
-            return buf
+        return self._buffer(idx, _raw_stream(idx), nbytes)
 
     def of_stream(self, index: int, stream: int, nbytes: int):
         """(pointer, bytes) of the workspace of `stream`, the current stream of device `index`, at least nbytes."""
         buf = self._bufs.get((index, stream))
         if buf is None or buf.numel() < nbytes:
-            buf = self.get(torch.device("cuda", index), nbytes)
+            buf = self._buffer(index, stream, nbytes)
         return buf.data_ptr(), buf.numel()
+
+    def _buffer(self, index: int, stream: int, nbytes: int) -> torch.Tensor:
+        key = (index, stream)
+        with self._lock:
+            buf = self._bufs.get(key)
+            if buf is not None and buf.numel() >= nbytes:
+                return buf
+            capture = _capture_id(stream)
+            if capture:
+                number, buf = self._recorded.get(key, (0, None))
+                if number != capture:
+                    buf = None
+                elif buf.numel() >= nbytes:
+                    return buf
+            elif buf is not None:
+                self._kept.append(buf)
+            buf = _zeros(index, max(nbytes, 2 * (buf.numel() if buf is not None else 0), 1 << 20))
+            if capture:
+                self._recorded[key] = (capture, buf)
+            else:
+                self._bufs[key] = buf
+            return buf
 
 
 WORKSPACE = Workspace()

@@ -157,10 +157,20 @@ int awq_repack_v2(const int32_t *qweight_v2, const int32_t *qzeros_v2, int32_t *
  *  - either way the workspace is zero again after every call;
  *  - it must be zero-filled once when allocated; no per-call clearing is
  *    needed;
- *  - calls that overlap in time (different streams) need separate workspaces.
+ *  - calls that overlap in time (different streams) need separate workspaces;
+ *  - a captured graph holds its calls' workspace: it has to live as long as the
+ *    graph, and a zero-fill that is only recorded has not happened before the
+ *    graph's first replay.
  * Returns 0 for invalid arguments.
  */
 size_t awq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int group_size, int split_k);
+
+/*
+ * awq_stream_capture_id -- for callers that keep workspaces: *id is the number
+ * of the graph capture that `stream` is recording, different for every
+ * capture, or 0 if it records none.  Errors: AWQ_EINVAL (id NULL), AWQ_EHIP.
+ */
+int awq_stream_capture_id(void *stream, uint64_t *id);
 
 /*
  * awq_plan_info -- how a call would be launched, without launching it: the

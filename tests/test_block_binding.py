@@ -1,0 +1,73 @@
+"""The torch binding's own parts, without a GPU: workspaces and strides."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+from bit_weight_only_awq_amd import _lib as L
+from bit_weight_only_awq_amd import ops
+
+
+@pytest.fixture
+def space(monkeypatch):
+    """A Workspace whose memory is the host's, and the number of the capture under way (0: none)."""
+    capture = [0]
+    monkeypatch.setattr(ops, "_zeros", lambda index, nbytes: torch.zeros(nbytes, dtype=torch.uint8))
+    monkeypatch.setattr(ops, "_capture_id", lambda stream: capture[0])
+    return ops.Workspace(), capture
+
+
+MB = 1 << 20
+
+
+def test_workspace_is_shared_by_a_streams_calls(space):
+    ws, _ = space
+    a = ws.of_stream(0, 7, 100)
+    assert a == ws.of_stream(0, 7, MB) and a[1] == MB
+    assert ws.of_stream(0, 8, 100)[0] != a[0] and ws.of_stream(1, 7, 100)[0] != a[0]
+
+
+def test_replaced_workspace_stays_alive(space):
+    """A graph that was captured with it still writes there."""
+    ws, _ = space
+    first = ws._buffer(0, 7, 100)
+    ref, at = weakref.ref(first), first.data_ptr()
+    del first
+    sizes = [ws.of_stream(0, 7, n)[1] for n in (MB + 1, 2 * MB + 1, 30 * MB, 30 * MB + 1)]
+    assert sizes == [2 * MB, 4 * MB, 30 * MB, 60 * MB]
+    gc.collect()
+    assert ref() is not None and ref().data_ptr() == at
+    assert sum(t.numel() for t in ws._kept) < sizes[-1]
+
+
+def test_capture_takes_the_streams_workspace(space):
+    ws, capture = space
+    a = ws.of_stream(0, 7, 100)
+    capture[0] = 5
+    assert ws.of_stream(0, 7, MB) == a
+
+
+@pytest.mark.parametrize("eager_first", [False, True])
+def test_memory_zeroed_in_a_capture_stays_in_it(space, eager_first):
+    """Its zero-fill runs when the graph does, so nothing else may rely on it."""
+    ws, capture = space
+    get = lambda n: ws._buffer(0, 7, n)  # noqa: E731
+    eager = get(100) if eager_first else None
+    capture[0] = 5
+    recorded = get(3 * MB)
+    assert recorded is not eager and get(2 * MB) is recorded  # one fill a capture
+    grown = get(4 * MB)
+    assert grown.numel() == 6 * MB and get(3 * MB) is grown
+    capture[0] = 6
+    other = get(3 * MB)
+    assert other is not grown
+    capture[0] = 0
+    after = get(100)
+    assert after is eager if eager_first else not any(after is t for t in (recorded, grown, other))
+    assert not any(get(3 * MB) is t for t in (recorded, grown, other))
+
+
+def test_capture_id_refuses():
+    assert L.lib().awq_stream_capture_id(None, None) == L.AWQ_EINVAL
+    assert ops._capture_id(0) == 0
