@@ -514,12 +514,14 @@ def kv4_append(q, k, v, rope, positions, slots, cache, interleaved: bool = False
     return out
 
 
-def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None, max_q: int = 1,
+def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None, max_q: int | None = None,
                   max_kv: int | None = None, window: int = 0, out=None):
     """Causal attention of q [total_q, Hq, D] over the paged 4-bit cache.
     tables int32 [B, pages of a sequence], lens int32 [B] (tokens with the new
-    ones); cu_q int32 [B + 1] and max_q where sequences have more than one new
-    token; max_kv: the longest sequence (default: what the tables can hold);
+    ones); cu_q int32 [B + 1] where sequences have more than one new token, and
+    max_q, the most that one has (default: all rows of q, which is right but
+    launches more than a tight bound; rows past a sequence's first max_q are not
+    written); max_kv: the longest sequence (default: what the tables can hold);
     scale: default 1 / sqrt(D)."""
     if not q.is_cuda:
         raise ValueError("all tensors must be on a CUDA (HIP) device")
@@ -538,6 +540,8 @@ def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None,
         out = torch.empty_like(q)
     elif out is not q:
         _tensor(out, shape, dt, dev, "out")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(total, 1)
     pages, hkv, _ = cache.shape
     width = tables.shape[1]
     if max_kv is None:
