@@ -7,10 +7,11 @@
 //   q = fl32(1 / fl32(sqrt(v)))
 //   y = act(fl32(fl32(h q) w))
 // then the codes and scales that the quantisers (w4a8.hip, w4a8_fp8.hip) give
-// of y, bit for bit.  Every rounding above is part of the definition.  The sum
-// of squares is taken in binary64: its error (2^-53 a term) does not reach v's
-// rounding to binary32, so y, and the codes with it, do not depend on the
-// order of the sum or on the launch's shape.
+// of y, bit for bit.  Every rounding above is part of the definition; only the
+// order in which the squares are summed is not.  It depends on K alone, so a
+// row's results are the same in every launch, and most sums' bits all fit in
+// binary64, so that no order matters: another's error (2^-53 an addition) changes
+// v's rounding to binary32 in fewer than one row of 10^6.
 //
 // Bound: device memory.  A row is read once (x, r, w), held in registers as h
 // and then y, and written once (h, codes, s1, y if asked for): 7 bytes a value
@@ -71,9 +72,11 @@ __device__ __forceinline__ uint32_t scale_act(uint32_t h, uint32_t w, float q) {
     return pair_act<DT>(act_bits_to_f32<DT>(h & 0xFFFFu) * q * act_bits_to_f32<DT>(w & 0xFFFFu),
                         act_bits_to_f32<DT>(h >> 16) * q * act_bits_to_f32<DT>(w >> 16));
 }
-// The row's factor from its sum of squares (inv_k = 1 / K).
-__device__ __forceinline__ float rms_factor(double sum, double inv_k, float eps) {
-    const float v = (float)(sum * inv_k + (double)eps);
+// The row's factor from its sum of squares.  A division, not a product with
+// 1 / K: its rounding error would reach v where the mean lies next to the middle
+// between two binary32 numbers.
+__device__ __forceinline__ float rms_factor(double sum, int K, float eps) {
+    const float v = (float)(sum / (double)K + (double)eps);
     return 1.0f / __builtin_sqrtf(v);
 }
 
@@ -86,7 +89,7 @@ template <int DT, int OUT, int NV, int T>
 __global__ __launch_bounds__(T) void rmsnorm_rows(const uint16_t *x, const uint16_t *r,
                                                   const uint16_t *__restrict__ w, uint16_t *h_out, uint16_t *y,
                                                   uint8_t *__restrict__ a, float *__restrict__ s1,
-                                                  float *__restrict__ asum, int K, double inv_k, float eps) {
+                                                  float *__restrict__ asum, int K, float eps) {
     constexpr int W = T / 64;
     __shared__ double wsum[W];
     __shared__ uint32_t wmax[W];
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(T) void rmsnorm_rows(const uint16_t *x, const uint1
     sum = wsum[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) sum += wsum[i];
-    const float q = rms_factor(sum, inv_k, eps);
+    const float q = rms_factor(sum, K, eps);
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(T) void rmsnorm_rows(const uint16_t *x, const uint1
 template <int DT, int OUT>
 __global__ __launch_bounds__(256) void rmsnorm_any(const uint16_t *x, const uint16_t *r, const uint16_t *w,
                                                    uint16_t *h_out, uint16_t *y, uint8_t *a, float *s1, float *asum,
-                                                   int K, double inv_k, float eps) {
+                                                   int K, float eps) {
     __shared__ double wsum[4];
     __shared__ uint32_t wmax[4];
     __shared__ long long wcode[4];
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(256) void rmsnorm_any(const uint16_t *x, const uint
     if (leader) wsum[wave] = sum;
     __syncthreads();
     sum = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
-    const float q = rms_factor(sum, inv_k, eps);
+    const float q = rms_factor(sum, K, eps);
     const uint16_t *h = r ? h_out : x;
     auto value = [&](int k) -> uint32_t {
         return one_act<DT>(act_bits_to_f32<DT>(h[at + k]) * q * act_bits_to_f32<DT>(w[k]));
@@ -258,7 +261,7 @@ template <int DT, int OUT, int NV, int T>
 static hipError_t launch_rows(const NormArgs &n, hipStream_t st) {
     hipLaunchKernelGGL((rmsnorm_rows<DT, OUT, NV, T>), dim3((unsigned)n.M), dim3(T), 0, st, (const uint16_t *)n.x,
                        (const uint16_t *)n.residual, (const uint16_t *)n.weight, (uint16_t *)n.residual_out,
-                       (uint16_t *)n.y, (uint8_t *)n.a, n.s1, n.asum, (int)n.K, 1.0 / (double)n.K, n.eps);
+                       (uint16_t *)n.y, (uint8_t *)n.a, n.s1, n.asum, (int)n.K, n.eps);
     return hipGetLastError();
 }
 
@@ -279,7 +282,7 @@ static hipError_t launch_norm(const NormArgs &n, hipStream_t st) {
     }
     hipLaunchKernelGGL((rmsnorm_any<DT, OUT>), dim3((unsigned)n.M), dim3(256), 0, st, (const uint16_t *)n.x,
                        (const uint16_t *)n.residual, (const uint16_t *)n.weight, (uint16_t *)n.residual_out,
-                       (uint16_t *)n.y, (uint8_t *)n.a, n.s1, n.asum, (int)n.K, 1.0 / (double)n.K, n.eps);
+                       (uint16_t *)n.y, (uint8_t *)n.a, n.s1, n.asum, (int)n.K, n.eps);
     return hipGetLastError();
 }
 

@@ -411,7 +411,8 @@ int w4a8_fp8_linear(const void *x, uint8_t *a, float *s1, float *asum, const int
  * w4a8_rmsnorm_quant -- residual addition, root-mean-square norm and per-token
  * int8 quantisation in one pass, the input of w4a8_gemm:
  *   h[m,k]  = act( fl32( x + residual ) )            (no residual: h = x)
- *   v[m]    = fl32( sum_k h^2 / K + eps )            (sum and quotient in binary64)
+ *   v[m]    = fl32( sum_k h^2 / K + eps )            (sum, in an order that K fixes, and
+ *                                                         quotient in binary64)
  *   q[m]    = fl32( 1 / fl32( sqrt(v) ) )
  *   y[m,k]  = act( fl32( fl32( h q ) weight[k] ) )
  *   s1, a8  = w4a8_quant_act of y
