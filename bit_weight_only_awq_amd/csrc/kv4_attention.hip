@@ -15,7 +15,7 @@
 // values' codes are exact in it) is the only one between q and the output's:
 //   p_j = 2^(t_j log2(e) - R),  P_j = fp16(p_j s'_j)
 //   O = (sum P_j c'_j - sum P_j z'_j) / sum p_j
-// The reference R of a row is raised when a P_j would pass 2^15 (or a p_j 2^100,
+// The reference R of a row is raised when a |P_j| would pass 2^15 (or a p_j 2^100,
 // for values whose scale is next to nothing), to put the largest at 2^11: P
 // then uses fp16's whole range, and one 2^-25 times the largest still has all 11
 // bits, whatever the scales' magnitude.  Most steps find nothing to raise and
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         sum += p[i][r];
-                        top = fmaxf(top, w[i][r]);
+                        top = fmaxf(top, fabsf(w[i][r]));
                     }
             };
             numerators();
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float y = x[n][i][r] * cf[n];
-                        const float c = fmaxf(y + __builtin_amdgcn_logf(vs[i][r]) - 11.0f, y - 90.0f);
+                        const float c = fmaxf(y + __builtin_amdgcn_logf(fabsf(vs[i][r])) - 11.0f, y - 90.0f);
                         t = plain || seen(i, r) ? fmaxf(t, c) : t;
                     }
                 t = column_max(t);

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
                 }
             }
             sum = (p[0] + p[1]) + (p[2] + p[3]);
-            top = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+            top = fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3])));
         };
         numerators();
         if (__builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0) {
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float y = x[r] * cf;
-                const float c = fmaxf(y + __builtin_amdgcn_logf(vs[r]) - 11.0f, y - 90.0f);
+                const float c = fmaxf(y + __builtin_amdgcn_logf(fabsf(vs[r])) - 11.0f, y - 90.0f);
                 t = plain || seen(r) ? fmaxf(t, c) : t;
             }
             t = column_max(t);

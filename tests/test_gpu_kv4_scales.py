@@ -116,3 +116,19 @@ def test_scales_that_rise_with_the_tokens(dtype, step):
         boost(c, 0, t, step * (t // 64))
     check(c, max_kv=LONG)
     check(c, window=70, max_kv=LONG)
+
+
+@pytest.mark.parametrize("new,max_kv", [(1, None), *NEW])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("which", ["values", "every third token"])
+def test_scales_below_zero(which, dtype, new, max_kv):
+    """(code - z) s holds for any s: a cache that something else has filled may have them."""
+    for D in (64, 128):
+        c = Case([320, 160], [new, min(new, 160)], 2, 1, D, 16, dtype, seed=D + new)
+        for b, n in enumerate(c.lens):
+            for t in range(0, n, 1 if which == "values" else 3):
+                page, at = slot_of(c, b, t)
+                c.cache[page, :, block.word_at("vm", 16, D, at)] ^= 0x8000
+                if which != "values":
+                    c.cache[page, :, block.word_at("km", 16, D, at)] ^= 0x8000
+        check(c, max_kv=max_kv)
