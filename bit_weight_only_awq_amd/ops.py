@@ -468,7 +468,7 @@ def _heads(t, shape, dtype, index, what):
     step, head, one = t.stride()
     if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{what} must have dense heads")
-    return step if T > 1 else max(step, H * D)
+    return step if T > 1 else H * D  # (a single token's stride says nothing)
 
 
 def kv4_append(q, k, v, rope, positions, slots, cache, interleaved: bool = False, out=None):

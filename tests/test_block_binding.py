@@ -71,3 +71,14 @@ def test_memory_zeroed_in_a_capture_stays_in_it(space, eager_first):
 def test_capture_id_refuses():
     assert L.lib().awq_stream_capture_id(None, None) == L.AWQ_EINVAL
     assert ops._capture_id(0) == 0
+
+
+def test_stride_of_a_single_token_says_nothing():
+    """One token out of rows whose length is odd, or far apart: the append takes it as dense."""
+    wide = torch.zeros(3, 2 * 64 + 1, dtype=torch.float16)
+    for t in (wide[:1, :128].view(1, 2, 64), torch.zeros(1, 2, 64, dtype=torch.float16).expand(1, 2, 64),
+              torch.as_strided(torch.zeros(128, dtype=torch.float16), (1, 2, 64), (1 << 40, 64, 1))):
+        assert ops._heads(t, torch.Size((1, 2, 64)), torch.float16, -1, "k") == 128
+    assert ops._heads(torch.zeros(0, 2, 64, dtype=torch.float16), torch.Size((0, 2, 64)), torch.float16, -1, "k") == 128
+    rows = torch.zeros(3, 200, dtype=torch.float16)
+    assert ops._heads(rows[:, :128].view(3, 2, 64), torch.Size((3, 2, 64)), torch.float16, -1, "k") == 200
