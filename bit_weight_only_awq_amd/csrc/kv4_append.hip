@@ -207,10 +207,27 @@ static hipError_t launch_append(const Kv4AppendArgs &g, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_kv4_append(const Kv4AppendArgs &g, hipStream_t st) {
+static hipError_t launch_part(const Kv4AppendArgs &g, hipStream_t st) {
     if (g.D == 128)
         return g.dtype == DT_BF16 ? launch_append<DT_BF16, 128>(g, st) : launch_append<DT_F16, 128>(g, st);
     return g.dtype == DT_BF16 ? launch_append<DT_BF16, 64>(g, st) : launch_append<DT_F16, 64>(g, st);
+}
+
+hipError_t launch_kv4_append(const Kv4AppendArgs &all, hipStream_t st) {
+    for (int64_t t = 0; t < all.T; t += kLaunchRows) {
+        auto tokens = [&](auto *p, int64_t bytes) { return p ? (decltype(p))((uintptr_t)p + t * bytes) : p; };
+        Kv4AppendArgs g = all;
+        g.T = all.T - t < kLaunchRows ? all.T - t : kLaunchRows;
+        g.q = tokens(all.q, 2 * all.q_stride);
+        g.k = tokens(all.k, 2 * all.k_stride);
+        g.v = tokens(all.v, 2 * all.v_stride);
+        g.positions = tokens(all.positions, 4);
+        g.slots = tokens(all.slots, 8);
+        g.q_out = tokens(all.q_out, (int64_t)2 * all.Hq * all.D);
+        const hipError_t e = launch_part(g, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace awq4

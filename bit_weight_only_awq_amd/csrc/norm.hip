@@ -292,8 +292,22 @@ static hipError_t launch_norm_dt(const NormArgs &n, hipStream_t st) {
     return n.asum ? launch_norm<DT, NORM_FP8>(n, st) : launch_norm<DT, NORM_INT8>(n, st);
 }
 
-hipError_t launch_rmsnorm(const NormArgs &n, hipStream_t st) {
-    return n.dtype == DT_BF16 ? launch_norm_dt<DT_BF16>(n, st) : launch_norm_dt<DT_F16>(n, st);
+hipError_t launch_rmsnorm(const NormArgs &all, hipStream_t st) {
+    for (int64_t m = 0; m < all.M; m += kLaunchRows) {
+        auto rows = [&](auto *p, int64_t bytes) { return p ? (decltype(p))((uintptr_t)p + m * bytes) : p; };
+        NormArgs n = all;
+        n.M = all.M - m < kLaunchRows ? all.M - m : kLaunchRows;
+        n.x = rows(all.x, 2 * all.K);
+        n.residual = rows(all.residual, 2 * all.K);
+        n.residual_out = rows(all.residual_out, 2 * all.K);
+        n.y = rows(all.y, 2 * all.K);
+        n.a = rows(all.a, all.K);
+        n.s1 = rows(all.s1, 4);
+        n.asum = rows(all.asum, 4);
+        const hipError_t e = n.dtype == DT_BF16 ? launch_norm_dt<DT_BF16>(n, st) : launch_norm_dt<DT_F16>(n, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace awq4

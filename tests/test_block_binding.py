@@ -1,4 +1,4 @@
-"""The torch binding's own parts, without a GPU: workspaces and strides."""
+"""The torch binding's own parts, without a GPU: workspaces and strides; launches past the runtime's limit."""
 import gc
 import weakref
 
@@ -82,3 +82,12 @@ def test_stride_of_a_single_token_says_nothing():
     assert ops._heads(torch.zeros(0, 2, 64, dtype=torch.float16), torch.Size((0, 2, 64)), torch.float16, -1, "k") == 128
     rows = torch.zeros(3, 200, dtype=torch.float16)
     assert ops._heads(rows[:, :128].view(3, 2, 64), torch.Size((3, 2, 64)), torch.float16, -1, "k") == 200
+
+
+def test_attention_past_the_launch_limit():
+    """A grid holds less than 2^32 threads along an axis: said before anything is enqueued."""
+    def call(B, heads):
+        return L.lib().awq_kv4_attention(0x10000, 0x10000, 0x10000, 0x10000, None, 0x10000, B, B, 1, 100, heads, heads, 64,
+                                         16, 9, 7, 0.125, 0, 0, 0x10000, 1 << 40, None)
+    assert call(1 << 20, 8) == L.AWQ_EUNSUPPORTED
+    assert call(1 << 20, 4096) == L.AWQ_EUNSUPPORTED
