@@ -1028,7 +1028,8 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
         !aligned_to(cu_q, 4))
         return AWQ_EALIGN;
     const Kv4Plan p = plan_kv4(B, max_q, Hq, Hkv, head_dim, max_kv, stream_props(stream));
-    if (p.tiles > kLaunchRows) return AWQ_EUNSUPPORTED;
+    // (less than 2^32 threads along an axis; 512 a workgroup of the prefill kernel, 256 of the others)
+    if (p.tiles >= (int64_t(1) << 32) / (p.kind == 3 ? 512 : 256)) return AWQ_EUNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, p.workspace_bytes);
     if (rc != AWQ_OK) return rc;
     Kv4AttnArgs g{q, cache, tables, lens, cu_q, out, num_pages, (int)B, (int)total_q, (int)max_q, (int)Hq, (int)Hkv,

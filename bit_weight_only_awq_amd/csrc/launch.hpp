@@ -157,8 +157,8 @@ hipError_t launch_repack_v2(const int32_t *qweight_v2, const int32_t *qzeros_v2,
 hipError_t launch_unpack(const int32_t *packed, void *vals, int64_t rows, int64_t cols, int layout,
                          hipStream_t st);
 
-// A grid holds less than 2^32 threads along an axis: rows (or tokens, or tiles),
-// one a workgroup of at most 512 (1024: norm) threads, go to a launch in pieces.
+// A grid holds less than 2^32 threads along an axis: rows or tokens, one a
+// workgroup of at most 1024 threads, go to a launch in pieces.
 constexpr int64_t kLaunchRows = int64_t(1) << 21;
 
 // Residual addition + RMS norm + 8-bit output (norm.hip).

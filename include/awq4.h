@@ -528,7 +528,7 @@ int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride
  * Workspace: as for the GEMMs (shared, zero before and after each call).
  * B == 0 or total_q == 0 is a no-op that returns AWQ_OK.
  * Errors: AWQ_EINVAL (also scale <= 0), AWQ_EUNSUPPORTED (head_dim,
- * page_size, more than 2^21 tiles of query rows), AWQ_EALIGN, AWQ_EWORKSPACE,
+ * page_size, 2^23 tiles of query rows and more), AWQ_EALIGN, AWQ_EWORKSPACE,
  * AWQ_EHIP.
  */
 int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables, const int32_t *lens,

@@ -86,8 +86,9 @@ def test_stride_of_a_single_token_says_nothing():
 
 def test_attention_past_the_launch_limit():
     """A grid holds less than 2^32 threads along an axis: said before anything is enqueued."""
-    def call(B, heads):
-        return L.lib().awq_kv4_attention(0x10000, 0x10000, 0x10000, 0x10000, None, 0x10000, B, B, 1, 100, heads, heads, 64,
-                                         16, 9, 7, 0.125, 0, 0, 0x10000, 1 << 40, None)
-    assert call(1 << 20, 8) == L.AWQ_EUNSUPPORTED
+    def call(B, heads, max_q=1):
+        return L.lib().awq_kv4_attention(0x10000, 0x10000, 0x10000, 0x10000, 0x10000, 0x10000, B, B, max_q, 100, heads,
+                                         heads, 64, 16, 9, 7, 0.125, 0, 0, 0x10000, 1 << 40, None)
+    assert call(1 << 20, 16) == L.AWQ_EUNSUPPORTED
     assert call(1 << 20, 4096) == L.AWQ_EUNSUPPORTED
+    assert call(1 << 20, 8, 200) == L.AWQ_EUNSUPPORTED  # (the prompts' kernel has twice the threads)
