@@ -629,7 +629,8 @@ static Kv4Plan plan_kv4(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64
     p.tiles = B * Hkv * p.col_tiles;
     // Workgroups to fill the device, each with `least` steps at least.  Of the
     // prefill kernel one goes to a CU, so no more than CUs (24 tiles, 10 splits
-    // against 11: 87 -> 70 us); of the others two a CU or a few more (one / two /
+    // against 11: 87 -> 70 us); of the others two a CU or a few more (kind 2 is
+    // chosen where its tiles are that many: never split; one / two /
     // three: two sequences of 131072 tokens 65 / 56 / 57 us, 64 of 4096 to 8192
     // 84 / 84 / 92, 16 of 2050 with 32 heads 27 / 27 / 33).  `least` halved: 137
     // tokens 9.0 us instead of 6.6, for the second launch; doubled: one sequence of

@@ -72,7 +72,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
     const int G = g.Hq / g.Hkv;
 
     const Kv4Span<COLS, 32> span(g, b, ct, G);
-    const int q0 = span.q0, kv_len = span.kv_len, c0 = span.c0, ncols = span.ncols, splits = span.splits;
+    const int q0 = span.q0, kv_len = span.kv_len, c0 = span.c0, ncols = span.ncols;
+    const int splits = NT == 2 ? 1 : span.splits;  // (tiles of 32 rows are taken where they fill the device unsplit)
     if (ncols <= 0 || split >= splits) return;
     const int s_begin = span.first(split), s_end = span.first(split + 1);
     const int kv_lo = span.kv_lo, kv_hi = span.kv_hi;

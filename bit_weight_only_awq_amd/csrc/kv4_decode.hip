@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
     // takes row w, a lane two dimensions (D = 64: the upper lanes none).  A lane
     // reads its column's row in the lane group of its run, and zeros elsewhere.
     if (tid < D / 2) lds_q[4][tid] = 0u;
-    if (wave < 4) {
+    {
         const int row = wave < ncols ? wave : 0, qi = row / G, hg = row - qi * G;
         const bool holds = 2 * lane < D;
         const uint32_t *src = (const uint32_t *)((const uint16_t *)g.q + ((size_t)(q0 + qi) * g.Hq + h * G + hg) * D);

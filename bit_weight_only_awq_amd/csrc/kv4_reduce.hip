@@ -1,6 +1,7 @@
 // kv4_reduce.hip -- the sums of an attention call's workgroups, where several
-// share a sequence: a kernel after the attention kernel (any of its four forms)
-// adds them, writes the rows and clears the workspace.  (Added in the attention
+// share a sequence: a kernel after the attention kernel (any but that for tiles
+// of 32 rows, which fill the device by themselves) adds them, writes the rows
+// and clears the workspace.  (Added in the attention
 // kernels by the last workgroup to arrive, through the device's coherence point,
 // they took longer at every number of splits tried from 2 on: 4 x 24 rows over
 // 1024 tokens 18.7 us against 16.6, 4 x 256 rows 68 against 46; a single row
@@ -144,7 +145,6 @@ static hipError_t launch_reduce_kind(const Kv4AttnArgs &g, hipStream_t st) {
     switch (g.kind) {
         case 0: return launch_reduce<DT, D, 4, 64>(g, st);
         case 1: return launch_reduce<DT, D, 16, 32>(g, st);
-        case 2: return launch_reduce<DT, D, 32, 32>(g, st);
         default: return launch_reduce<DT, D, 256, 128>(g, st);
     }
 }
