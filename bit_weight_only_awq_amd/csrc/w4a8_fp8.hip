@@ -28,11 +28,6 @@
 
 namespace awq4 {
 
-template <int DT>
-__device__ __forceinline__ float round_act_f(float v) {
-    return DT == DT_F16 ? (float)(f16)v : (float)(__bf16)v;
-}
-
 // ---------------------------------------------------------------------------
 // Quantisation: one workgroup of 256 threads per row, two passes over the row
 // (abs-max, then codes).  The row sum of the codes' values is accumulated
@@ -59,7 +54,7 @@ __global__ __launch_bounds__(256) void w4a8_fp8_quant(const uint16_t *__restrict
     __syncthreads();
     mx = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
     const float amax = act_bits_to_f32<DT>(mx);
-    const float s = round_act_f<DT>(amax / 448.0f);  // correctly rounded fp32 divide, then the activation type
+    const float s = round_to_act<DT>(amax / 448.0f);  // correctly rounded fp32 divide, then the activation type
     const Fp8Quotient<DT> fq(s);
     long long sum = 0;
     auto code_of = [&](uint32_t h) -> uint32_t {
@@ -136,7 +131,7 @@ __global__ __launch_bounds__(T) void w4a8_fp8_quant_rows(const uint16_t *__restr
     mx = wmax[0];
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) mx = max(mx, wmax[w]);
-    const float s = round_act_f<DT>(act_bits_to_f32<DT>(mx) / 448.0f);
+    const float s = round_to_act<DT>(act_bits_to_f32<DT>(mx) / 448.0f);
     const Fp8Quotient<DT> fq(s);
     long long sum = 0;
     if (!fq.exact_divide) {
@@ -277,7 +272,7 @@ __global__ __launch_bounds__(256) void w4a8_fp8_skinny(const uint8_t *__restrict
         mx = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
         // the quantiser's own expressions (w4a8_fp8_quant_rows), so s1 and
         // every code come out the same
-        const float s = round_act_f<DT>(act_bits_to_f32<DT>(mx) / 448.0f);
+        const float s = round_to_act<DT>(act_bits_to_f32<DT>(mx) / 448.0f);
         const Fp8Quotient<DT> fq(s);
         const int k_lo = 128 * s_lo, nc = 16 * (s_hi - s_lo);  // chunks of 8 values
         int32_t part = 0;  // at most ceil(nc / 256) <= 16 chunks of at most 1835008 units
