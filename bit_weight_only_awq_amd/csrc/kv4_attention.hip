@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
             };
             numerators();
             if (__builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0) {
-                float t = ref[n];
+                float t = -__builtin_inff();
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 ? 3 : 2) void kv4_attentio
                         const float c = fmaxf(y + __builtin_amdgcn_logf(fabsf(vs[i][r])) - 11.0f, y - 90.0f);
                         t = plain || seen(i, r) ? fmaxf(t, c) : t;
                     }
-                t = column_max(t);
+                t = raised(ref[n], column_max(t));
                 const float f = __builtin_amdgcn_exp2f(ref[n] - t);
                 ref[n] = t;
                 l[n] *= f;

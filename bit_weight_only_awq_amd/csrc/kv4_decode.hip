@@ -235,14 +235,14 @@ __global__ __launch_bounds__(64 * kAttnWaves, 3) void kv4_decode_kernel(Kv4AttnA
         };
         numerators();
         if (__builtin_amdgcn_ballot_w64(!(top <= kMaxP && sum <= kMaxSum)) != 0) {
-            float t = ref;
+            float t = -__builtin_inff();
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float y = x[r] * cf;
                 const float c = fmaxf(y + __builtin_amdgcn_logf(fabsf(vs[r])) - 11.0f, y - 90.0f);
                 t = plain || seen(r) ? fmaxf(t, c) : t;
             }
-            t = column_max(t);
+            t = raised(ref, column_max(t));
             const float f = __builtin_amdgcn_exp2f(ref - t);
             ref = t;
             l *= f;

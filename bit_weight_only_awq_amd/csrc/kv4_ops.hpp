@@ -10,8 +10,19 @@
 namespace awq4 {
 
 constexpr int kAttnWaves = 4;
-constexpr float kNoRef = -1e30f;  // the reference of a row that has seen nothing
+constexpr float kNoRef = -0x1.fffffep127f;  // the reference of a row that has seen nothing
 constexpr float kMaxP = 0x1p15f, kMaxSum = 0x1p100f;
+// From here on a reference is too coarse for the numerators to stay within
+// fp16's range around it: such a row is NaN (a row of zeros would look like an answer).
+constexpr float kFarRef = 0x1p25f;
+
+// The reference of a row whose scores ask for m (-infinity: nothing seen).
+// Scores of 2^24 and more come in steps of two and more, and m's roundings may
+// leave it as far below what the numerators then are; from there on it is
+// taken higher by as much, so that they never pass fp16's range.
+__device__ __forceinline__ float raised(float ref, float m) {
+    return fmaxf(ref, m + fmaxf(__builtin_fmaf(fabsf(m), 0x1p-22f, -4.0f), 0.0f));
+}
 
 // The larger of the values of the four lanes of a column (lanes l, l ^ 16, l ^
 // 32, l ^ 48), in each of them.
@@ -141,7 +152,8 @@ struct AttnRows {
     int tile, splits, split, c0, q0, h, G;
 
     // (a sum of p that is not a number shows in the row)
-    __device__ __forceinline__ static f32x4 quotient(f32x4 v, float sum) {
+    __device__ __forceinline__ static f32x4 quotient(f32x4 v, float sum, float ref) {
+        sum = ref == kNoRef || fabsf(ref) < kFarRef ? sum : __builtin_nanf("");
         return sum == 0.0f ? (f32x4){0, 0, 0, 0} : v / sum;
     }
     __device__ __forceinline__ void put(int col, int d, f32x4 v) const {
@@ -168,7 +180,7 @@ struct AttnRows {
                 ll += a * row[D + 1];
             }
             if (splits == 1) {
-                put(col0 + col, d, quotient(v, ll));
+                put(col0 + col, d, quotient(v, ll, rr));
             } else {
                 float *row = row_of(split, col0 + col);
                 *(f32x4 *)(row + d) = v;

@@ -437,7 +437,7 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
         }
         if (__builtin_amdgcn_ballot_w64(raise) != 0) {
             products(tile - 1, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{}, nothing);
-            float m = kNoRef;
+            float m = -__builtin_inff();
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const f32x4 ks = lds_get<f32x4>(ks_from + 32 * c), to = lds_get<f32x4>(ks_from + kTo + 32 * c);
@@ -451,8 +451,8 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
             }
             // (rows that need not stay as they are, so that no row's result depends on another's)
             const bool either = pair_max(raise ? 1.0f : 0.0f) != 0.0f;
-            m = pair_max(m);
-            m = either ? fmaxf(ref, m) : ref;
+            m = raised(ref, pair_max(m));
+            m = either ? m : ref;
             const float f = __builtin_amdgcn_exp2f(ref - m);
             ref = m;
             l *= f;
@@ -538,7 +538,10 @@ __global__ __launch_bounds__(64 * kPreWaves, 1) void kv4_prefill_kernel(Kv4AttnA
         return (f32x4){v[4 * (q % 4)], v[4 * (q % 4) + 1], v[4 * (q % 4) + 2], v[4 * (q % 4) + 3]};
     };
     // (a sum that is not a number shows in the row)
-    auto inverse = [](float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; };
+    auto inverse = [&](float sum) {
+        sum = ref == kNoRef || fabsf(ref) < kFarRef ? sum : __builtin_nanf("");
+        return sum == 0.0f ? 0.0f : 1.0f / sum;
+    };
     l = pair_sum(l);
     if (splits == 1) {
         const float inv = inverse(l);

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void kv4_reduce_few_kernel(Kv4AttnArgs g) {
         v += a * w[s];
         ll += a * rl[s][1];
     }
-    t.out.put(col, 4 * q, AttnRows<DT, D>::quotient(v, ll));
+    t.out.put(col, 4 * q, AttnRows<DT, D>::quotient(v, ll, rr));
     // (the threads of a row are of one wave, so all of them have read its references)
     for (int s = 0; s < splits; ++s) {
         *(f32x4 *)(t.out.row_of(s, col) + 4 * q) = (f32x4){0, 0, 0, 0};
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void kv4_reduce_kernel(Kv4AttnArgs g) {
             v += lds_v[i][q];
             ll += lds_l[i];
         }
-        out.put(col, 4 * q, AttnRows<DT, D>::quotient(v, ll));
+        out.put(col, 4 * q, AttnRows<DT, D>::quotient(v, ll, rr));
     }
     for (int s = group; s < span.splits; s += GROUPS) {
         *(f32x4 *)(out.row_of(s, col) + 4 * q) = (f32x4){0, 0, 0, 0};

@@ -522,13 +522,17 @@ int awq_kv4_append(const void *q, const void *k, const void *v, int64_t q_stride
  * Numerics: the codes enter the matrix cores exactly; scores, running maxima,
  * sums and outputs are fp32; the softmax numerators times the values' scales
  * are rounded once to 11 bits for the second product (those below 2^-19 of a
- * row's largest to 2^-30 of it); out is rounded to nearest even.  A NaN or
+ * row's largest to 2^-30 of it); out is rounded to nearest even.  (Down to
+ * value scales of 2^-79 in magnitude; smaller ones keep fewer bits.)  A NaN or
  * infinity in q, or a NaN scale in a token that a row sees, makes that row NaN;
  * nothing that a row does not see changes it by more than its rounding.
+ * Scores of 2^24 and more in magnitude have binary32's steps of two and more
+ * (times log2(e)), the softmax with them; a row whose largest is past 2.3 10^7
+ * (2^25 / log2(e)), or below minus that, is NaN.
  * Workspace: as for the GEMMs (shared, zero before and after each call).
  * B == 0 or total_q == 0 is a no-op that returns AWQ_OK.
  * Errors: AWQ_EINVAL (also scale <= 0), AWQ_EUNSUPPORTED (head_dim,
- * page_size, 2^23 tiles of query rows and more), AWQ_EALIGN, AWQ_EWORKSPACE,
+ * page_size, more tiles of query rows than a launch holds), AWQ_EALIGN, AWQ_EWORKSPACE,
  * AWQ_EHIP.
  */
 int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables, const int32_t *lens,

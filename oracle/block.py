@@ -174,8 +174,8 @@ def page_values(cache, P: int, D: int, page: int, h: int, dtype: str):
 # ------------------------------------------------------------------ attention
 
 def _rows(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
-    """For every row of q that sees anything: (row, query head, the row's values, softmax weights of the tokens it sees,
-    their values, key scales and value scales)."""
+    """For every row of q that sees anything: (row, query head, the row's values, scores of the tokens it sees, their
+    softmax weights, values, key scales and value scales)."""
     T, hq, D = q.shape
     pages, hkv, _ = cache.shape
     G = hq // hkv
@@ -211,14 +211,14 @@ def _rows(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype
                     t = scale * (K[seen] @ row)
                     w = np.exp(t - t.max())
                     w /= w.sum()
-                    yield r0 + i, e, row, w, V[seen], ks[seen], vs[seen]
+                    yield r0 + i, e, row, t, w, V[seen], ks[seen], vs[seen]
 
 
 def attention(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
     """(out, spread, unit): out [T, Hq, D] in binary64, and what an error bound needs: sum of p |v| (spread), and per row
     (sum of p s', scale * largest |s| * sum |q|, largest s') over the tokens that it sees, from the words of the cache."""
     out, spread, unit = np.zeros(q.shape), np.zeros(q.shape), np.zeros((*q.shape[:2], 3))
-    for r, e, row, w, V, ks, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
+    for r, e, row, _, w, V, ks, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
         out[r, e] = w @ V
         spread[r, e] = w @ np.abs(V)
         unit[r, e] = (w @ vs, scale * np.abs(ks).max() * np.abs(row).sum(), np.nanmax(vs))
@@ -228,6 +228,6 @@ def attention(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, d
 def products(q, cache, P: int, tables, lens, cu_q, scale: float, window: int, dtype: str):
     """[T, Hq, 3]: over the tokens that a row sees, the largest p |s'|, their number, and the sum of p |s'|."""
     top = np.zeros((*q.shape[:2], 3))
-    for r, e, _, w, _, _, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
+    for r, e, _, _, w, _, _, vs in _rows(q, cache, P, tables, lens, cu_q, scale, window, dtype):
         top[r, e] = (w * np.abs(vs)).max(), len(w), w @ np.abs(vs)
     return top
