@@ -569,7 +569,7 @@ static bool known_dtype(int dtype) { return dtype == AWQ_DTYPE_F16 || dtype == A
 // out8: the call has codes and scales (a, s1; fp8: asum too)
 static int run_rmsnorm(const void *x, const void *residual, const void *weight, void *residual_out, void *y, void *a,
                        float *s1, float *asum, bool fp8, int64_t M, int64_t K, float eps, int dtype, void *stream) {
-    if (!x || !weight || (!residual != !residual_out)) return AWQ_EINVAL;
+    if (!x || !weight || (!residual != !residual_out) || (y && y == residual_out)) return AWQ_EINVAL;
     if (fp8 ? (!a || !s1 || !asum) : (!a != !s1 || (!a && !y))) return AWQ_EINVAL;
     if (M < 1 || K < 1 || M > (int64_t(1) << 31) - 1 || K > kMaxDim) return AWQ_EINVAL;
     if (!known_dtype(dtype) || !(eps >= 0.0f) || !std::isfinite(eps)) return AWQ_EINVAL;

@@ -427,7 +427,8 @@ int w4a8_fp8_linear(const void *x, uint8_t *a, float *s1, float *asum, const int
  *   No other tensors may overlap.  A row whose h holds a NaN or an infinity,
  *   or whose norm overflows the activation type, has an s1 that is not
  *   finite; its codes mean nothing.  eps >= 0 and finite.
- * Errors: AWQ_EINVAL (M, K < 1, K > 2^20, pointers, dtype, eps), AWQ_EALIGN,
+ * Errors: AWQ_EINVAL (M, K < 1, K > 2^20, pointers, y at residual_out, dtype,
+ * eps), AWQ_EALIGN,
  * AWQ_EHIP.
  */
 int w4a8_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *residual_out, void *y,

@@ -92,3 +92,11 @@ def test_attention_past_the_launch_limit():
     assert call(1 << 20, 16) == L.AWQ_EUNSUPPORTED
     assert call(1 << 20, 4096) == L.AWQ_EUNSUPPORTED
     assert call(1 << 20, 8, 200) == L.AWQ_EUNSUPPORTED  # (the prompts' kernel has twice the threads)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_norm_refuses_y_over_the_residual_stream(fp8):
+    """Both would be written to one place, and one of them lost."""
+    a, o = 0x10000, 0x20000
+    fn = L.lib().w4a8_fp8_rmsnorm_quant if fp8 else L.lib().w4a8_rmsnorm_quant
+    assert fn(a, a, a, o, o, a, a, *([a] if fp8 else []), 4, 64, 1e-6, 0, None) == L.AWQ_EINVAL
