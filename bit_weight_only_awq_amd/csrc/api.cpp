@@ -597,8 +597,10 @@ struct Kv4Plan {
     int64_t col_tiles, tiles;
     size_t workspace_bytes;
 };
-// Which attention kernel (heads: sequences times key/value heads; times of
-// 32 query heads over 8, D = 128, bf16, pages of 16):
+// Which attention kernel, for the whole call and by its bounds (heads: sequences
+// times key/value heads; times of 32 query heads over 8, D = 128, bf16, pages of
+// 16).  A window is not counted, nor are lengths below max_kv: calls of loose
+// bounds may get the kernel and the shares of a larger one.
 //  - at most four rows: kv4_decode.hip.  64 sequences of about 4900 tokens 81 us,
 //    tiles of 16 rows 89.
 //  - the prefill kernel where every CU gets four of its steps or more and a tile

@@ -1,5 +1,6 @@
 // kv4.hpp -- the paged key/value cache in 4 bits, as the kernels address it
-// (kv4_append.hip writes it, kv4_attention.hip and kv4_prefill.hip read it).
+// (kv4_append.hip writes it; kv4_decode.hip, kv4_attention.hip and
+// kv4_prefill.hip read it).
 //
 // int32 [pages, kv_heads, P (D/4 + 2)]; the words of one page and head:
 //   K words  [P][D/8]       AWQ order along the head dimension: nibble i of

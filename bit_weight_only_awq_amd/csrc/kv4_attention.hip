@@ -26,7 +26,7 @@
 // of a product far below the largest of its sum, always downwards: every other
 // wave sums negated probabilities, whose loss is upwards.  (Error of the output
 // for 131072 tokens, its own rounding to 11 bits 2.0e-4: zero points taken off
-// at the end 8.4e-4, step by step 5.6e-4, with half the waves negated 2.3e-4.)
+// at the end 8.4e-4, step by step 5.5e-4, with half the waves negated 2.7e-4.)
 // Queries are scaled by a power of two to just below 2^15 before they become
 // fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest.
 //
@@ -41,8 +41,9 @@
 // join their sums through LDS, and the workgroups of a sequence (as many as
 // its length asks for, known only on the device) leave theirs in the workspace
 // for kv4_reduce.hip.  Measured (32 heads over 8, D = 128, bf16): 16 sequences of
-// 4096 tokens, 8 rows a head 21 us, 16 rows 24, 128 rows (two tiles of 16 a
-// workgroup) 66; one of 8192, 64 rows 18.
+// 4096 tokens, 8 rows a head 21 us, 16 rows 22, 64 rows 51, 128 rows (two tiles
+// of 16 a workgroup) 66; one of 8192, 64 rows 18.  (Eight rows take nearly the
+// time of sixteen: their tile's other columns are computed too.)
 #include "kv4_ops.hpp"
 
 namespace awq4 {

@@ -29,9 +29,9 @@
 // registers of two waves a SIMD: a single spilled one waits for the cache
 // words in flight, which are ahead of it in the queue.
 //
-// Measured (32 heads over 8, D = 128, bf16): a prompt of 4096 tokens 159 us, 865
+// Measured (32 heads over 8, D = 128, bf16): a prompt of 4096 tokens 160 us, 860
 // TFLOP/s; five chunks of 700 tokens behind 3000 others with a window of 1000,
-// 100 us.  128 rows a workgroup, two of them a CU, a barrier every 64 tokens:
+// 97 us.  128 rows a workgroup, two of them a CU, a barrier every 64 tokens:
 // 225 and 125.  One wave a SIMD with 64 rows: over 600 (the sums alone are 128
 // registers, and queries spill).  The two waves of a SIMD made to take turns
 // between products and scores by barriers: 223 and 175 (a wave alone issues a

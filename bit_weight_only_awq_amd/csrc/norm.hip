@@ -193,7 +193,8 @@ __global__ __launch_bounds__(T) void rmsnorm_rows(const uint16_t *x, const uint1
 }
 
 // General form (any K): one workgroup of 256 threads per row, a value at a
-// time, three passes (sum of squares, abs-max, codes).  Each thread reads in
+// time, three passes (sum of squares, abs-max, codes); 1024 rows of 4097 values,
+// fp16, int8, 22.5 us where 4096 in registers take 8.6.  Each thread reads in
 // the later passes only what it wrote or left unchanged itself: h from h_out
 // where there is a residual, y from y where it is asked for.
 template <int DT, int OUT>
@@ -266,10 +267,18 @@ static hipError_t launch_rows(const NormArgs &n, hipStream_t st) {
 }
 
 // Threads for a row: 8 values each up to 512 threads, then two chunks each up
-// to 8192 values, then 1024 threads (bf16, fp8 codes, residual: 777 rows of 8192
-// in 512 threads 14.7 us, in 1024 15.4, in 256 14.1; of 5120, int8, 10.4, 13.1,
-// 10.1; 4096 rows of 4096, fp16, int8: 512 threads 21.5, 256 22.8; 2048 rows of
-// 14336, fp8: 1024 threads 44, 512 49, 256 49).
+// to 8192 values, then 1024 threads.  Both sides, with a residual, in us:
+//   8192 values, bf16, fp8 codes   rows     1    64   300   777  2048  4096
+//     512 threads                         5.0   5.4   8.2  14.6  24.7  45.8
+//     256                                 5.9   6.5   8.7  14.0  24.4  49.4
+//   5120 values, fp16, int8 codes
+//     512                                 4.0   4.4   5.7  10.5  17.3  32.0
+//     256                                 4.7   5.1   6.1  10.1  17.6  32.4
+//   14336 values, bf16, fp8 codes  rows     1   300   777  2048
+//     1024                                6.2  12.9  22.0  45.6
+//     512                                 6.3  12.3  22.2  48.2
+// (777 rows of 8192 in 1024 threads 15.4; 4096 rows of 4096, fp16, int8: 512
+// threads 21.5, 256 22.8.)
 template <int DT, int OUT>
 static hipError_t launch_norm(const NormArgs &n, hipStream_t st) {
     if (n.K % 8 == 0 && n.K <= 8 * 1024 * 4) {
