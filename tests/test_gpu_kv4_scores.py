@@ -1,11 +1,11 @@
 """Attention over the 4-bit cache at scores where binary32 has no fractions left.
 
-Scores of magnitude y have an error of some 2^-17 y here (2^-24 a term, over D
-+ 32 roundings of terms 30 times as large, as test_gpu_kv4_attention.py counts
-them).  So a row whose best score is ahead of the next by more than that is the
-value of its best token, to the roundings of the output and of the numerators;
-rows without such a lead are left out.  From 2^25 on (times log2 e), a row is
-NaN: it is never finite and wrong."""
+A score's error is 2^-24 a term for the sums of D products of codes up to 15 and
+of the zero points' part: 30 sum |q| s scale, over D + 32 roundings.  A row whose
+best score is ahead of the next by twice that, and 40, is the value of its best
+token, to the roundings of the output and of the numerators; rows without such
+a lead are left out.  From 2^25 on (times log2 e) a row is NaN: it is never
+finite and wrong."""
 import numpy as np
 import pytest
 
@@ -22,17 +22,17 @@ def check(c, scale, **kw):
     got = block.decode(b16(c.gpu(scale=scale, **kw)), c.dtype)
     u = 2.0 ** -11 if c.dtype == "f16" else 2.0 ** -8
     sums = 2.0 ** -24 * (int(c.lens.max()) / 4 + 256) * 30
-    sure = 0
-    for r, e, _, t, _, V, _, vs in block._rows(c.q, c.cache, c.P, c.tables, c.lens, c.cu, float(np.float32(scale)), 0,
-                                               c.dtype):
+    sure, scale = 0, float(np.float32(scale))
+    for r, e, row, t, _, V, ks, vs in block._rows(c.q, c.cache, c.P, c.tables, c.lens, c.cu, scale, 0, c.dtype):
         t, out = t * LOG2E, got[r, e]
-        first, y = int(t.argmax()), np.abs(t).max()
+        first = int(t.argmax())
+        error = 2.0 ** -24 * (c.D + 32) * 30 * scale * ks.max() * np.abs(row).sum() * LOG2E
         lead = t[first] - np.sort(t)[-2] if len(t) > 1 else np.inf
         if np.abs(t[first]) > 2.0 ** 25.2:
             assert np.isnan(out).all(), (r, e)
         elif np.abs(t[first]) < 2.0 ** 24.8:
             assert np.isfinite(out).all(), (r, e)
-            if lead > 2.0 ** -16 * y + 40:
+            if lead > 2 * error + 40:
                 # (the others' weights together are below n 2^-40)
                 v, rest = V[first], len(t) * 2.0 ** -40 * np.abs(V).max()
                 assert (np.abs(out - v) <= (u + 2.0 ** -11 + 2.0 ** -20) * np.abs(v) + sums * vs[first] + rest
