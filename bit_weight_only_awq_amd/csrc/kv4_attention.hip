@@ -28,7 +28,8 @@
 // for 131072 tokens, its own rounding to 11 bits 2.0e-4: zero points taken off
 // at the end 8.4e-4, step by step 5.5e-4, with half the waves negated 2.7e-4.)
 // Queries are scaled by a power of two to just below 2^15 before they become
-// fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest.
+// fp16: exact for fp16 and for bf16 (8 bits), down to 2^-25 of a row's largest
+// (bf16 rows that are below 2^-86 throughout keep fewer bits).
 //
 // Tiles are transposed, S^T = K Q^T and O^T = V^T P^T: the lanes of a column
 // (one query row) hold the scores of the tokens that they then need as the
