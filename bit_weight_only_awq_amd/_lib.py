@@ -20,6 +20,7 @@ AWQ_EHIP = -5
 
 AWQ_DTYPE_F16 = 0
 AWQ_DTYPE_BF16 = 1
+AWQ_DTYPE_F32 = 2
 AWQ_LAYOUT_N8 = 0
 W4A8_LAYOUT_K8 = 1
 AWQ_LAYOUT_V2 = 2
@@ -89,6 +90,20 @@ def lib() -> ctypes.CDLL:
                                     i32, vp, sz, vp]
     L.awq_kv4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.awq_kv4_attention_workspace_bytes.restype = sz
+    L.awq_moe_route.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
+    L.awq_moe_combine.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, vp]
+    L.awq_moe_gemm_w4a16.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, i32, vp, sz, vp]
+    L.awq_fp8_block_quant_act.argtypes = [vp, vp, vp, i64, i64, i32, vp]
+    L.awq_fp8_block_gemm.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, sz, vp]
+    L.awq_moe_fp8_block_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, vp, sz, vp]
+    L.awq_moe_route_workspace_bytes.argtypes = [i64, i64, i64]
+    L.awq_moe_gemm_w4a16_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    L.awq_fp8_block_gemm_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    for f in ("awq_moe_route", "awq_moe_gemm_w4a16", "awq_fp8_block_gemm"):
+        getattr(L, f + "_workspace_bytes").restype = sz
+    for f in ("awq_moe_route", "awq_moe_combine", "awq_moe_gemm_w4a16", "awq_fp8_block_quant_act", "awq_fp8_block_gemm",
+              "awq_moe_fp8_block_gemm"):
+        getattr(L, f).restype = i32
     for f in ("w4a8_rmsnorm_quant", "w4a8_fp8_rmsnorm_quant", "awq_kv4_append", "awq_kv4_attention"):
         getattr(L, f).restype = i32
     for f in ("awq_pack", "awq_unpack", "awq_gemm_w4a16", "awq_gemv_w4a16", "w4a8_quant_act", "w4a8_gemm", "w4a8_linear",

@@ -655,6 +655,123 @@ static int check_attention(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, in
     return AWQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Routing, products grouped by expert, and block-scaled E4M3 products.
+static constexpr int64_t kMaxGroupedRows = int64_t(1) << 24;  // (row tiles of all experts in 32 bits)
+
+static int check_route(int64_t T, int64_t E, int64_t k) {
+    if (T < 0 || T > kMaxDim || E < 1 || E > kMoeMaxExperts) return AWQ_EINVAL;
+    if (k < 1 || k > E || k > kMoeMaxTop || T * k > kMaxGroupedRows) return AWQ_EINVAL;
+    return AWQ_OK;
+}
+// One launch for as many tokens as one workgroup's waves take at once, and up to 512 experts
+// (whose counts fit its LDS beside the slots); else two, of workgroups of 16 tokens or more,
+// 256 of them at most while the slots of one fit its LDS.
+static RoutePlan plan_route(int64_t T, int64_t E, int64_t k) {
+    RoutePlan p{};
+    p.block_tokens = (int)std::min<int64_t>(std::max<int64_t>(16, cdiv(T, 256)), 8192 / k);
+    p.blocks = T <= 16 && E <= 512 ? 1 : (int)cdiv(T, p.block_tokens);
+    if (p.blocks == 1 && E > 512) p.blocks = 2, p.block_tokens = (int)std::max<int64_t>(1, cdiv(T, 2));
+    return p;
+}
+
+// Experts that R rows reach when each goes to any of E alike.
+static double live_experts(int64_t R, int64_t E) { return E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)R)); }
+// Row tiles of `rows` that any split of R rows over E experts needs at most.
+static int64_t group_tiles(int64_t R, int64_t E, int64_t rows) { return std::min(E, R) + R / rows; }
+
+static int check_grouped(const int32_t *offsets, const int32_t *rows, int64_t R, int64_t x_rows, int64_t top,
+                         int64_t E) {
+    if (R < 0 || R > kMaxGroupedRows || E < 1 || E > kMoeMaxExperts || top < 1 || top > kMoeMaxTop) return AWQ_EINVAL;
+    if (x_rows < 0 || x_rows > kMaxGroupedRows || (!rows && x_rows != R)) return AWQ_EINVAL;
+    if (R == 0) return AWQ_OK;
+    if (!offsets || x_rows == 0) return AWQ_EINVAL;
+    if (!aligned_to(offsets, 4) || !aligned_to(rows, 4)) return AWQ_EALIGN;
+    return AWQ_OK;
+}
+// a grid holds less than 2^32 threads along an axis
+static bool grid_fits(int64_t workgroups) { return workgroups < (int64_t(1) << 32) / 512; }
+
+static int check_moe_w4a16_shape(int64_t R, int64_t E, int64_t N, int64_t K, int G) {
+    if (R < 0 || R > kMaxGroupedRows || E < 1 || E > kMoeMaxExperts) return AWQ_EINVAL;
+    if (N < 8 || K < 1 || N > kMaxDim || K > kMaxDim || N % 8) return AWQ_EINVAL;
+    if ((G != 32 && G != 64 && G != 128) || K % G) return AWQ_EINVAL;
+    return AWQ_OK;
+}
+static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
+    W4A16Plan p{};
+    const double live = live_experts(R, E), avg = (double)R / live;
+    if (avg > 48 && K % 64 == 0 && N % 32 == 0 && K * (N / 2) < (int64_t(1) << 31)) {
+        p.kind = 3;
+        p.mt = avg > 128 ? 16 : 8;
+        p.wn = avg > 128 ? 8 : 4;
+        p.ksplit = 1;
+        p.splits = 1;
+        p.tiles_n = (int)cdiv(N, 32 * p.wn);
+        p.tiles_m = (int)group_tiles(R, E, 16 * p.mt);
+        return p;
+    }
+    p.kind = 5;
+    p.blk = 1;
+    p.cs = G >= 64 ? 2 : 1;
+    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    p.waves = kStreamWaves(p.mt);
+    p.tiles_n = (int)cdiv(N, 128);
+    p.tiles_m = (int)group_tiles(R, E, 16 * p.mt);
+    // K splits as for a dense layer of as many tiles
+    const double rows = 16.0 * p.mt;
+    const int64_t tiles = std::max<int64_t>(1, (int64_t)(p.tiles_n * live * std::ceil(avg / rows)));
+    const int64_t chunks = K / (32 * p.cs);
+    const int64_t smax = std::max<int64_t>(1, std::min<int64_t>(d.cus / tiles, chunks / p.waves));
+    const double stream_bytes = (double)K * (64 + 2 * rows), tail_bytes = rows * 128 * 4;
+    p.splits = 1;
+    double best = 0;
+    for (int64_t c = 1; c <= smax; ++c) {
+        const double t = stream_bytes / c / 25.0 + c * tail_bytes / 40.0;
+        if (c == 1 || t < best) best = t, p.splits = (int)c;
+    }
+    if (p.splits > 1)
+        p.workspace_bytes = (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, R, N);
+    return p;
+}
+
+// M rows in all; E = 0: one matrix
+static int check_fp8_block_shape(int64_t M, int64_t E, int64_t N, int64_t K) {
+    if (M < 0 || M > kMaxGroupedRows || E < 0 || E > kMoeMaxExperts) return AWQ_EINVAL;
+    if (N < 8 || K < 16 || N > kMaxDim || K > kMaxDim || N % 8 || K % 16) return AWQ_EINVAL;
+    if (N * K >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;  // (a matrix is addressed by 32-bit offsets)
+    return AWQ_OK;
+}
+static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, const DeviceProps &d) {
+    Fp8BlockPlan p{};
+    const double live = E ? live_experts(M, E) : 1.0, avg = (double)M / live;
+    auto row_tiles = [&](int64_t rows) { return E ? group_tiles(M, E, rows) : cdiv(M, rows); };
+    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    p.tiles_n = (int)cdiv(N, kFp8StreamCols);
+    p.tiles_m = (int)row_tiles(16 * p.mt);
+    const int64_t blocks = cdiv(K, 128);
+    const int64_t tiles = std::max<int64_t>(1, (int64_t)(p.tiles_n * live * std::ceil(avg / (16.0 * p.mt))));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * d.cus / tiles, blocks / 16, 8}));
+    if (p.splits > 1)
+        p.workspace_bytes = (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);
+    return p;
+}
+static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
+                         int64_t E, int64_t N, int64_t K, int dtype, Groups groups, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    if (!a || !w || !sa || !sw || !y || !known_dtype(dtype)) return AWQ_EINVAL;
+    for (const void *q : {(const void *)a, (const void *)w, (const void *)sa, (const void *)sw, (const void *)y})
+        if (!aligned16(q)) return AWQ_EALIGN;
+    Fp8BlockPlan p = plan_fp8_block(M, E, N, K, stream_props(stream));
+    if (!grid_fits((int64_t)p.tiles_n * p.tiles_m)) return AWQ_EUNSUPPORTED;
+    const int rc = check_workspace(workspace, workspace_bytes, p.workspace_bytes);
+    if (rc != AWQ_OK) return rc;
+    if (p.splits > 1) p.acc = static_cast<uint64_t *>(workspace);
+    groups.max_tiles = p.tiles_m;
+    const Fp8BlockArgs g{a, w, sa, sw, y, (int)M, (int)N, (int)K, dtype, groups};
+    return hip_status(launch_fp8_block_stream(g, p, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace awq4
 
 using namespace awq4;
@@ -1044,6 +1161,108 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
                                   : launch_kv4_attention(g, st));
     if (rc != AWQ_OK || p.splits == 1) return rc;
     return hip_status(launch_kv4_reduce(g, st));
+}
+
+size_t awq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k) {
+    if (check_route(T, E, k) != AWQ_OK) return 0;
+    const RoutePlan p = plan_route(T, E, k);
+    return p.blocks == 1 ? 0 : (size_t)p.blocks * E * 4;
+}
+
+int awq_moe_route(const void *logits, float *weights, int32_t *experts, int32_t *offsets, int32_t *rows,
+                  int32_t *places, int64_t T, int64_t E, int64_t k, int renormalize, int dtype, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+    int rc = check_route(T, E, k);
+    if (rc != AWQ_OK) return rc;
+    if (!known_dtype(dtype) && dtype != AWQ_DTYPE_F32) return AWQ_EINVAL;
+    if ((renormalize != 0 && renormalize != 1) || !offsets) return AWQ_EINVAL;
+    if (T > 0 && (!logits || !weights || !experts || !rows || !places)) return AWQ_EINVAL;
+    for (const void *q : {logits, (const void *)weights, (const void *)experts, (const void *)offsets,
+                          (const void *)rows, (const void *)places})
+        if (!aligned16(q)) return AWQ_EALIGN;
+    RoutePlan p = plan_route(T, E, k);
+    rc = check_workspace(workspace, workspace_bytes, p.blocks == 1 ? 0 : (size_t)p.blocks * E * 4);
+    if (rc != AWQ_OK) return rc;
+    p.counts = static_cast<int *>(workspace);
+    const RouteArgs g{logits, weights, experts, offsets, rows, places, T, (int)E, (int)k, renormalize, dtype};
+    return hip_status(launch_route(g, p, static_cast<hipStream_t>(stream)));
+}
+
+int awq_moe_combine(const void *y, const float *weights, const int32_t *places, void *out, int64_t T, int64_t R,
+                    int64_t N, int64_t k, int dtype, void *stream) {
+    if (T < 0 || T > kMaxDim || R < 0 || R > kMaxGroupedRows || k < 1 || k > kMoeMaxTop) return AWQ_EINVAL;
+    if (N < 8 || N > kMaxDim || N % 8 || !known_dtype(dtype)) return AWQ_EINVAL;
+    if (T == 0) return AWQ_OK;
+    if ((R > 0 && !y) || !weights || !places || !out) return AWQ_EINVAL;
+    if (!aligned16(y) || !aligned16(out) || !aligned_to(weights, 4) || !aligned_to(places, 4)) return AWQ_EALIGN;
+    const CombineArgs g{y, weights, places, out, T, R, N, (int)k, dtype};
+    return hip_status(launch_combine(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t awq_moe_gemm_w4a16_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K, int group_size) {
+    if (check_moe_w4a16_shape(R, E, N, K, group_size) != AWQ_OK || R == 0) return 0;
+    return plan_moe_w4a16(R, E, N, K, group_size, stream_props(nullptr)).workspace_bytes;
+}
+
+int awq_moe_gemm_w4a16(const void *x, const int32_t *qweight, const void *scales, const int32_t *qzeros,
+                       const int32_t *offsets, const int32_t *rows, void *y, int64_t R, int64_t x_rows, int64_t top_k,
+                       int64_t E, int64_t N, int64_t K, int group_size, int dtype, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    int rc = check_moe_w4a16_shape(R, E, N, K, group_size);
+    if (rc != AWQ_OK) return rc;
+    if (!known_dtype(dtype)) return AWQ_EINVAL;
+    rc = check_grouped(offsets, rows, R, x_rows, top_k, E);
+    if (rc != AWQ_OK || R == 0) return rc;
+    if (!x || !qweight || !scales || !y) return AWQ_EINVAL;
+    for (const void *q : {x, (const void *)qweight, scales, (const void *)qzeros, (const void *)y})
+        if (!aligned16(q)) return AWQ_EALIGN;
+    // (gathered rows are addressed by 32-bit offsets)
+    if (rows && x_rows * K * 2 >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;
+    W4A16Plan p = plan_moe_w4a16(R, E, N, K, group_size, stream_props(stream));
+    if (!grid_fits((int64_t)p.tiles_n * p.tiles_m)) return AWQ_EUNSUPPORTED;
+    rc = check_workspace(workspace, workspace_bytes, p.workspace_bytes);
+    if (rc != AWQ_OK) return rc;
+    if (p.workspace_bytes > 0) p.acc = static_cast<uint64_t *>(workspace);
+    const W4A16Args a{x, qweight, scales, qzeros, y, R, N, K, group_size, dtype};
+    const Groups g{offsets, rows, (int)E, (int)R, (int)top_k, (int)x_rows, p.tiles_m};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return hip_status(p.kind == 3 ? launch_w4a16_gemm_grouped(a, p, g, st) : launch_w4a16_stream_grouped(a, p, g, st));
+}
+
+int awq_fp8_block_quant_act(const void *x, uint8_t *a, float *s, int64_t M, int64_t K, int dtype, void *stream) {
+    if (M < 0 || M > (int64_t(1) << 31) - 1 || K < 16 || K > kMaxDim || K % 16 || !known_dtype(dtype))
+        return AWQ_EINVAL;
+    if (M == 0) return AWQ_OK;
+    if (!x || !a || !s) return AWQ_EINVAL;
+    if (!aligned16(x) || !aligned16(a) || !aligned16(s)) return AWQ_EALIGN;
+    return hip_status(launch_fp8_block_quant(x, a, s, M, K, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t awq_fp8_block_gemm_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K) {
+    if (check_fp8_block_shape(M, E, N, K) != AWQ_OK || M == 0) return 0;
+    return plan_fp8_block(M, E, N, K, stream_props(nullptr)).workspace_bytes;
+}
+
+int awq_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
+                       int64_t N, int64_t K, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = check_fp8_block_shape(M, 0, N, K);
+    if (rc != AWQ_OK) return rc;
+    if (M == 0) return AWQ_OK;
+    return run_fp8_block(a, w, sa, sw, y, M, 0, N, K, dtype, Groups{}, workspace, workspace_bytes, stream);
+}
+
+int awq_moe_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw,
+                           const int32_t *offsets, const int32_t *rows, void *y, int64_t R, int64_t x_rows,
+                           int64_t top_k, int64_t E, int64_t N, int64_t K, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    int rc = check_fp8_block_shape(R, E, N, K);
+    if (rc != AWQ_OK) return rc;
+    rc = check_grouped(offsets, rows, R, x_rows, top_k, E);
+    if (rc != AWQ_OK || R == 0) return rc;
+    // (gathered rows are addressed by 32-bit offsets)
+    if (rows && x_rows * K >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;
+    const Groups g{offsets, rows, (int)E, (int)R, (int)top_k, (int)x_rows, 0};
+    return run_fp8_block(a, w, sa, sw, y, R, E, N, K, dtype, g, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

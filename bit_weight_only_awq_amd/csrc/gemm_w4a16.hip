@@ -31,6 +31,7 @@
 // M <= 128, where 256-row tiles would be half padding).
 #include "device.hpp"
 #include "launch.hpp"
+#include "moe.hpp"
 #include "w4a16_ops.hpp"
 
 namespace awq4 {
@@ -79,13 +80,18 @@ __host__ __device__ constexpr int gemm_col(int u) { return (u & 1) + ((u >> 1) <
 // the output tile and split its K range (each with its own LDS ring); the
 // groups trade partial sums through LDS at the end.  This doubles the waves
 // per SIMD for layers with no more tiles than CUs.
-template <int DT, bool SYM, int KS, int MT, int AB, int BB, int WN>
+// Grp: Groups, for rows grouped by expert (grid x: the column tiles of every
+// row tile that there may be; M: the rows of all experts; no K split over
+// workgroups), or NoGroups.
+template <int DT, bool SYM, int KS, int MT, int AB, int BB, int WN, class Grp>
 __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ? 3 : 2) void w4a16_gemm(const uint16_t *__restrict__ x,
                                                                 const uint32_t *__restrict__ qw,
                                                                 const uint16_t *__restrict__ sc,
                                                                 const uint32_t *__restrict__ qz,
                                                                 uint16_t *__restrict__ y, uint64_t *__restrict__ acc64,
-                                                                int M, int N, int K, int G, int S, int sep) {
+                                                                int M, int N, int K, int G, int S, int sep,
+                                                                Grp groups) {
+    constexpr bool GROUPED = !std::is_same_v<Grp, NoGroups>;
     using R = GRing<MT, AB, BB, WN>;
     static_assert(KS == 1 || (WN == 4 && KS * R::LDS >= 2 * 4 * MT * 64 * 16), "the K-split handover fits in the rings");
     static_assert(AB >= 2 && BB >= 3 && MT > kPrefA, "ring depths and prefetch distance");
@@ -102,9 +108,26 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
     const int j = lane & 15, gq = lane >> 4;
     const int nw = N >> 3;
     // logical tile of this workgroup (XCD-aware order over the tiles_n x tiles_m grid)
-    const int tile = tile_of_xcd_order(blockIdx.x + gridDim.x * blockIdx.y, gridDim.x * gridDim.y);
-    const int tn = tile % gridDim.x, tm = tile / gridDim.x, split = blockIdx.z;
-    const int m0 = tm * GB_M, wc0 = tn * WC;
+    int tn, tm = 0, m0;
+    const int split = blockIdx.z, lg = __builtin_ctz(G);  // G is 32, 64 or 128
+    if constexpr (GROUPED) {
+        const GroupTile t = group_tile(groups.offsets, groups.E, groups.R, GB_M, (N + GB_N - 1) / GB_N,
+                                       groups.max_tiles, blockIdx.x);
+        if (!t.live) return;
+        tn = t.tile_n;
+        m0 = t.row0;
+        M = t.row_end;
+        const size_t e = t.expert;
+        qw += e * K * nw;
+        sc += e * (size_t)(K >> lg) * N;
+        if (!SYM) qz += e * (size_t)(K >> lg) * nw;
+    } else {
+        const int tile = tile_of_xcd_order(blockIdx.x + gridDim.x * blockIdx.y, gridDim.x * gridDim.y);
+        tn = tile % gridDim.x;
+        tm = tile / gridDim.x;
+        m0 = tm * GB_M;
+    }
+    const int wc0 = tn * WC;
     const int T = K / GB_K;
     // stages of this workgroup, then of this group: group 0 takes the first
     // ceil(n/2), group 1 the rest; both pass `iters` loop barriers (group 1
@@ -120,19 +143,25 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
     // outputs are never stored).  Words: wave w copies k-rows B_ROWS w +
     // lane/(WC/4), lane%(WC/4) being the stored segment; word-columns past
     // the end repeat the last 4.
-    const char *const xg = (const char *)(x + (size_t)m0 * K);
+    bool gather = false;  // (then every row is at an offset from x itself)
+    if constexpr (GROUPED) gather = groups.rows != nullptr;
+    const char *const xg = (const char *)(x + (gather ? (size_t)0 : (size_t)m0 * K));
     const char *const wg = (const char *)(qw + wc0);
     // descriptors over the rest of X from row m0 and of the packed words from
     // word-column wc0 (the planner keeps both under 2^31 bytes)
-    const __amdgpu_buffer_rsrc_t xrs = buf_rsrc(xg, (int64_t)(M - m0) * K * 2);
+    int x_rows = M - m0;
+    if constexpr (GROUPED) x_rows = gather ? groups.x_rows : min(x_rows, GB_M);
+    const __amdgpu_buffer_rsrc_t xrs = buf_rsrc(xg, (int64_t)x_rows * K * 2);
     const __amdgpu_buffer_rsrc_t wrs = buf_rsrc(wg, (int64_t)K * nw * 4 - (int64_t)wc0 * 4);
-    const int lg = __builtin_ctz(G);  // G is 32, 64 or 128
     uint32_t xoff[R::A_COPIES];
 #pragma unroll
     for (int i = 0; i < R::A_COPIES; ++i) {
         const int r = (GB_M / WN) * wave + 8 * i + (lane >> 3);
         const int m = min(m0 + r, M - 1);
-        xoff[i] = (uint32_t)(((m - m0) * K + 8 * aseg(r, lane & 7)) * 2);
+        int src = m - m0;
+        if constexpr (GROUPED)
+            if (gather) src = group_source(groups.rows, m, groups.top, groups.x_rows);
+        xoff[i] = (uint32_t)((src * K + 8 * aseg(r, lane & 7)) * 2);
     }
     uint32_t woff;
     {
@@ -409,9 +438,10 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
             }
         return;
     }
-    // (256-column tiles never split K: the launcher refuses such a plan, and
-    // the split path below would only add to their register count)
-    if constexpr (WN == 8) {
+    // (256-column tiles never split K, and neither do rows grouped by expert:
+    // the launchers refuse such a plan, and the split path below would only add to
+    // their register count)
+    if constexpr (WN == 8 || GROUPED) {
         return;
     } else {
     // K split.  The partials move as column quads, 16 bytes each, with the
@@ -564,9 +594,9 @@ template <int DT, bool SYM, int KS, int MT, int AB, int BB, int WN>
 static hipError_t launch_gemm_t(const W4A16Args &a, const W4A16Plan &p, hipStream_t st) {
     dim3 grid(p.tiles_n, p.tiles_m, p.splits);
     const int sep = split_reduce_apart(p.splits, 16 * MT);
-    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, AB, BB, WN>), grid, dim3(64 * WN * KS), 0, st, (const uint16_t *)a.x,
+    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, AB, BB, WN, NoGroups>), grid, dim3(64 * WN * KS), 0, st, (const uint16_t *)a.x,
                        (const uint32_t *)a.qweight, (const uint16_t *)a.scales, (const uint32_t *)a.qzeros,
-                       (uint16_t *)a.y, p.acc, (int)a.M, (int)a.N, (int)a.K, a.G, p.splits, sep);
+                       (uint16_t *)a.y, p.acc, (int)a.M, (int)a.N, (int)a.K, a.G, p.splits, sep, NoGroups{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !sep) return e;
     return launch_w4a16_split_reduce(a, p, (int64_t)p.tiles_n * p.tiles_m, st);
@@ -594,6 +624,32 @@ hipError_t launch_w4a16_gemm(const W4A16Args &a, const W4A16Plan &p, hipStream_t
     }
     if (p.mt == 8) return p.ksplit == 2 ? launch_gemm_ks<2, 8, 2, 3, 4>(a, p, st) : launch_gemm_ks<1, 8, 2, 3, 4>(a, p, st);
     return p.ksplit == 2 ? launch_gemm_ks<2, 16, 2, 3, 4>(a, p, st) : launch_gemm_ks<1, 16, 2, 3, 4>(a, p, st);
+}
+
+// Rows grouped by expert: 128-row tiles, 128 columns (p.wn = 4), or 256-row ones, 256 columns (p.wn = 8).
+template <int DT, bool SYM, int KS, int MT, int WN>
+static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m)),
+                       dim3(64 * WN * KS), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
+                       (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, (uint64_t *)nullptr,
+                       (int)a.M, (int)a.N, (int)a.K, a.G, 1, 0, g);
+    return hipGetLastError();
+}
+
+template <int KS, int MT, int WN>
+static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    const bool sym = a.qzeros == nullptr;
+    if (a.dtype == DT_F16)
+        return sym ? launch_grouped_t<DT_F16, true, KS, MT, WN>(a, p, g, st)
+                   : launch_grouped_t<DT_F16, false, KS, MT, WN>(a, p, g, st);
+    return sym ? launch_grouped_t<DT_BF16, true, KS, MT, WN>(a, p, g, st)
+               : launch_grouped_t<DT_BF16, false, KS, MT, WN>(a, p, g, st);
+}
+
+hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    if (p.splits != 1) return hipErrorInvalidValue;
+    if (p.mt == 8) return launch_grouped_dt<1, 8, 4>(a, p, g, st);
+    return p.wn == 8 ? launch_grouped_dt<1, 16, 8>(a, p, g, st) : hipErrorInvalidValue;
 }
 
 }  // namespace awq4

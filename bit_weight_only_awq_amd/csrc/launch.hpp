@@ -78,6 +78,15 @@ struct W4A8Plan {
     uint64_t *acc;
 };
 
+// Products grouped by expert (moe.hpp): rows offsets[e] .. offsets[e + 1] - 1 are expert e's.
+struct Groups {
+    const int32_t *offsets;  // [E + 1]
+    const int32_t *rows;     // [R] slots, row r of the product reads x[rows[r] / top]; nullptr: x[r]
+    int E, R, top, x_rows;
+    int max_tiles;  // row tiles that any offsets give at most
+};
+struct NoGroups {};
+
 // Workspace of a split-K launch, zero between calls (device.hpp): for the
 // decode GEMV and small W4A8 outputs one 64-bit counting accumulator per
 // output element (M x N); for the GEMM kernels per-tile arrival counters and
@@ -116,6 +125,9 @@ hipError_t launch_w4a16_tiled(const W4A16Args &a, const W4A16Plan &p, hipStream_
 // eight waves up to 32 rows, four 512-register waves at 64
 constexpr int kStreamWaves(int mt) { return mt >= 4 ? 4 : 8; }
 hipError_t launch_w4a16_stream(const W4A16Args &a, const W4A16Plan &p, hipStream_t st);
+// the same two kernels over rows grouped by expert (a.M = the rows of all, p.tiles_m = g.max_tiles)
+hipError_t launch_w4a16_stream_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
+hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
 // K-split reduction of the LDS GEMM and the streaming kernel in a launch of
 // its own (partials after the counters of `tiles` tiles), taken where a
 // tile's partials are large: S splits of `rows`-row tiles, S x rows >= 384.
@@ -173,6 +185,57 @@ struct NormArgs {
     int dtype;
 };
 hipError_t launch_rmsnorm(const NormArgs &n, hipStream_t st);
+
+// Mixture-of-experts routing and the weighted sum of the experts' rows (moe_route.hip).
+constexpr int kMoeMaxExperts = 1024, kMoeMaxTop = 32;
+struct RouteArgs {
+    const void *logits;  // [T, E], dtype (DT_F16, DT_BF16 or 2: fp32)
+    float *weights;      // [T, k]
+    int32_t *experts, *offsets, *rows, *places;  // [T, k], [E + 1], [T k], [T k]
+    int64_t T;
+    int E, k, renormalize, dtype;
+};
+struct RoutePlan {
+    int blocks, block_tokens;  // workgroups (1: one launch), and tokens of each
+    int *counts;               // [blocks, E], two launches only
+};
+hipError_t launch_route(const RouteArgs &g, const RoutePlan &p, hipStream_t st);
+struct CombineArgs {
+    const void *y;          // [R, N]
+    const float *weights;   // [T, k]
+    const int32_t *places;  // [T k]; outside 0 .. R - 1: no row
+    void *out;              // [T, N]
+    int64_t T, R, N;
+    int k, dtype;
+};
+hipError_t launch_combine(const CombineArgs &g, hipStream_t st);
+
+// E4M3 codes with a scale for each block of 128 (fp8_block.hpp).
+hipError_t launch_fp8_block_quant(const void *x, uint8_t *a, float *s, int64_t M, int64_t K, int dtype,
+                                  hipStream_t st);
+struct Fp8BlockArgs {
+    const uint8_t *a;  // [M, K], or the rows that are gathered
+    const uint8_t *w;  // [N, K], or one such matrix an expert
+    const float *sa;   // [M, ceil(K / 128)]
+    const float *sw;   // [ceil(N / 128), ceil(K / 128)], or one such an expert
+    void *y;           // [M, N]
+    int M, N, K, dtype;
+    Groups groups;     // offsets == nullptr: one matrix for all rows
+};
+struct Fp8BlockPlan {
+    int kind;     // 0 streaming kernel, 1 LDS-pipelined
+    int mt;       // streaming: 16-row tiles (1, 2, 4)
+    int tiles_n;  // column tiles
+    int tiles_m;  // row tiles (grouped: at most)
+    int splits;   // workgroups along K
+    size_t workspace_bytes;
+    uint64_t *acc;
+};
+hipError_t launch_fp8_block_stream(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
+hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
+// rows and columns of the LDS-pipelined kernel's tile
+constexpr int kFp8TileRows = 256, kFp8TileCols = 256;
+constexpr int kFp8StreamCols = 64;  // and columns of the streaming kernel's
 
 // Rotary positions and the 4-bit paged cache (kv4.hpp has its layout).
 struct Kv4AppendArgs {

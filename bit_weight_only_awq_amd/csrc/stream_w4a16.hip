@@ -20,6 +20,8 @@
 // them in split order -- so the result does not depend on timing.
 #include "device.hpp"
 #include "launch.hpp"
+#include "moe.hpp"
+#include "split_exchange.hpp"
 #include "w4a16_ops.hpp"
 
 namespace awq4 {
@@ -34,116 +36,6 @@ namespace awq4 {
 template <int COLS>
 __device__ __forceinline__ int lds_col(int c) {
     return (COLS / 2) * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
-}
-
-// The workgroup's M x COLS tile sum -- the SLOTS tiles its waves parked in
-// LDS (ROWS x COLS floats each, COLS a row in the order lds_col gives), added
-// in slot order -- goes out: written directly when the K range is not split
-// (S == 1); otherwise handed over as fp32 partials (one M x N array per
-// split after the tile counters), added in split order -- by the reduction
-// kernel launched next where they are large (sep), else by the last
-// workgroup of the column tile (device.hpp: split_tile_last_atomic), which
-// also clears them and writes the output.  Everything moves as quads of columns (N is a
-// multiple of 8, so a quad never straddles the last column): 8-byte output
-// stores, 16-byte partial loads and stores.  The partials move with the
-// cache policy of agent-scope atomic loads and stores (sc1: through to the
-// device-wide coherence point), as 16-byte buffer accesses -- half the
-// requests of 8-byte atomics; the tail of the kernel is the last workgroups'
-// partial traffic, so its request count sets the tail's length.
-
-template <int NT, int DT, int ROWS, int COLS, int SLOTS>
-__device__ __forceinline__ void tile_store_or_exchange(const float *red, uint16_t *__restrict__ y,
-                                                       uint64_t *__restrict__ ws, int M, int N, int tile, int S,
-                                                       int sep) {
-    constexpr int QR = COLS / 4;         // quads per row
-    constexpr int kQ = ROWS * QR / NT;   // quads per thread, whole tile
-    static_assert(kQ >= 1 && kQ * NT == ROWS * QR, "whole quads per thread");
-    const int n_base = tile * COLS;
-    const int quads = M * QR;
-    // thread t takes quads t, t + NT, ...: its sums of the SLOTS parked tiles
-    // and their 16-byte index in an [M, N] array
-    f32x4 v[kQ];
-    bool ok[kQ];
-    uint32_t at[kQ];
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-        const int qi = threadIdx.x + q * NT;
-        const int r = qi / QR, c = 4 * (qi % QR);
-        ok[q] = qi < quads && n_base + c < N;
-        at[q] = ok[q] ? (uint32_t)(r * (N / 4) + (n_base + c) / 4) : 0u;
-        v[q] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if (ok[q]) {
-            const float *p = red + r * COLS + lds_col<COLS>(c);
-            v[q] = *(const f32x4 *)p;
-#pragma unroll
-            for (int w = 1; w < SLOTS; ++w) v[q] += *(const f32x4 *)(p + w * ROWS * COLS);
-        }
-    }
-    auto out_quad = [&](uint32_t a, f32x4 t) { *(uint2 *)(y + 4 * (size_t)a) = quad_out_bits<DT>(t); };
-    if (S == 1) {
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-            if (ok[q]) out_quad(at[q], v[q]);
-        return;
-    }
-    // split s's partials: a buffer over its M x N floats (under 2^31 bytes,
-    // which the planner ensures)
-    char *const part = (char *)ws + split_counters_bytes(gridDim.x);
-    const uint32_t slot_bytes = (uint32_t)M * (uint32_t)N * 4u;
-    auto split_rsrc = [&](int s) { return buf_rsrc(part + (size_t)s * slot_bytes, slot_bytes); };
-    const int own = blockIdx.y;
-    // sep: the reduction kernel launched next adds the splits (plain stores,
-    // made visible by the kernel boundary); else the column tile's last
-    // workgroup adds them below.
-    {
-        const __amdgpu_buffer_rsrc_t rs = split_rsrc(own);
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-            if (ok[q]) {
-                if (sep) __builtin_amdgcn_raw_buffer_store_b128(bit_as<u32x4>(v[q]), rs, at[q] * 16u, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b128(bit_as<u32x4>(v[q]), rs, at[q] * 16u, 0, kPartCoherent);
-            }
-    }
-    if (sep || !split_tile_last_atomic((uint32_t *)ws + tile, S)) return;
-    // The last workgroup of the column tile: the other splits' partials of
-    // all its quads, kB splits at a time with every load of a batch issued
-    // before the first add (one memory round trip per batch), added in split
-    // order with its own partial (still in registers) in its place.
-    constexpr int kB = 32 / kQ < 1 ? 1 : 32 / kQ > 8 ? 8 : 32 / kQ;
-    f32x4 sum[kQ];
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) sum[q] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int s0 = 0; s0 < S; s0 += kB) {
-        u32x4 b[kQ][kB];
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            const int s = s0 + i;
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) b[q][i] = (u32x4){0u, 0u, 0u, 0u};
-            if (s < S && s != own) {
-                const __amdgpu_buffer_rsrc_t rs = split_rsrc(s);
-#pragma unroll
-                for (int q = 0; q < kQ; ++q)
-                    if (ok[q]) b[q][i] = __builtin_amdgcn_raw_buffer_load_b128(rs, at[q] * 16u, 0, kPartCoherent);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            const int s = s0 + i;
-            if (s >= S) break;
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) sum[q] += s == own ? v[q] : bit_as<f32x4>(b[q][i]);
-        }
-    }
-    for (int s = 0; s < S; ++s) {
-        const __amdgpu_buffer_rsrc_t rs = split_rsrc(s);
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-            if (ok[q]) __builtin_amdgcn_raw_buffer_store_b128((u32x4){0u, 0u, 0u, 0u}, rs, at[q] * 16u, 0, kPartCoherent);
-    }
-#pragma unroll
-    for (int q = 0; q < kQ; ++q)
-        if (ok[q]) out_quad(at[q], sum[q]);
 }
 
 // One chunk's loads: scales and zero points of its group, MT row tiles of X
@@ -262,13 +154,16 @@ __device__ __forceinline__ void prefetch_fence() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int MT, int CS, int WV, int DT, bool SYM>
+// Grp: Groups, for rows grouped by expert (grid x: the column tiles of every
+// row tile that there may be; M: the rows of all experts), or NoGroups.
+template <int MT, int CS, int WV, int DT, bool SYM, class Grp>
 __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__restrict__ x,
                                                           const uint32_t *__restrict__ qw,
                                                           const uint16_t *__restrict__ sc,
                                                           const uint32_t *__restrict__ qz, uint16_t *__restrict__ y,
                                                           uint64_t *__restrict__ ws, int M, int N, int K, int lgG,
-                                                          int sep) {
+                                                          int sep, Grp grp) {
+    constexpr bool GROUPED = !std::is_same_v<Grp, NoGroups>;
     constexpr int ROWS = 16 * MT, COLS = 128;
     // one parked ROWS x COLS tile per wave (128 KB at 4 row tiles)
     __shared__ __attribute__((aligned(16))) float red[WV * ROWS * COLS];
@@ -282,7 +177,23 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
     // to one XCD, so that the line is fetched into one L2 instead of two.
     // (Two word-columns per lane, whole lines per wave, measured slower: the
     // doubled accumulators cost half the waves per CU.)
-    const int tile = tile_of_xcd_order(blockIdx.x, gridDim.x);
+    int tile, row0 = 0, rows = M, cnt_at;
+    if constexpr (GROUPED) {
+        const GroupTile t = group_tile(grp.offsets, grp.E, grp.R, ROWS, (N + COLS - 1) / COLS, grp.max_tiles, blockIdx.x);
+        if (!t.live) return;
+        tile = t.tile_n;
+        row0 = t.row0;
+        rows = min(t.row_end - t.row0, ROWS);
+        cnt_at = t.index;
+        const size_t e = t.expert;
+        qw += e * K * nw;
+        sc += e * (size_t)(K >> lgG) * N;
+        if (!SYM) qz += e * (size_t)(K >> lgG) * nw;
+        if (!grp.rows) x += (size_t)row0 * K;
+    } else {
+        tile = tile_of_xcd_order(blockIdx.x, gridDim.x);
+        cnt_at = tile;
+    }
     const int wcol = tile * 16 + j;
     const int wld = wcol < nw ? wcol : nw - 1;  // past the last word-column: in-bounds words, sums never stored
     // this workgroup's chunks [c_lo, c_hi) and this wave's share of them
@@ -301,7 +212,10 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int row = 16 * mt + j;
-        off.x[mt] = (uint32_t)((row < M ? row : 0) * K + 8 * gq) * 2u;
+        int src = row < rows ? row : 0;
+        if constexpr (GROUPED)
+            if (grp.rows) src = group_source(grp.rows, row0 + src, grp.top, grp.x_rows);
+        off.x[mt] = (uint32_t)(src * K + 8 * gq) * 2u;
     }
 
     f32x4 acc[MT][8];
@@ -366,7 +280,10 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
     // passes with one or two waves at work in each.)
     park(wave);
     __syncthreads();
-    tile_store_or_exchange<64 * WV, DT, ROWS, COLS, WV>(red, y, ws, M, N, tile, S, sep);
+    const size_t at = (size_t)row0 * N;  // (0 where rows are not grouped)
+    tile_store_or_exchange<64 * WV, DT, ROWS, COLS, COLS, WV>(
+        red, lds_col<COLS>, y + at, (uint32_t *)ws + cnt_at, (char *)ws + split_counters_bytes(gridDim.x) + at * 4, (size_t)M * N * 4,
+        rows, N, tile, S, sep);
 }
 
 template <int MT, int CS, int DT, bool SYM>
@@ -374,10 +291,10 @@ static hipError_t launch_stream_t(const W4A16Args &a, const W4A16Plan &p, hipStr
     constexpr int WV = kStreamWaves(MT);
     if (p.waves != WV || (p.splits > 1 && p.acc == nullptr)) return hipErrorInvalidValue;
     const int sep = split_reduce_apart(p.splits, 16 * MT);
-    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM>), dim3(p.tiles_n, p.splits), dim3(64 * WV), 0, st,
+    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM, NoGroups>), dim3(p.tiles_n, p.splits), dim3(64 * WV), 0, st,
                        (const uint16_t *)a.x, (const uint32_t *)a.qweight, (const uint16_t *)a.scales,
                        (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc, (int)a.M, (int)a.N, (int)a.K,
-                       __builtin_ctz((unsigned)a.G), sep);
+                       __builtin_ctz((unsigned)a.G), sep, NoGroups{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !sep) return e;
     return launch_w4a16_split_reduce(a, p, p.tiles_n, st);
@@ -400,6 +317,41 @@ hipError_t launch_w4a16_stream(const W4A16Args &a, const W4A16Plan &p, hipStream
         case 22: return launch_stream_dt<2, 2>(a, p, st);
         case 41: return launch_stream_dt<4, 1>(a, p, st);
         case 42: return launch_stream_dt<4, 2>(a, p, st);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+// Rows grouped by expert.  (The splits are always added by the last workgroup of a tile: a
+// reduction launch would have to pass over every row that an expert might have had.)
+template <int MT, int CS, int DT, bool SYM>
+static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    constexpr int WV = kStreamWaves(MT);
+    if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), p.splits),
+                       dim3(64 * WV), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
+                       (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc, (int)a.M,
+                       (int)a.N, (int)a.K, __builtin_ctz((unsigned)a.G), 0, g);
+    return hipGetLastError();
+}
+
+template <int MT, int CS>
+static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    const bool sym = a.qzeros == nullptr;
+    if (a.dtype == DT_F16)
+        return sym ? launch_grouped_t<MT, CS, DT_F16, true>(a, p, g, st)
+                   : launch_grouped_t<MT, CS, DT_F16, false>(a, p, g, st);
+    return sym ? launch_grouped_t<MT, CS, DT_BF16, true>(a, p, g, st)
+               : launch_grouped_t<MT, CS, DT_BF16, false>(a, p, g, st);
+}
+
+hipError_t launch_w4a16_stream_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
+    switch (p.mt * 10 + p.cs) {
+        case 11: return launch_grouped_dt<1, 1>(a, p, g, st);
+        case 12: return launch_grouped_dt<1, 2>(a, p, g, st);
+        case 21: return launch_grouped_dt<2, 1>(a, p, g, st);
+        case 22: return launch_grouped_dt<2, 2>(a, p, g, st);
+        case 41: return launch_grouped_dt<4, 1>(a, p, g, st);
+        case 42: return launch_grouped_dt<4, 2>(a, p, g, st);
         default: return hipErrorInvalidValue;
     }
 }

@@ -563,6 +563,179 @@ def kv4_attention(q, cache, tables, lens, scale: float | None = None, cu_q=None,
     return out
 
 
+# ----------------------------------------------------------------------------- mixture of experts, block-scaled FP8
+
+_LOGITS = {**_F16, torch.float32: L.AWQ_DTYPE_F32}
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _on_device(index: int, fn, *args):
+    """fn(*args) with device `index` current (the planners ask for the current device)."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _need_gpu(t, dtypes, dims, what):
+    if not t.is_cuda:
+        raise ValueError("all tensors must be on a CUDA (HIP) device")
+    if t.dtype not in dtypes or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, of {dims} dimensions and one of "
+                         f"{', '.join(str(d)[6:] for d in dtypes)}")
+
+
+def moe_route(logits, top_k: int, renormalize: bool = False, out=None):
+    """Routing of logits [T, E] (fp16, bf16 or fp32): (weights fp32 [T, top_k],
+    experts int32 [T, top_k], offsets int32 [E + 1], rows int32 [T top_k],
+    places int32 [T top_k]), new or those of `out`.  weights: the softmax over
+    all experts, or over the chosen ones; offsets and rows: what the products
+    grouped by expert take; places: what moe_combine takes."""
+    _need_gpu(logits, _LOGITS, 2, "logits")
+    T, E = logits.shape
+    dev, index = logits.device, logits.get_device()
+    shapes = ((T, top_k), (T, top_k), (E + 1,), (T * top_k,), (T * top_k,))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.int32 if i else torch.float32, device=dev) for i, s in enumerate(shapes))
+    else:
+        for i, (t, s) in enumerate(zip(out, shapes, strict=True)):
+            _tensor(t, s, torch.int32 if i else torch.float32, index, "weights, experts, offsets, rows and places")
+    lib = L.lib()
+    need = lib.awq_moe_route_workspace_bytes(T, E, top_k)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    status = lib.awq_moe_route(logits.data_ptr(), *[t.data_ptr() for t in out], T, E, top_k, int(renormalize),
+                               _LOGITS[logits.dtype], _ptr(ws), need, _raw_stream(index))
+    if status:
+        L.check("awq_moe_route", status)
+    return out
+
+
+def moe_combine(y, weights, places, out=None):
+    """[T, N]: the sum over j of weights[t, j] y[places[t top_k + j]], y [R, N] in
+    the order of the experts, weights and places from moe_route."""
+    _need_gpu(y, _F16, 2, "y")
+    index, (R, N) = y.get_device(), y.shape
+    T, k = weights.shape
+    _tensor(weights, (T, k), torch.float32, index, "weights")
+    _tensor(places, (T * k,), torch.int32, index, "places")
+    if out is None:
+        out = torch.empty(T, N, dtype=y.dtype, device=y.device)
+    else:
+        _tensor(out, (T, N), y.dtype, index, "out")
+    status = L.lib().awq_moe_combine(y.data_ptr(), weights.data_ptr(), places.data_ptr(), out.data_ptr(), T, R, N, k,
+                                     _F16[y.dtype], _raw_stream(index))
+    if status:
+        L.check("awq_moe_combine", status)
+    return out
+
+
+def _grouped(x_rows, experts, offsets, rows, index):
+    """Checks of a plan; the rows of the product and the pointers of offsets and rows."""
+    _tensor(offsets, (experts + 1,), torch.int32, index, "offsets")
+    if rows is None:
+        return x_rows, offsets.data_ptr(), None
+    _tensor(rows, rows.shape[:1], torch.int32, index, "rows")
+    return rows.shape[0], offsets.data_ptr(), rows.data_ptr()
+
+
+def moe_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, top_k: int = 1, group_size: int = 128, out=None):
+    """The W4A16 layer with a matrix per expert: qweight int32 [E, K, N / 8], scales
+    [E, K / G, N], qzeros int32 [E, K / G, N / 8] or None.  Expert e takes rows
+    offsets[e] .. offsets[e + 1] - 1 of the product; row r reads
+    x[rows[r] // top_k] (rows of moe_route, x one row a token), or x[r] without
+    rows.  [rows, N]; those behind the last expert's are not written."""
+    _need_gpu(x, _F16, 2, "x")
+    index, (x_rows, K) = x.get_device(), x.shape
+    _need_gpu(qweight, (torch.int32,), 3, "qweight")
+    E, _, nw = qweight.shape
+    N = 8 * nw
+    _tensor(qweight, (E, K, nw), torch.int32, index, "qweight")
+    _tensor(scales, (E, K // group_size, N), x.dtype, index, "scales")
+    if qzeros is not None:
+        _tensor(qzeros, (E, K // group_size, nw), torch.int32, index, "qzeros")
+    R, offsets_ptr, rows_ptr = _grouped(x_rows, E, offsets, rows, index)
+    if out is None:
+        out = torch.empty(R, N, dtype=x.dtype, device=x.device)
+    else:
+        _tensor(out, (R, N), x.dtype, index, "out")
+    lib = L.lib()
+    need = _on_device(index, lib.awq_moe_gemm_w4a16_workspace_bytes, R, E, N, K, group_size)
+    stream = _raw_stream(index)
+    ws, ws_bytes = WORKSPACE.of_stream(index, stream, need) if need else (None, 0)
+    status = lib.awq_moe_gemm_w4a16(x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr(qzeros), offsets_ptr,
+                                    rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, group_size, _F16[x.dtype], ws,
+                                    ws_bytes, stream)
+    if status:
+        L.check("awq_moe_gemm_w4a16", status)
+    return out
+
+
+def quant_act_fp8_block(x, a=None, s=None):
+    """E4M3 codes of fp16 or bf16 activations with a scale for each run of 128
+    values of a row -> (codes uint8 [M, K], s fp32 [M, ceil(K / 128)])."""
+    _need_gpu(x, _F16, 2, "x")
+    M, K = x.shape
+    index, blocks = x.get_device(), -(-K // 128)
+    if a is None:
+        a = torch.empty(M, K, dtype=torch.uint8, device=x.device)
+    else:
+        _tensor(a, (M, K), torch.uint8, index, "a")
+    if s is None:
+        s = torch.empty(M, blocks, dtype=torch.float32, device=x.device)
+    else:
+        _tensor(s, (M, blocks), torch.float32, index, "s")
+    status = L.lib().awq_fp8_block_quant_act(x.data_ptr(), a.data_ptr(), s.data_ptr(), M, K, _F16[x.dtype],
+                                             _raw_stream(index))
+    if status:
+        L.check("awq_fp8_block_quant_act", status)
+    return a, s
+
+
+def _fp8_block(a, w, sa, sw, plan, top_k, dtype, out):
+    """Checks and call of the block-scaled products; plan: (offsets, rows), or None for one matrix."""
+    _need_gpu(a, _E4M3, 2, "a")
+    index, (x_rows, K) = a.get_device(), a.shape
+    _need_gpu(w, _E4M3, 2 if plan is None else 3, "w")
+    E, N = (0, w.shape[0]) if plan is None else w.shape[:2]
+    lead = w.shape[:-2]
+    _tensor(w, (*lead, N, K), w.dtype, index, "w")
+    _tensor(sa, (x_rows, -(-K // 128)), torch.float32, index, "sa")
+    _tensor(sw, (*lead, -(-N // 128), -(-K // 128)), torch.float32, index, "sw")
+    if dtype not in _F16:
+        raise ValueError("the output must be fp16 or bf16")
+    R, offsets_ptr, rows_ptr = (x_rows, None, None) if plan is None else _grouped(x_rows, E, *plan, index)
+    if out is None:
+        out = torch.empty(R, N, dtype=dtype, device=a.device)
+    else:
+        _tensor(out, (R, N), dtype, index, "out")
+    lib = L.lib()
+    need = _on_device(index, lib.awq_fp8_block_gemm_workspace_bytes, R, E, N, K)
+    stream = _raw_stream(index)
+    ws, ws_bytes = WORKSPACE.of_stream(index, stream, need) if need else (None, 0)
+    if plan is None:
+        status = lib.awq_fp8_block_gemm(a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(), out.data_ptr(), R, N,
+                                        K, _F16[dtype], ws, ws_bytes, stream)
+    else:
+        status = lib.awq_moe_fp8_block_gemm(a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(), offsets_ptr,
+                                            rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, _F16[dtype], ws,
+                                            ws_bytes, stream)
+    if status:
+        L.check("awq_fp8_block_gemm" if plan is None else "awq_moe_fp8_block_gemm", status)
+    return out
+
+
+def gemm_fp8_block(a, w, sa, sw, dtype=torch.bfloat16, out=None):
+    """y [M, N] = codes a [M, K] times codes w [N, K] (E4M3, uint8 or float8_e4m3fn),
+    with scales sa [M, ceil(K / 128)] and sw [ceil(N / 128), ceil(K / 128)]."""
+    return _fp8_block(a, w, sa, sw, None, 1, dtype, out)
+
+
+def moe_gemm_fp8_block(a, w, sa, sw, offsets, rows=None, top_k: int = 1, dtype=torch.bfloat16, out=None):
+    """gemm_fp8_block with a matrix per expert, w [E, N, K] and sw [E, ., .]; offsets,
+    rows and top_k as for moe_gemm_w4a16."""
+    return _fp8_block(a, w, sa, sw, (offsets, rows), top_k, dtype, out)
+
+
 # ----------------------------------------------------------------------------- measurement helper
 
 STREAM_SINK_WORDS = 8192

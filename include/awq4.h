@@ -8,7 +8,9 @@
  * (per-token int8 activations x symmetric int4 weights, exact int32
  * accumulation, per-token and per-channel (optionally per-group) scales).
  * Around those layers it has RMS norm with the residual's addition and an
- * 8-bit output, and attention over a paged key/value cache in 4 bits.
+ * 8-bit output, and attention over a paged key/value cache in 4 bits; for
+ * mixtures of experts the routing and the same products grouped by expert; and
+ * products of E4M3 activations and weights with a scale for each block of 128.
  *
  * Sources (web pages, cited by title and passage):
  *  [P1] vLLM pull request "Speed up AWQ 2.5x with updated kernel": the list of
@@ -31,7 +33,7 @@
  *  - All tensors are dense, row-major and contiguous, in device memory owned
  *    by the caller (awq_kv4_append takes token strides).  Device pointers must
  *    be 16-byte aligned (AWQ_EALIGN), those of the kv4 calls' index arrays
- *    aligned to their type.
+ *    and of the products' offsets and rows aligned to their type.
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *    Work is enqueued on it; no entry point synchronises or allocates device
  *    memory, so all of them are asynchronous and safe to call from several
@@ -64,6 +66,7 @@ extern "C" {
 /* Activation / scale / output dtypes. */
 #define AWQ_DTYPE_F16 0
 #define AWQ_DTYPE_BF16 1
+#define AWQ_DTYPE_F32 2 /* logits of awq_moe_route only */
 
 /* Packed layouts for awq_pack / awq_unpack. */
 #define AWQ_LAYOUT_N8 0  /* AWQ: uint8 vals [rows, cols] in 0..15 -> int32 [rows, cols/8];
@@ -553,6 +556,119 @@ int awq_kv4_attention(const void *q, const int32_t *cache, const int32_t *tables
  * none, or for invalid arguments). */
 size_t awq_kv4_attention_workspace_bytes(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t head_dim,
                                          int64_t max_kv);
+
+/*
+ * Mixture of experts: routing, products grouped by expert, and their weighted
+ * sum.  A token t takes part in k products; slot t k + j is its j-th.  The products'
+ * rows lie in the order of their experts: expert e has rows offsets[e] ..
+ * offsets[e+1] - 1, which the device alone knows, so no call waits for them.
+ *
+ * awq_moe_route -- each token's k experts, their weights, and the plan.
+ * Of the logits l[t, .] the k largest, larger ones first, equal ones by expert (-0 is
+ * 0; +infinity counts as the largest finite binary32 number; -infinity and NaN
+ * are never chosen).  With m the largest,
+ *   weight = exp(l - m) / sum_e exp(l_e - m)
+ * over all experts that could be chosen, or over the chosen ones (renormalize);
+ * fp32.  A token with fewer than k such experts has expert -1 and weight 0 in
+ * the places left, and no rows for them.
+ *   logits:  device [T, E] in dtype (AWQ_DTYPE_F32 too).
+ *   weights: device fp32 [T, k];  experts: device int32 [T, k].
+ *   offsets: device int32 [E + 1]: the rows of each expert.
+ *   rows:    device int32 [T k]: the slot of each row -- by expert, then by slot;
+ *            -1 behind the last.
+ *   places:  device int32 [T k]: the row of each slot, or -1.
+ *   1 <= k <= min(E, 32), E <= 1024, T <= 2^20, T k <= 2^24.  T == 0 writes offsets.
+ *   Workspace: awq_moe_route_workspace_bytes of any contents, not left zero:
+ *   not the one that the products share.
+ * Errors: AWQ_EINVAL, AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
+ */
+int awq_moe_route(const void *logits, float *weights, int32_t *experts, int32_t *offsets, int32_t *rows,
+                  int32_t *places, int64_t T, int64_t E, int64_t k, int renormalize, int dtype, void *workspace,
+                  size_t workspace_bytes, void *stream);
+size_t awq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
+
+/*
+ * awq_moe_gemm_w4a16 -- y[r] = x[row of r] . dequant(weights of r's expert), the
+ * layer of awq_gemm_w4a16 with a matrix per expert.
+ *   x:       device [x_rows, K] (dtype).
+ *   qweight: device int32 [E, K, N/8], scales [E, K/G, N], qzeros int32
+ *            [E, K/G, N/8] or NULL, each expert's as for awq_gemm_w4a16.
+ *   offsets: device int32 [E + 1], from 0, not falling, at most R.  (Whatever
+ *            they hold, nothing outside the tensors is read or written.)
+ *   rows:    device int32 [R]: row r reads x[rows[r] / top_k] (the plan's rows:
+ *            the first product of a layer, x one row a token); or NULL: it reads
+ *            x[r] (x_rows == R; the second one, on rows in the plan's order).  An entry
+ *            that names no row of x reads row 0.
+ *   y:       device [R, N]; rows from offsets[E] on are not written.
+ *   G, K, N as for awq_gemm_w4a16; E <= 1024, R <= 2^24, 1 <= top_k <= 32.  With
+ *   rows, x is under 2^31 bytes (AWQ_EUNSUPPORTED).  One kernel takes the whole call, by
+ *   R / E: rows per expert, if all had alike.
+ * Numerics: up to 48 rows an expert (R over the experts that R rows reach on
+ * average) as awq_gemm_w4a16 for M <= 64, else as for M > 64.
+ * Workspace: as for the GEMMs (shared, zero before and after each call).  R == 0
+ * is a no-op that returns AWQ_OK.
+ * Errors: AWQ_EINVAL, AWQ_EUNSUPPORTED, AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
+ */
+int awq_moe_gemm_w4a16(const void *x, const int32_t *qweight, const void *scales, const int32_t *qzeros,
+                       const int32_t *offsets, const int32_t *rows, void *y, int64_t R, int64_t x_rows, int64_t top_k,
+                       int64_t E, int64_t N, int64_t K, int group_size, int dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+size_t awq_moe_gemm_w4a16_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K, int group_size);
+
+/*
+ * awq_moe_combine -- out[t] = act( sum_j weights[t,j] y[places[t k + j]] ), summed
+ * by fp32 FMAs in the order of j; a place outside 0 .. R - 1 (-1: no expert)
+ * adds nothing.
+ *   y: device [R, N];  weights: device fp32 [T, k];  places: device int32 [T k];
+ *   out: device [T, N], not overlapping y.  N % 8 == 0, k <= 32.
+ * T == 0 is a no-op that returns AWQ_OK.
+ * Errors: AWQ_EINVAL, AWQ_EALIGN, AWQ_EHIP.
+ */
+int awq_moe_combine(const void *y, const float *weights, const int32_t *places, void *out, int64_t T, int64_t R,
+                    int64_t N, int64_t k, int dtype, void *stream);
+
+/*
+ * E4M3 (as for INT4-FP8 above) with one scale for each block of 128 along K.
+ *
+ * awq_fp8_block_quant_act -- activations, one scale for each run of 128 values
+ * of a row (the last run of a row may be shorter):
+ *   s[m,b] = fl32( max |x| / 448 ),  a = e4m3( clamp( fl32(x / s), -448, 448 ) )
+ * A run whose s is 0 has codes 0; one that holds a NaN or an infinity has an s
+ * that is not finite and codes 0, which makes its row of a product NaN.
+ *   x: device fp16/bf16 [M, K] (dtype); a: device uint8 [M, K]; s: device fp32
+ *   [M, ceil(K/128)].  K % 16 == 0.  M == 0 is a no-op that returns AWQ_OK.
+ * Errors: AWQ_EINVAL, AWQ_EALIGN, AWQ_EHIP.
+ */
+int awq_fp8_block_quant_act(const void *x, uint8_t *a, float *s, int64_t M, int64_t K, int dtype, void *stream);
+
+/*
+ * awq_fp8_block_gemm -- y[m,n] = act( sum_b sa[m,b] sw[n/128,b]
+ *                                     sum_{k in b} value(a[m,k]) value(w[n,k]) )
+ *   a, sa: from awq_fp8_block_quant_act.
+ *   w:     device uint8 [N, K]: E4M3 codes, a row per output (finite ones).
+ *   sw:    device fp32 [ceil(N/128), ceil(K/128)].
+ *   y:     device [M, N] fp16/bf16 (dtype).
+ *   K % 16 == 0, N % 8 == 0, N K under 2^31 (AWQ_EUNSUPPORTED), M <= 2^24.
+ * Numerics: a block's sum of 128 products comes from the fp8 matrix cores in
+ * fp32; the blocks are added by fp32 FMAs, times fl32(sa sw).  Not exact: the
+ * matrix cores line up the products of four consecutive k with the one of the largest
+ * exponent, and drop what lies below 2^-13 of it.  (On random data that is 6 10^-5
+ * of the result's norm, a third of fp16's own rounding.)
+ * Workspace: as for the GEMMs (E = 0 in awq_fp8_block_gemm_workspace_bytes).  M == 0 is a
+ * no-op that returns AWQ_OK.
+ * Errors: AWQ_EINVAL, AWQ_EUNSUPPORTED, AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
+ *
+ * awq_moe_fp8_block_gemm -- the same with a matrix per expert: w [E, N, K], sw
+ * [E, ceil(N/128), ceil(K/128)]; offsets, rows, R, x_rows, top_k and y as for
+ * awq_moe_gemm_w4a16, the gathered rows' scales with them.
+ */
+int awq_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
+                       int64_t N, int64_t K, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+int awq_moe_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw,
+                           const int32_t *offsets, const int32_t *rows, void *y, int64_t R, int64_t x_rows,
+                           int64_t top_k, int64_t E, int64_t N, int64_t K, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t awq_fp8_block_gemm_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K);
 
 /*
  * awq_stream_read -- measurement helper, not a step of the method: reads
