@@ -746,6 +746,13 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     Fp8BlockPlan p{};
     const double live = E ? live_experts(M, E) : 1.0, avg = (double)M / live;
     auto row_tiles = [&](int64_t rows) { return E ? group_tiles(M, E, rows) : cdiv(M, rows); };
+    if (avg > 64) {
+        p.kind = 1;
+        p.splits = 1;
+        p.tiles_n = (int)cdiv(N, kFp8TileCols);
+        p.tiles_m = (int)row_tiles(kFp8TileRows);
+        return p;
+    }
     p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
     p.tiles_n = (int)cdiv(N, kFp8StreamCols);
     p.tiles_m = (int)row_tiles(16 * p.mt);
@@ -769,7 +776,8 @@ static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, co
     if (p.splits > 1) p.acc = static_cast<uint64_t *>(workspace);
     groups.max_tiles = p.tiles_m;
     const Fp8BlockArgs g{a, w, sa, sw, y, (int)M, (int)N, (int)K, dtype, groups};
-    return hip_status(launch_fp8_block_stream(g, p, static_cast<hipStream_t>(stream)));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return hip_status(p.kind == 1 ? launch_fp8_block_gemm(g, p, st) : launch_fp8_block_stream(g, p, st));
 }
 
 }  // namespace awq4
