@@ -750,7 +750,8 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
         p.kind = 1;
         p.splits = 1;
         p.tiles_n = (int)cdiv(N, kFp8TileCols);
-        p.tiles_m = (int)row_tiles(kFp8TileRows);
+        p.mt = avg <= 192 ? 2 : 4;
+        p.tiles_m = (int)row_tiles(64 * p.mt);
         return p;
     }
     p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;

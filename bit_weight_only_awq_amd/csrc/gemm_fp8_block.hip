@@ -1,46 +1,48 @@
 // gemm_fp8_block.hip -- block-scaled E4M3 products of many rows (fp8_block.hpp
 // has the arithmetic): tiles through LDS.
 //
-// A workgroup of 8 waves has BN outputs n and BM tokens, a wave NT x MT tiles of
-// 16 x 16 of them.  A stage is one block of 128 k: the rows of both matrices (128
-// bytes of each) and the block's scales are copied straight into LDS, one
-// stage ahead.  The matrix cores' sum of a tile and block is scaled and added
-// to the running sums two matrix-core instructions later, so that a wave
-// issues the next ones while it waits for none: four FMAs beside every
-// instruction of 32 cycles.
+// A workgroup of 8 waves has BN = 256 outputs n and BM = 256 or 128 tokens, a wave
+// NT x MT tiles of 16 x 16 of them.  A stage is one block of 128 k: 128 bytes of
+// each row of both matrices, copied straight into one of two LDS slots.
+//
+// One barrier a stage, and no wave waits for LDS behind it: a wave holds all NT weight
+// operands of the stage and goes through its tokens 16 at a time, the
+// operand of the next 16 being read meanwhile.  When the last 16 are in
+// registers, nothing of the stage is left to read: the barrier stands there.
+// Behind it the slot takes the copies of the stage after the next (in flight for a whole
+// stage), and each weight operand is replaced by the next stage's as soon as its last
+// matrix-core instruction is issued.  (With the barrier at the stage's end, where the first
+// operands of all waves are read at once while the matrix cores wait: 1566
+// TFLOP/s at 4096 x 14336 x 4096 against 1850.  Two groups of waves taking turns at the
+// matrix cores: 1480 -- one wave a SIMD cannot keep them busy beside its own FMAs.)
+// The copies are issued one beside each of the instructions behind the barrier (all at once:
+// 1750).  The scales of four blocks are copied together, 16 bytes a row
+// (each block's for itself, 256 rows in 256 cache lines: 6 % of the time).
+//
+// The matrix cores' sum of a tile is added to the running ones LAG instructions later.  The
+// sum's FMAs take issue slots from the matrix cores: beside four FMAs an instruction of 32 cycles
+// takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2400 are reached
+// where the tiles are as many as the CUs (4096 x 4096 x 14336), the rest goes to
+// the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).
 #include "fp8_block.hpp"
 
 namespace awq4 {
 
-// 4 bytes a lane, as dma16_buf
-__device__ __forceinline__ void dma4_buf(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void *dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds_address(dst)), "v"(voff), "s"(r), "s"(soff)
-                 : "memory", "m0");
-}
-
 // 16-byte segment s of row r is stored at s ^ blk_swz(r): the 16 rows of an
 // operand read lie on 16 different bank groups of 256 bytes.
-__device__ __forceinline__ int blk_swz(int r) { return (r ^ (r >> 3)) & 7; }
+__device__ __forceinline__ int blk_swz(int j) { return (j ^ (j >> 3)) & 7; }  // j = r & 15
 
-template <int BM, int BN, int WM, int RING>
-struct Fp8Lds {
-    static constexpr int WN = 8 / WM;
-    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
-    static constexpr int W_BYTES = BN * kBlk, A_BYTES = BM * kBlk;
-    static constexpr int S_BYTES = BM * 4 + 16;  // token scales, then the weights' (up to 4)
-    static constexpr int STAGE = W_BYTES + A_BYTES + S_BYTES;
-    static constexpr int LDS = RING * STAGE;
-    static constexpr int W_COPIES = BN / 64, A_COPIES = BM / 64;  // 1 KB copies of a wave and stage
-    static_assert(LDS <= 163840 && BN % 128 == 0 && BM % 64 == 0 && (BN / WN) % 16 == 0, "fits");
-};
+constexpr int kFp8Lag = 3;
 
-template <int DT, int BM, int BN, int WM, int RING>
+template <int DT, int NT, int MT, int WN>
 __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
-    using L = Fp8Lds<BM, BN, WM, RING>;
-    constexpr int NT = L::NT, MT = L::MT;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[L::LDS];
+    constexpr int WM = 8 / WN, BN = 16 * NT * WN, BM = 16 * MT * WM;
+    constexpr int W_BYTES = BN * kBlk, A_BYTES = BM * kBlk, STAGE = W_BYTES + A_BYTES;
+    constexpr int S_BYTES = BM * 16 + 64, LDS = 2 * (STAGE + S_BYTES);
+    constexpr int W_COPIES = BN / 64, A_COPIES = BM / 64, COPIES = W_COPIES + A_COPIES;
+    static_assert(MT % 2 == 0 && kBlk % (16 * NT) == 0 && BM / 64 <= 4 && BN / kBlk <= 4 && LDS <= 163840, "fits");
+    static_assert(COPIES <= NT && COPIES < 16, "a copy beside each weight operand; the wait's field");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[LDS];
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
@@ -48,109 +50,124 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     if (!t.live) return;
     const int K = g.K, N = g.N, blocks = (K + kBlk - 1) / kBlk;
     const int n0 = t.tile_n * BN;
-
-    // rows past the matrices, and k past K, are past the buffers: they read as zero
     const __amdgpu_buffer_rsrc_t wr = buf_rsrc(t.w + (size_t)n0 * K, (int64_t)min(BN, N - n0) * K);
     const __amdgpu_buffer_rsrc_t ar = buf_rsrc(t.a, (int64_t)t.a_rows * K);
-    const __amdgpu_buffer_rsrc_t sr = buf_rsrc(t.sa, (int64_t)t.a_rows * blocks * 4);
-    const __amdgpu_buffer_rsrc_t vr =
-        buf_rsrc(t.sw, (int64_t)((N + kBlk - 1) / kBlk) * blocks * 4);
-    // Copies: copy i of wave w takes rows 8 (w C + i) + lane / 8, lane % 8 being the stored segment.
+    // waves 0 .. BM / 64 - 1 copy the tokens' scales, wave 4 the weights'
+    const bool row_scales = wave < BM / 64, scales = row_scales || wave == 4;
+    const __amdgpu_buffer_rsrc_t sr = row_scales
+        ? buf_rsrc(t.sa, (int64_t)t.a_rows * blocks * 4)
+        : buf_rsrc(t.sw, (int64_t)((N + kBlk - 1) / kBlk) * blocks * 4);
+    // Copies of 1 KB: 8 rows from row 8 c, lane % 8 being the stored segment of row 8 c + lane / 8.  Rows past
+    // the matrices, and segments past K, are past the buffers: they read as zero.
     const int seg0 = (lane & 7) ^ (lane >> 3);
-    uint32_t wo[L::W_COPIES], ao[L::A_COPIES], so = kOut;
+    uint32_t off[COPIES], so = kOut;
 #pragma unroll
-    for (int i = 0; i < L::W_COPIES; ++i) {
-        const int c = wave * L::W_COPIES + i;
-        wo[i] = (uint32_t)((8 * c + (lane >> 3)) * K + 16 * (seg0 ^ (c & 7)));
+    for (int i = 0; i < W_COPIES; ++i) {
+        const int c = wave * W_COPIES + i;
+        off[i] = (uint32_t)((8 * c + (lane >> 3)) * K + 16 * (seg0 ^ (c & 1)));
     }
 #pragma unroll
-    for (int i = 0; i < L::A_COPIES; ++i) {
-        const int c = wave * L::A_COPIES + i;
+    for (int i = 0; i < A_COPIES; ++i) {
+        const int c = wave * A_COPIES + i;
         const int src = fp8_source(g, t, 8 * c + (lane >> 3));
-        ao[i] = src < 0 ? kOut : (uint32_t)src * (uint32_t)K + 16 * (seg0 ^ (c & 7));
+        off[W_COPIES + i] = src < 0 ? kOut : (uint32_t)src * (uint32_t)K + 16 * (seg0 ^ (c & 1));
     }
-    const bool scale_wave = wave < BM / 64, weight_wave = wave == 7;
-    static_assert(BM / 64 <= 7, "wave 7 copies the weights' scales");
-    if (scale_wave) {
+    if (row_scales) {
         const int src = fp8_source(g, t, 64 * wave + lane);
         if (src >= 0) so = (uint32_t)src * (uint32_t)blocks * 4u;
-    } else if (weight_wave && lane < BN / kBlk) {
+    } else if (wave == 4 && lane < BN / kBlk) {
         so = (uint32_t)((n0 / kBlk + lane) * blocks) * 4u;
     }
-    auto copy = [&](int st, int slot) {
-        unsigned char *const base = lds + slot * L::STAGE;
-        const uint32_t k = (uint32_t)st * kBlk;
-        unsigned char *const w = base + wave * L::W_COPIES * 1024, *const a = base + L::W_BYTES + wave * L::A_COPIES * 1024;
-        const int left = (K - st * kBlk) / 16;  // 16-byte segments of a row that are left
-        if (left >= 8) {
-#pragma unroll
-            for (int i = 0; i < L::W_COPIES; ++i) dma16_buf(wr, wo[i], k, w + i * 1024);
-#pragma unroll
-            for (int i = 0; i < L::A_COPIES; ++i) dma16_buf(ar, ao[i], k, a + i * 1024);
-        } else {
-#pragma unroll
-            for (int i = 0; i < L::W_COPIES; ++i)
-                dma16_buf(wr, (seg0 ^ ((wave * L::W_COPIES + i) & 7)) < left ? wo[i] : kOut, k, w + i * 1024);
-#pragma unroll
-            for (int i = 0; i < L::A_COPIES; ++i)
-                dma16_buf(ar, (seg0 ^ ((wave * L::A_COPIES + i) & 7)) < left ? ao[i] : kOut, k, a + i * 1024);
-        }
-        unsigned char *const s = base + L::W_BYTES + L::A_BYTES;
-        if (scale_wave) dma4_buf(sr, so, (uint32_t)st * 4u, s + wave * 256);
-        else if (weight_wave && lane < BN / kBlk) dma4_buf(vr, so, (uint32_t)st * 4u, s + BM * 4);
+    // copy i of stage st, whose rows have `left` 16-byte segments
+    auto copy1 = [&](int st, int left, auto ic) {
+        constexpr int i = decltype(ic)::value;
+        constexpr bool isw = i < W_COPIES;
+        unsigned char *const dst = lds + (st & 1) * STAGE + (isw ? 0 : W_BYTES) +
+                                   (wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES)) * 1024;
+        const int c = wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES);
+        dma16_buf(isw ? wr : ar, (seg0 ^ (c & 1)) < left ? off[i] : kOut, (uint32_t)st * kBlk, dst);
     };
+    auto copy_scales = [&](int st) {
+        if (scales && (st & 3) == 0 && st < blocks && (row_scales || lane < BN / kBlk))
+            dma16_buf(sr, so, (uint32_t)st * 4u, lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
+    };
+    auto left_of = [&](int st) { return st < blocks ? min((K - st * kBlk) / 16, 8) : 0; };
 
     f32x4 acc[NT][MT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-
-    // operand of 16 rows from row r0: segments 2 gq and 2 gq + 1 of row r0 + j
-    auto operand = [&](const unsigned char *base, int r0) {
-        const int r = r0 + j;
-        const unsigned char *p = base + r * kBlk;
-        return operand32(*(const u32x4 *)(p + 16 * ((2 * gq) ^ blk_swz(r))),
-                         *(const u32x4 *)(p + 16 * ((2 * gq + 1) ^ blk_swz(r))));
+    const int a0 = j * kBlk + 16 * ((2 * gq) ^ blk_swz(j)), a1 = j * kBlk + 16 * ((2 * gq + 1) ^ blk_swz(j));
+    auto operand = [&](int slot, int first, int tile) {
+        const unsigned char *p = lds + slot * STAGE + first + tile * 16 * kBlk;
+        return operand32(*(const u32x4 *)(p + a0), *(const u32x4 *)(p + a1));
     };
-    auto stage = [&](int st, int slot) {
-        if (st + 1 < blocks) copy(st + 1, slot ^ 1);
-        const unsigned char *const W = lds + slot * L::STAGE, *const A = W + L::W_BYTES, *const S = A + L::A_BYTES;
-        i32x8 b[MT], w[3];
+    auto row_scale = [&](int st, int m) {
+        return *(const float *)(lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + 16 * (16 * (wm * MT + m) + j) + 4 * (st & 3));
+    };
+    auto col_scale = [&](int st) {
+        return *(const float *)(lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + BM * 16 + 16 * (wn * NT * 16 / kBlk) + 4 * (st & 3));
+    };
+    {
+        const int l0 = left_of(0), l1 = left_of(1);
+        copy_scales(0);
+        static_for<COPIES>([&](auto ic) { copy1(0, l0, ic); });
+        static_for<COPIES>([&](auto ic) { copy1(1, l1, ic); });
+        __builtin_amdgcn_s_waitcnt(0x0F70 | COPIES);  // stage 0's have landed
+        asm volatile("s_barrier" ::: "memory");
+    }
+    i32x8 w[NT], b[2];
+    float sa[MT], sw;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) w[i] = operand(0, 0, wn * NT + i);
+    b[0] = operand(0, W_BYTES, wm * MT);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sa[m] = row_scale(0, m);
+    sw = col_scale(0);
+    for (int st = 0; st < blocks; ++st) {
+        const int slot = st & 1, left = left_of(st + 2);
+        constexpr int LAG = kFp8Lag, TILES = NT * MT;
+        f32x4 p[LAG + 1];
         float sc[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) b[m] = operand(A, 16 * (wm * MT + m));
-        w[0] = operand(W, 16 * (wn * NT));
-        w[1] = operand(W, 16 * (wn * NT + 1));
-        const float sw = *(const float *)(S + BM * 4 + 4 * (wn * NT * 16 / kBlk));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) sc[m] = *(const float *)(S + 4 * (16 * (wm * MT + m) + j)) * sw;
-        constexpr int LAG = 2, TILES = NT * MT;
-        f32x4 p[4];
+        for (int m = 0; m < MT; ++m) sc[m] = sa[m] * sw;
         static_for<TILES + LAG>([&](auto c) {
             constexpr int s = decltype(c)::value;
             if constexpr (s < TILES) {
-                constexpr int i = s / MT, m = s % MT;
-                if constexpr (m == 0 && i + 2 < NT) w[(i + 2) % 3] = operand(W, 16 * (wn * NT + i + 2));
-                p[s & 3] = mfma_fp8(w[i % 3], b[m], (f32x4){0.f, 0.f, 0.f, 0.f});
+                constexpr int m = s / NT, i = s % NT;
+                if constexpr (m == MT - 1 && i == 0) {
+                    // every operand of this stage is in registers and the next one's data have landed
+                    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+                    asm volatile("s_barrier" ::: "memory");
+                    copy_scales(st + 2);
+                }
+                if constexpr (i == 0) {
+                    if constexpr (m + 1 < MT) b[(m + 1) & 1] = operand(slot, W_BYTES, wm * MT + m + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                p[s % (LAG + 1)] = mfma_fp8(w[i], b[m & 1], (f32x4){0.f, 0.f, 0.f, 0.f});
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (m == MT - 1) {
+                    w[i] = operand(slot ^ 1, 0, wn * NT + i);
+                    if constexpr (i == 0) {
+                        b[0] = operand(slot ^ 1, W_BYTES, wm * MT);
+                    }
+                    if constexpr (i < MT) sa[i] = row_scale(st + 1, i);
+                    if constexpr (i == MT) sw = col_scale(st + 1);
+                    if constexpr (i < COPIES) copy1(st + 2, left, std::integral_constant<int, i>{});
+                }
             }
             if constexpr (s >= LAG) {
-                constexpr int i = (s - LAG) / MT, m = (s - LAG) % MT;
+                constexpr int m = (s - LAG) / NT, i = (s - LAG) % NT;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][m][r] = __builtin_fmaf(p[(s - LAG) & 3][r], sc[m], acc[i][m][r]);
+                for (int r = 0; r < 4; ++r) acc[i][m][r] = __builtin_fmaf(p[(s - LAG) % (LAG + 1)][r], sc[m], acc[i][m][r]);
+                asm volatile("" : "+v"(acc[i][m]));
             }
             __builtin_amdgcn_sched_barrier(0);
         });
-        wait_vm_all();
-        asm volatile("s_barrier" ::: "memory");
-    };
-    static_assert((NT * 16) % kBlk == 0 || kBlk % (NT * 16) == 0, "a wave's columns lie in one block");
-    copy(0, 0);
+    }
     wait_vm_all();
-    __syncthreads();
-    for (int st = 0; st < blocks; ++st) stage(st, st & 1);
-
-    // lane: outputs n + r of token 16 m + j
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int row = 16 * (wm * MT + m) + j;
@@ -164,19 +181,25 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     }
 }
 
-template <int BM, int BN, int WM, int RING>
+template <int MT>
 static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles_n * p.tiles_m));
+    static_assert(kFp8TileCols == 16 * 8 * 2, "8 tiles of 16 columns, two waves along them");
     if (g.dtype == DT_BF16)
-        hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, BM, BN, WM, RING>), grid, dim3(512), 0, st, g);
+        hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, 8, MT, 2>), grid, dim3(512), 0, st, g);
     else
-        hipLaunchKernelGGL((fp8_block_gemm<DT_F16, BM, BN, WM, RING>), grid, dim3(512), 0, st, g);
+        hipLaunchKernelGGL((fp8_block_gemm<DT_F16, 8, MT, 2>), grid, dim3(512), 0, st, g);
     return hipGetLastError();
 }
 
+// p.mt: tiles of 16 rows a wave, four waves along them (4: 256 rows, 2: 128)
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
     if (p.splits != 1) return hipErrorInvalidValue;
-    return launch_t<256, 256, 4, 2>(g, p, st);
+    switch (p.mt) {
+        case 2: return launch_t<2>(g, p, st);
+        case 4: return launch_t<4>(g, p, st);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace awq4

@@ -224,7 +224,7 @@ struct Fp8BlockArgs {
 };
 struct Fp8BlockPlan {
     int kind;     // 0 streaming kernel, 1 LDS-pipelined
-    int mt;       // streaming: 16-row tiles (1, 2, 4)
+    int mt;       // 16-row tiles: streaming (1, 2, 4); LDS-pipelined, of a wave (2: 128 rows, 4: 256)
     int tiles_n;  // column tiles
     int tiles_m;  // row tiles (grouped: at most)
     int splits;   // workgroups along K
@@ -233,9 +233,7 @@ struct Fp8BlockPlan {
 };
 hipError_t launch_fp8_block_stream(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
-// rows and columns of the LDS-pipelined kernel's tile
-constexpr int kFp8TileRows = 256, kFp8TileCols = 256;
-constexpr int kFp8StreamCols = 64;  // and columns of the streaming kernel's
+constexpr int kFp8TileCols = 256, kFp8StreamCols = 64;  // columns of the two kernels' tiles
 
 // Rotary positions and the 4-bit paged cache (kv4.hpp has its layout).
 struct Kv4AppendArgs {
