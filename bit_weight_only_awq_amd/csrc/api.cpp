@@ -701,7 +701,7 @@ static int check_moe_w4a16_shape(int64_t R, int64_t E, int64_t N, int64_t K, int
 static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
     W4A16Plan p{};
     const double live = live_experts(R, E), avg = (double)R / live;
-    if (avg > 48 && K % 64 == 0 && N % 32 == 0 && K * (N / 2) < (int64_t(1) << 31)) {
+    if (avg > 64 && K % 64 == 0 && N % 32 == 0) {
         p.kind = 3;
         p.mt = avg > 128 ? 16 : 8;
         p.wn = avg > 128 ? 8 : 4;
@@ -712,24 +712,13 @@ static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int 
         return p;
     }
     p.kind = 5;
-    p.blk = 1;
-    p.cs = G >= 64 ? 2 : 1;
-    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-    p.waves = kStreamWaves(p.mt);
-    p.tiles_n = (int)cdiv(N, 128);
+    p.mt = avg <= 12 ? 1 : 2;
+    p.cs = std::min(G / 32, 2);
+    p.tiles_n = (int)cdiv(N, kGroupedCols);
     p.tiles_m = (int)group_tiles(R, E, 16 * p.mt);
-    // K splits as for a dense layer of as many tiles
-    const double rows = 16.0 * p.mt;
-    const int64_t tiles = std::max<int64_t>(1, (int64_t)(p.tiles_n * live * std::ceil(avg / rows)));
+    const double tiles = std::max(1.0, p.tiles_n * live * std::ceil(avg / (16.0 * p.mt)));
     const int64_t chunks = K / (32 * p.cs);
-    const int64_t smax = std::max<int64_t>(1, std::min<int64_t>(d.cus / tiles, chunks / p.waves));
-    const double stream_bytes = (double)K * (64 + 2 * rows), tail_bytes = rows * 128 * 4;
-    p.splits = 1;
-    double best = 0;
-    for (int64_t c = 1; c <= smax; ++c) {
-        const double t = stream_bytes / c / 25.0 + c * tail_bytes / 40.0;
-        if (c == 1 || t < best) best = t, p.splits = (int)c;
-    }
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)(2 * d.cus / tiles), chunks / (2 * kGroupedWaves)));
     if (p.splits > 1)
         p.workspace_bytes = (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, R, N);
     return p;
@@ -1227,6 +1216,7 @@ int awq_moe_gemm_w4a16(const void *x, const int32_t *qweight, const void *scales
         if (!aligned16(q)) return AWQ_EALIGN;
     // (gathered rows are addressed by 32-bit offsets)
     if (rows && x_rows * K * 2 >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;
+    if (K * (N / 2) >= (int64_t(1) << 31)) return AWQ_EUNSUPPORTED;
     W4A16Plan p = plan_moe_w4a16(R, E, N, K, group_size, stream_props(stream));
     if (!grid_fits((int64_t)p.tiles_n * p.tiles_m)) return AWQ_EUNSUPPORTED;
     rc = check_workspace(workspace, workspace_bytes, p.workspace_bytes);
@@ -1235,7 +1225,7 @@ int awq_moe_gemm_w4a16(const void *x, const int32_t *qweight, const void *scales
     const W4A16Args a{x, qweight, scales, qzeros, y, R, N, K, group_size, dtype};
     const Groups g{offsets, rows, (int)E, (int)R, (int)top_k, (int)x_rows, p.tiles_m};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return hip_status(p.kind == 3 ? launch_w4a16_gemm_grouped(a, p, g, st) : launch_w4a16_stream_grouped(a, p, g, st));
+    return hip_status(p.kind == 3 ? launch_w4a16_gemm_grouped(a, p, g, st) : launch_w4a16_grouped(a, p, g, st));
 }
 
 int awq_fp8_block_quant_act(const void *x, uint8_t *a, float *s, int64_t M, int64_t K, int dtype, void *stream) {
@@ -1257,7 +1247,8 @@ int awq_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, cons
     const int rc = check_fp8_block_shape(M, 0, N, K);
     if (rc != AWQ_OK) return rc;
     if (M == 0) return AWQ_OK;
-    return run_fp8_block(a, w, sa, sw, y, M, 0, N, K, dtype, Groups{}, workspace, workspace_bytes, stream);
+    return run_fp8_block(a, w, sa, sw, y, M, 0, N, K, dtype, Groups{nullptr, nullptr, 1, (int)M, 1, (int)M, 0}, workspace,
+                         workspace_bytes, stream);
 }
 
 int awq_moe_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw,

@@ -32,44 +32,23 @@ __device__ __forceinline__ i32x8 operand32(u32x4 lo, u32x4 hi) {
                    (int32_t)hi[0], (int32_t)hi[1], (int32_t)hi[2], (int32_t)hi[3]};
 }
 
-// One tile of a product, dense or grouped by expert: its rows and the matrices it reads.
+// One tile: its rows and the matrices it reads.
 struct Fp8Tile {
     const uint8_t *a, *w;    // a: row row0, or row 0 where rows are gathered
     const float *sa, *sw;
     int tile_n, row0, rows;  // rows: those of the tile that exist
     int a_rows;              // rows that `a` may be read for
-    int index;
-    bool live, gather;
+    bool gather;
 };
-__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8BlockArgs &g, int BM, int BN, int i) {
+__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8BlockArgs &g, const GroupTile &q, int BM) {
     Fp8Tile t;
-    const int tiles_n = (g.N + BN - 1) / BN, blocks = (g.K + kBlk - 1) / kBlk;
-    t.gather = false;
-    size_t e = 0;
-    int end;
-    if (g.groups.offsets) {
-        const GroupTile q = group_tile(g.groups.offsets, g.groups.E, g.groups.R, BM, tiles_n, g.groups.max_tiles, i);
-        t.live = q.live;
-        if (!q.live) return t;
-        t.tile_n = q.tile_n;
-        t.row0 = q.row0;
-        t.index = q.index;
-        t.gather = g.groups.rows != nullptr;
-        end = q.row_end;
-        e = q.expert;
-    } else {
-        // dense: the row tiles of a column tile side by side, as for an expert's
-        const int tiles_m = (g.M + BM - 1) / BM;
-        t.live = true;
-        const int id = tile_of_xcd_order(i, tiles_m * tiles_n);
-        t.tile_n = id / tiles_m;
-        t.row0 = (id - t.tile_n * tiles_m) * BM;
-        t.index = id;
-        end = g.M;
-    }
-    t.rows = min(end - t.row0, BM);
+    const int blocks = (g.K + kBlk - 1) / kBlk;
+    t.gather = g.groups.rows != nullptr;
+    t.tile_n = q.tile_n;
+    t.row0 = q.row0;
+    t.rows = min(q.row_end - q.row0, BM);
     t.a_rows = t.gather ? g.groups.x_rows : t.rows;
-    const size_t first = t.gather ? 0 : (size_t)t.row0;
+    const size_t first = t.gather ? 0 : (size_t)t.row0, e = q.expert;
     t.a = g.a + first * g.K;
     t.sa = g.sa + first * blocks;
     t.w = g.w + e * (size_t)g.N * g.K;

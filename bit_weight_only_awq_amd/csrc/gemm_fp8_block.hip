@@ -46,8 +46,9 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    const Fp8Tile t = fp8_tile(g, BM, BN, blockIdx.x);
-    if (!t.live) return;
+    const GroupMap map(g.groups, BM, (g.N + BN - 1) / BN);
+    if ((int)blockIdx.x >= map.tiles()) return;
+    const Fp8Tile t = fp8_tile(g, map.at(tile_of_xcd_order(blockIdx.x, map.tiles())), BM);
     const int K = g.K, N = g.N, blocks = (K + kBlk - 1) / kBlk;
     const int n0 = t.tile_n * BN;
     const __amdgpu_buffer_rsrc_t wr = buf_rsrc(t.w + (size_t)n0 * K, (int64_t)min(BN, N - n0) * K);

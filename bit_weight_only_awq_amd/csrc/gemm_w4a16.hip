@@ -111,9 +111,9 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
     int tn, tm = 0, m0;
     const int split = blockIdx.z, lg = __builtin_ctz(G);  // G is 32, 64 or 128
     if constexpr (GROUPED) {
-        const GroupTile t = group_tile(groups.offsets, groups.E, groups.R, GB_M, (N + GB_N - 1) / GB_N,
-                                       groups.max_tiles, blockIdx.x);
-        if (!t.live) return;
+        const GroupMap map(groups, GB_M, (N + GB_N - 1) / GB_N);
+        if ((int)blockIdx.x >= map.tiles()) return;
+        const GroupTile t = map.at(tile_of_xcd_order(blockIdx.x, map.tiles()));
         tn = t.tile_n;
         m0 = t.row0;
         M = t.row_end;

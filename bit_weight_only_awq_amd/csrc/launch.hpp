@@ -80,7 +80,7 @@ struct W4A8Plan {
 
 // Products grouped by expert (moe.hpp): rows offsets[e] .. offsets[e + 1] - 1 are expert e's.
 struct Groups {
-    const int32_t *offsets;  // [E + 1]
+    const int32_t *offsets;  // [E + 1]; nullptr (with E = 1): all R rows
     const int32_t *rows;     // [R] slots, row r of the product reads x[rows[r] / top]; nullptr: x[r]
     int E, R, top, x_rows;
     int max_tiles;  // row tiles that any offsets give at most
@@ -125,9 +125,11 @@ hipError_t launch_w4a16_tiled(const W4A16Args &a, const W4A16Plan &p, hipStream_
 // eight waves up to 32 rows, four 512-register waves at 64
 constexpr int kStreamWaves(int mt) { return mt >= 4 ? 4 : 8; }
 hipError_t launch_w4a16_stream(const W4A16Args &a, const W4A16Plan &p, hipStream_t st);
-// the same two kernels over rows grouped by expert (a.M = the rows of all, p.tiles_m = g.max_tiles)
-hipError_t launch_w4a16_stream_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
+// rows grouped by expert (a.M = the rows of all, p.tiles_m = g.max_tiles): the LDS GEMM, and a streaming kernel
+// of their own
 hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
+constexpr int kGroupedWaves = 4, kGroupedCols = 256;  // of a workgroup
+hipError_t launch_w4a16_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
 // K-split reduction of the LDS GEMM and the streaming kernel in a launch of
 // its own (partials after the counters of `tiles` tiles), taken where a
 // tile's partials are large: S splits of `rows`-row tiles, S x rows >= 384.
@@ -220,7 +222,7 @@ struct Fp8BlockArgs {
     const float *sw;   // [ceil(N / 128), ceil(K / 128)], or one such an expert
     void *y;           // [M, N]
     int M, N, K, dtype;
-    Groups groups;     // offsets == nullptr: one matrix for all rows
+    Groups groups;     // dense: offsets == nullptr, E = 1, R = M
 };
 struct Fp8BlockPlan {
     int kind;     // 0 streaming kernel, 1 LDS-pipelined

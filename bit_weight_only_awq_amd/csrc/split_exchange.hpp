@@ -8,6 +8,18 @@
 
 namespace awq4 {
 
+// Position of column c inside a parked row.  Lane j holds columns 8j .. 8j+7
+// of its rows and parks them as two 16-byte halves: half h of every lane sits
+// in the h-th half of the row, at the lane's 16-byte slot (4j floats), so the
+// 16 lanes of a row write 16 consecutive slots -- all of the LDS banks, no
+// two lanes of a write on one bank.  (Columns in plain order put lanes j and
+// j+8 on the same banks and the four row groups of a wave on the same ones
+// again: eight-way conflicts.)
+template <int COLS>
+__device__ __forceinline__ int lds_col(int c) {
+    return (COLS / 2) * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
+}
+
 // The workgroup's M x COLS tile sum -- the SLOTS tiles its waves parked in
 // LDS (ROWS rows of PITCH floats each, column c of a row at slot_of(c)), added
 // in slot order -- goes out: written directly when the K range is not split

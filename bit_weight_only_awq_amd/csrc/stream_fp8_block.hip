@@ -25,8 +25,10 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
     __shared__ __attribute__((aligned(16))) float red[WV * ROWS * PITCH];
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Fp8Tile t = fp8_tile(g, ROWS, COLS, blockIdx.x);
-    if (!t.live) return;
+    const GroupMap map(g.groups, ROWS, (g.N + COLS - 1) / COLS);
+    if ((int)blockIdx.x >= map.tiles()) return;
+    const int index = tile_of_xcd_order(blockIdx.x, map.tiles());
+    const Fp8Tile t = fp8_tile(g, map.at(index), ROWS);
     const int K = g.K, N = g.N, blocks = (K + kBlk - 1) / kBlk;
     const int n0 = t.tile_n * COLS;
     // this workgroup's blocks [lo, hi) and this wave's share of them
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
     __syncthreads();
     const size_t at = (size_t)t.row0 * N;
     tile_store_or_exchange<64 * WV, DT, ROWS, COLS, PITCH, WV>(
-        red, [](int c) { return c; }, (uint16_t *)g.y + at, (uint32_t *)ws + t.index,
+        red, [](int c) { return c; }, (uint16_t *)g.y + at, (uint32_t *)ws + index,
         (char *)ws + split_counters_bytes(gridDim.x) + at * 4, (size_t)g.M * N * 4, t.rows, N, t.tile_n, S, 0);
 }
 

@@ -20,23 +20,10 @@
 // them in split order -- so the result does not depend on timing.
 #include "device.hpp"
 #include "launch.hpp"
-#include "moe.hpp"
 #include "split_exchange.hpp"
 #include "w4a16_ops.hpp"
 
 namespace awq4 {
-
-// Position of column c inside a parked row.  Lane j holds columns 8j .. 8j+7
-// of its rows and parks them as two 16-byte halves: half h of every lane sits
-// in the h-th half of the row, at the lane's 16-byte slot (4j floats), so the
-// 16 lanes of a row write 16 consecutive slots -- all of the LDS banks, no
-// two lanes of a write on one bank.  (Columns in plain order put lanes j and
-// j+8 on the same banks and the four row groups of a wave on the same ones
-// again: eight-way conflicts.)
-template <int COLS>
-__device__ __forceinline__ int lds_col(int c) {
-    return (COLS / 2) * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
-}
 
 // One chunk's loads: scales and zero points of its group, MT row tiles of X
 // (from L2: every column tile reads the same rows), the packed words.
@@ -154,16 +141,13 @@ __device__ __forceinline__ void prefetch_fence() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Grp: Groups, for rows grouped by expert (grid x: the column tiles of every
-// row tile that there may be; M: the rows of all experts), or NoGroups.
-template <int MT, int CS, int WV, int DT, bool SYM, class Grp>
+template <int MT, int CS, int WV, int DT, bool SYM>
 __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__restrict__ x,
                                                           const uint32_t *__restrict__ qw,
                                                           const uint16_t *__restrict__ sc,
                                                           const uint32_t *__restrict__ qz, uint16_t *__restrict__ y,
                                                           uint64_t *__restrict__ ws, int M, int N, int K, int lgG,
-                                                          int sep, Grp grp) {
-    constexpr bool GROUPED = !std::is_same_v<Grp, NoGroups>;
+                                                          int sep) {
     constexpr int ROWS = 16 * MT, COLS = 128;
     // one parked ROWS x COLS tile per wave (128 KB at 4 row tiles)
     __shared__ __attribute__((aligned(16))) float red[WV * ROWS * COLS];
@@ -177,23 +161,7 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
     // to one XCD, so that the line is fetched into one L2 instead of two.
     // (Two word-columns per lane, whole lines per wave, measured slower: the
     // doubled accumulators cost half the waves per CU.)
-    int tile, row0 = 0, rows = M, cnt_at;
-    if constexpr (GROUPED) {
-        const GroupTile t = group_tile(grp.offsets, grp.E, grp.R, ROWS, (N + COLS - 1) / COLS, grp.max_tiles, blockIdx.x);
-        if (!t.live) return;
-        tile = t.tile_n;
-        row0 = t.row0;
-        rows = min(t.row_end - t.row0, ROWS);
-        cnt_at = t.index;
-        const size_t e = t.expert;
-        qw += e * K * nw;
-        sc += e * (size_t)(K >> lgG) * N;
-        if (!SYM) qz += e * (size_t)(K >> lgG) * nw;
-        if (!grp.rows) x += (size_t)row0 * K;
-    } else {
-        tile = tile_of_xcd_order(blockIdx.x, gridDim.x);
-        cnt_at = tile;
-    }
+    const int tile = tile_of_xcd_order(blockIdx.x, gridDim.x);
     const int wcol = tile * 16 + j;
     const int wld = wcol < nw ? wcol : nw - 1;  // past the last word-column: in-bounds words, sums never stored
     // this workgroup's chunks [c_lo, c_hi) and this wave's share of them
@@ -212,10 +180,7 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int row = 16 * mt + j;
-        int src = row < rows ? row : 0;
-        if constexpr (GROUPED)
-            if (grp.rows) src = group_source(grp.rows, row0 + src, grp.top, grp.x_rows);
-        off.x[mt] = (uint32_t)(src * K + 8 * gq) * 2u;
+        off.x[mt] = (uint32_t)((row < M ? row : 0) * K + 8 * gq) * 2u;
     }
 
     f32x4 acc[MT][8];
@@ -280,10 +245,9 @@ __global__ __launch_bounds__(64 * WV, 1) void w4a16_stream(const uint16_t *__res
     // passes with one or two waves at work in each.)
     park(wave);
     __syncthreads();
-    const size_t at = (size_t)row0 * N;  // (0 where rows are not grouped)
     tile_store_or_exchange<64 * WV, DT, ROWS, COLS, COLS, WV>(
-        red, lds_col<COLS>, y + at, (uint32_t *)ws + cnt_at, (char *)ws + split_counters_bytes(gridDim.x) + at * 4, (size_t)M * N * 4,
-        rows, N, tile, S, sep);
+        red, lds_col<COLS>, y, (uint32_t *)ws + tile, (char *)ws + split_counters_bytes(gridDim.x), (size_t)M * N * 4, M,
+        N, tile, S, sep);
 }
 
 template <int MT, int CS, int DT, bool SYM>
@@ -291,10 +255,10 @@ static hipError_t launch_stream_t(const W4A16Args &a, const W4A16Plan &p, hipStr
     constexpr int WV = kStreamWaves(MT);
     if (p.waves != WV || (p.splits > 1 && p.acc == nullptr)) return hipErrorInvalidValue;
     const int sep = split_reduce_apart(p.splits, 16 * MT);
-    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM, NoGroups>), dim3(p.tiles_n, p.splits), dim3(64 * WV), 0, st,
+    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM>), dim3(p.tiles_n, p.splits), dim3(64 * WV), 0, st,
                        (const uint16_t *)a.x, (const uint32_t *)a.qweight, (const uint16_t *)a.scales,
                        (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc, (int)a.M, (int)a.N, (int)a.K,
-                       __builtin_ctz((unsigned)a.G), sep, NoGroups{});
+                       __builtin_ctz((unsigned)a.G), sep);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !sep) return e;
     return launch_w4a16_split_reduce(a, p, p.tiles_n, st);
@@ -317,41 +281,6 @@ hipError_t launch_w4a16_stream(const W4A16Args &a, const W4A16Plan &p, hipStream
         case 22: return launch_stream_dt<2, 2>(a, p, st);
         case 41: return launch_stream_dt<4, 1>(a, p, st);
         case 42: return launch_stream_dt<4, 2>(a, p, st);
-        default: return hipErrorInvalidValue;
-    }
-}
-
-// Rows grouped by expert.  (The splits are always added by the last workgroup of a tile: a
-// reduction launch would have to pass over every row that an expert might have had.)
-template <int MT, int CS, int DT, bool SYM>
-static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    constexpr int WV = kStreamWaves(MT);
-    if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((w4a16_stream<MT, CS, WV, DT, SYM, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), p.splits),
-                       dim3(64 * WV), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
-                       (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc, (int)a.M,
-                       (int)a.N, (int)a.K, __builtin_ctz((unsigned)a.G), 0, g);
-    return hipGetLastError();
-}
-
-template <int MT, int CS>
-static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    const bool sym = a.qzeros == nullptr;
-    if (a.dtype == DT_F16)
-        return sym ? launch_grouped_t<MT, CS, DT_F16, true>(a, p, g, st)
-                   : launch_grouped_t<MT, CS, DT_F16, false>(a, p, g, st);
-    return sym ? launch_grouped_t<MT, CS, DT_BF16, true>(a, p, g, st)
-               : launch_grouped_t<MT, CS, DT_BF16, false>(a, p, g, st);
-}
-
-hipError_t launch_w4a16_stream_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    switch (p.mt * 10 + p.cs) {
-        case 11: return launch_grouped_dt<1, 1>(a, p, g, st);
-        case 12: return launch_grouped_dt<1, 2>(a, p, g, st);
-        case 21: return launch_grouped_dt<2, 1>(a, p, g, st);
-        case 22: return launch_grouped_dt<2, 2>(a, p, g, st);
-        case 41: return launch_grouped_dt<4, 1>(a, p, g, st);
-        case 42: return launch_grouped_dt<4, 2>(a, p, g, st);
         default: return hipErrorInvalidValue;
     }
 }
