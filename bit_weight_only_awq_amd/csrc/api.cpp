@@ -735,22 +735,20 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     Fp8BlockPlan p{};
     const double live = E ? live_experts(M, E) : 1.0, avg = (double)M / live;
     auto row_tiles = [&](int64_t rows) { return E ? group_tiles(M, E, rows) : cdiv(M, rows); };
-    if (avg > 64) {
-        p.kind = 1;
-        p.splits = 1;
-        p.tiles_n = (int)cdiv(N, kFp8TileCols);
-        p.mt = avg <= 192 ? 2 : 4;
-        p.tiles_m = (int)row_tiles(64 * p.mt);
-        return p;
-    }
-    p.mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-    p.tiles_n = (int)cdiv(N, kFp8StreamCols);
-    p.tiles_m = (int)row_tiles(16 * p.mt);
     const int64_t blocks = cdiv(K, 128);
-    const int64_t tiles = std::max<int64_t>(1, (int64_t)(p.tiles_n * live * std::ceil(avg / (16.0 * p.mt))));
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * d.cus / tiles, blocks / 16, 8}));
+    // workgroups to be expected with tiles of so many rows and columns
+    auto workgroups = [&](int64_t rows, int64_t cols) { return cdiv(N, cols) * live * std::ceil(avg / (double)rows); };
+    // Up to 16 rows (of an expert: 4, whose tiles are many without a K split), the
+    // streaming kernel.
+    p.tile = avg <= (E ? 4 : 16) ? 0 : avg > 192 && workgroups(256, 256) >= 0.6 * d.cus ? 256 : 128;
+    const int64_t rows = p.tile ? p.tile : kFp8StreamRows, cols = p.tile ? p.tile : kFp8StreamCols;
+    p.tiles_n = (int)cdiv(N, cols);
+    p.tiles_m = (int)row_tiles(rows);
+    const double fill = p.tile == 256 ? 0 : p.tile ? 1.5 : 2;
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(fill * d.cus / workgroups(rows, cols)), blocks / 8, 8}));
     if (p.splits > 1)
-        p.workspace_bytes = (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);
+        p.workspace_bytes = p.tile ? (size_t)p.splits * M * N * 4
+                                   : (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);
     return p;
 }
 static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
@@ -767,7 +765,7 @@ static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, co
     groups.max_tiles = p.tiles_m;
     const Fp8BlockArgs g{a, w, sa, sw, y, (int)M, (int)N, (int)K, dtype, groups};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return hip_status(p.kind == 1 ? launch_fp8_block_gemm(g, p, st) : launch_fp8_block_stream(g, p, st));
+    return hip_status(p.tile ? launch_fp8_block_gemm(g, p, st) : launch_fp8_block_stream(g, p, st));
 }
 
 }  // namespace awq4

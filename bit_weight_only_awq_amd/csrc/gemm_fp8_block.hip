@@ -34,14 +34,14 @@ __device__ __forceinline__ int blk_swz(int j) { return (j ^ (j >> 3)) & 7; }  //
 
 constexpr int kFp8Lag = 3;
 
-template <int DT, int NT, int MT, int WN>
-__global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
-    constexpr int WM = 8 / WN, BN = 16 * NT * WN, BM = 16 * MT * WM;
+template <int DT, int NT, int MT, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g, f32x4 *__restrict__ part) {
+    constexpr int WAVES = WN * WM, BN = 16 * NT * WN, BM = 16 * MT * WM;
     constexpr int W_BYTES = BN * kBlk, A_BYTES = BM * kBlk, STAGE = W_BYTES + A_BYTES;
     constexpr int S_BYTES = BM * 16 + 64, LDS = 2 * (STAGE + S_BYTES);
-    constexpr int W_COPIES = BN / 64, A_COPIES = BM / 64, COPIES = W_COPIES + A_COPIES;
-    static_assert(MT % 2 == 0 && kBlk % (16 * NT) == 0 && BM / 64 <= 4 && BN / kBlk <= 4 && LDS <= 163840, "fits");
-    static_assert(COPIES <= NT && COPIES < 16, "a copy beside each weight operand; the wait's field");
+    constexpr int W_COPIES = BN / 8 / WAVES, A_COPIES = BM / 8 / WAVES, COPIES = W_COPIES + A_COPIES;
+    static_assert(MT % 2 == 0 && kBlk % (16 * NT) == 0 && BM / 64 < WAVES && BN / kBlk <= 4 && LDS <= 163840, "fits");
+    static_assert(COPIES <= 2 * NT && COPIES < 16, "two copies beside each weight operand at most; the wait's field");
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS];
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -51,10 +51,13 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     const Fp8Tile t = fp8_tile(g, map.at(tile_of_xcd_order(blockIdx.x, map.tiles())), BM);
     const int K = g.K, N = g.N, blocks = (K + kBlk - 1) / kBlk;
     const int n0 = t.tile_n * BN;
+    // this workgroup's stages; a K split begins at a multiple of four, where scales are copied
+    const int S = gridDim.y, quarters = (blocks + 3) / 4;
+    const int s_lo = 4 * (quarters * (int)blockIdx.y / S), s_hi = min(blocks, 4 * (quarters * ((int)blockIdx.y + 1) / S));
     const __amdgpu_buffer_rsrc_t wr = buf_rsrc(t.w + (size_t)n0 * K, (int64_t)min(BN, N - n0) * K);
     const __amdgpu_buffer_rsrc_t ar = buf_rsrc(t.a, (int64_t)t.a_rows * K);
-    // waves 0 .. BM / 64 - 1 copy the tokens' scales, wave 4 the weights'
-    const bool row_scales = wave < BM / 64, scales = row_scales || wave == 4;
+    // waves 0 .. BM / 64 - 1 copy the tokens' scales, the next one the weights'
+    const bool row_scales = wave < BM / 64, scales = wave <= BM / 64;
     const __amdgpu_buffer_rsrc_t sr = row_scales
         ? buf_rsrc(t.sa, (int64_t)t.a_rows * blocks * 4)
         : buf_rsrc(t.sw, (int64_t)((N + kBlk - 1) / kBlk) * blocks * 4);
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     if (row_scales) {
         const int src = fp8_source(g, t, 64 * wave + lane);
         if (src >= 0) so = (uint32_t)src * (uint32_t)blocks * 4u;
-    } else if (wave == 4 && lane < BN / kBlk) {
+    } else if (wave == BM / 64 && lane < BN / kBlk) {
         so = (uint32_t)((n0 / kBlk + lane) * blocks) * 4u;
     }
     // copy i of stage st, whose rows have `left` 16-byte segments
@@ -89,10 +92,10 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
         dma16_buf(isw ? wr : ar, (seg0 ^ (c & 1)) < left ? off[i] : kOut, (uint32_t)st * kBlk, dst);
     };
     auto copy_scales = [&](int st) {
-        if (scales && (st & 3) == 0 && st < blocks && (row_scales || lane < BN / kBlk))
+        if (scales && (st & 3) == 0 && st < s_hi && (row_scales || lane < BN / kBlk))
             dma16_buf(sr, so, (uint32_t)st * 4u, lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
     };
-    auto left_of = [&](int st) { return st < blocks ? min((K - st * kBlk) / 16, 8) : 0; };
+    auto left_of = [&](int st) { return st < s_hi ? min((K - st * kBlk) / 16, 8) : 0; };
 
     f32x4 acc[NT][MT];
 #pragma unroll
@@ -111,10 +114,10 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
         return *(const float *)(lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + BM * 16 + 16 * (wn * NT * 16 / kBlk) + 4 * (st & 3));
     };
     {
-        const int l0 = left_of(0), l1 = left_of(1);
-        copy_scales(0);
-        static_for<COPIES>([&](auto ic) { copy1(0, l0, ic); });
-        static_for<COPIES>([&](auto ic) { copy1(1, l1, ic); });
+        const int l0 = left_of(s_lo), l1 = left_of(s_lo + 1);
+        copy_scales(s_lo);
+        static_for<COPIES>([&](auto ic) { copy1(s_lo, l0, ic); });
+        static_for<COPIES>([&](auto ic) { copy1(s_lo + 1, l1, ic); });
         __builtin_amdgcn_s_waitcnt(0x0F70 | COPIES);  // stage 0's have landed
         asm volatile("s_barrier" ::: "memory");
     }
@@ -124,9 +127,9 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     for (int i = 0; i < NT; ++i) w[i] = operand(0, 0, wn * NT + i);
     b[0] = operand(0, W_BYTES, wm * MT);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sa[m] = row_scale(0, m);
-    sw = col_scale(0);
-    for (int st = 0; st < blocks; ++st) {
+    for (int m = 0; m < MT; ++m) sa[m] = row_scale(s_lo, m);
+    sw = col_scale(s_lo);
+    for (int st = s_lo; st < s_hi; ++st) {
         const int slot = st & 1, left = left_of(st + 2);
         constexpr int LAG = kFp8Lag, TILES = NT * MT;
         f32x4 p[LAG + 1];
@@ -154,9 +157,11 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
                     if constexpr (i == 0) {
                         b[0] = operand(slot ^ 1, W_BYTES, wm * MT);
                     }
+                    static_assert(MT <= NT, "a token scale beside each");
                     if constexpr (i < MT) sa[i] = row_scale(st + 1, i);
-                    if constexpr (i == MT) sw = col_scale(st + 1);
+                    if constexpr (i == NT - 1) sw = col_scale(st + 1);
                     if constexpr (i < COPIES) copy1(st + 2, left, std::integral_constant<int, i>{});
+                    if constexpr (i + NT < COPIES) copy1(st + 2, left, std::integral_constant<int, i + NT>{});
                 }
             }
             if constexpr (s >= LAG) {
@@ -173,32 +178,64 @@ __global__ __launch_bounds__(512, 2) void fp8_block_gemm(Fp8BlockArgs g) {
     for (int m = 0; m < MT; ++m) {
         const int row = 16 * (wm * MT + m) + j;
         if (row >= t.rows) continue;
-        uint16_t *const y = (uint16_t *)g.y + (size_t)(t.row0 + row) * N;
+        const size_t at = (size_t)(t.row0 + row) * N;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int n = n0 + 16 * (wn * NT + i) + 4 * gq;
-            if (n < N) *(uint2 *)(y + n) = quad_out_bits<DT>(acc[i][m]);
+            if (n >= N) continue;
+            if (S == 1) *(uint2 *)((uint16_t *)g.y + at + n) = quad_out_bits<DT>(acc[i][m]);
+            else part[((size_t)blockIdx.y * g.M * N + at + n) / 4] = acc[i][m];
         }
     }
 }
 
-template <int MT>
+// The K splits' sums [S][M][N], added in split order, written and cleared; one thread a quad of outputs.  Rows behind
+// the last expert's have none.
+template <int DT>
+__global__ __launch_bounds__(256) void fp8_block_split_sum(f32x4 *__restrict__ part, uint16_t *__restrict__ y,
+                                                           const int32_t *__restrict__ rows, int64_t quads, int N, int S) {
+    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (q >= (rows ? min(quads, (int64_t)max(*rows, 0) * (N / 4)) : quads)) return;
+    f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
+    constexpr int kB = 4;
+    for (int s0 = 0; s0 < S; s0 += kB) {
+        f32x4 b[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) b[i] = s0 + i < S ? part[q + (s0 + i) * quads] : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+            if (s0 + i < S) v += b[i];
+    }
+    *(uint2 *)(y + 4 * q) = quad_out_bits<DT>(v);
+    for (int s = 0; s < S; ++s) part[q + s * quads] = (f32x4){0.f, 0.f, 0.f, 0.f};
+}
+
+template <int NT, int MT, int WN, int WM>
 static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
-    const dim3 grid((unsigned)(p.tiles_n * p.tiles_m));
-    static_assert(kFp8TileCols == 16 * 8 * 2, "8 tiles of 16 columns, two waves along them");
+    const dim3 grid((unsigned)(p.tiles_n * p.tiles_m), (unsigned)p.splits), block(64 * WN * WM);
+    f32x4 *const part = (f32x4 *)p.acc;
+    if (g.dtype == DT_BF16) hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, NT, MT, WN, WM>), grid, block, 0, st, g, part);
+    else hipLaunchKernelGGL((fp8_block_gemm<DT_F16, NT, MT, WN, WM>), grid, block, 0, st, g, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t quads = (int64_t)g.M * g.N / 4;
+    const dim3 sums((unsigned)((quads + 255) / 256));
+    const int32_t *const rows = g.groups.offsets ? g.groups.offsets + g.groups.E : nullptr;
     if (g.dtype == DT_BF16)
-        hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, 8, MT, 2>), grid, dim3(512), 0, st, g);
+        hipLaunchKernelGGL(fp8_block_split_sum<DT_BF16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, rows, quads, g.N,
+                           p.splits);
     else
-        hipLaunchKernelGGL((fp8_block_gemm<DT_F16, 8, MT, 2>), grid, dim3(512), 0, st, g);
+        hipLaunchKernelGGL(fp8_block_split_sum<DT_F16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, rows, quads, g.N,
+                           p.splits);
     return hipGetLastError();
 }
 
-// p.mt: tiles of 16 rows a wave, four waves along them (4: 256 rows, 2: 128)
+// Tiles of 128 x 128: 4 waves, two workgroups a CU; of 256 x 256: 8 waves, one.
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
-    if (p.splits != 1) return hipErrorInvalidValue;
-    switch (p.mt) {
-        case 2: return launch_t<2>(g, p, st);
-        case 4: return launch_t<4>(g, p, st);
+    if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
+    switch (p.tile) {
+        case 128: return launch_t<4, 4, 2, 2>(g, p, st);
+        case 256: return launch_t<8, 4, 2, 4>(g, p, st);
         default: return hipErrorInvalidValue;
     }
 }

@@ -225,8 +225,7 @@ struct Fp8BlockArgs {
     Groups groups;     // dense: offsets == nullptr, E = 1, R = M
 };
 struct Fp8BlockPlan {
-    int kind;     // 0 streaming kernel, 1 LDS-pipelined
-    int mt;       // 16-row tiles: streaming (1, 2, 4); LDS-pipelined, of a wave (2: 128 rows, 4: 256)
+    int tile;     // rows and columns of the LDS-pipelined kernel's tile (128, 256), or 0: the streaming kernel
     int tiles_n;  // column tiles
     int tiles_m;  // row tiles (grouped: at most)
     int splits;   // workgroups along K
@@ -235,7 +234,7 @@ struct Fp8BlockPlan {
 };
 hipError_t launch_fp8_block_stream(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st);
-constexpr int kFp8TileCols = 256, kFp8StreamCols = 64;  // columns of the two kernels' tiles
+constexpr int kFp8StreamRows = 16, kFp8StreamCols = 32;  // of the streaming kernel's tile
 
 // Rotary positions and the 4-bit paged cache (kv4.hpp has its layout).
 struct Kv4AppendArgs {

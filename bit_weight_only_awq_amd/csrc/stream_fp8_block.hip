@@ -1,27 +1,30 @@
 // stream_fp8_block.hip -- block-scaled E4M3 products of few rows (fp8_block.hpp has
 // the arithmetic): the weights are read once, straight into registers.
 //
-// A workgroup has 64 outputs n and one tile of 16 MT tokens; its 8 waves take
-// the blocks of 128 k in turn (with a K split: of the workgroup's share of
-// them), two blocks' loads in flight, and their sums are added through LDS in wave order at
-// the end, then over the K splits in split order (split_exchange.hpp).
-// Bound by memory: a block is 8 KB of weights a wave, used once.
+// A workgroup has 32 outputs n and one tile of 16 tokens; its 4 waves take the
+// blocks of 128 k in turn (with a K split: of the workgroup's share of them), two
+// blocks' loads in flight, and their sums are added through LDS in wave order at
+// the end, then over the K splits in split order (split_exchange.hpp).  Bound by
+// memory: one token through 4096 x 14336 takes 18 us, of which 13 are what the
+// same loads take alone and 4 what the smallest call does (64 outputs a workgroup
+// 18.7, 16 of them 18.2, 8 waves 18.2).  From 17 tokens on the tiles of 128 through
+// LDS, split along K, take as long or less (17 tokens 18.5, here 22).
 #include "fp8_block.hpp"
 #include "split_exchange.hpp"
 
 namespace awq4 {
 
-constexpr int kStreamNT = kFp8StreamCols / 16;  // 16-column tiles of a wave
+constexpr int kFp8StreamWaves = 4;
 
-template <int MT>
+template <int NT>
 struct Fp8Buf {
-    u32x4 w[kStreamNT][2], a[MT][2];
-    float sa[MT], sw;
+    u32x4 w[NT][2], a[2];
+    float sa, sw;
 };
 
-template <int MT, int DT>
-__global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint64_t *__restrict__ ws) {
-    constexpr int WV = 8, NT = kStreamNT, ROWS = 16 * MT, COLS = kFp8StreamCols, PITCH = COLS + 4;
+template <int DT>
+__global__ __launch_bounds__(64 * kFp8StreamWaves, 2) void fp8_block_stream(Fp8BlockArgs g, uint64_t *__restrict__ ws) {
+    constexpr int WV = kFp8StreamWaves, COLS = kFp8StreamCols, NT = COLS / 16, ROWS = 16, PITCH = COLS + 4;
     __shared__ __attribute__((aligned(16))) float red[WV * ROWS * PITCH];
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -40,16 +43,13 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
     const __amdgpu_buffer_rsrc_t ar = buf_rsrc(t.a, (int64_t)t.a_rows * K);
     const __amdgpu_buffer_rsrc_t sr = buf_rsrc(t.sa, (int64_t)t.a_rows * blocks * 4);
     const float *const sw = t.sw + (size_t)(n0 / kBlk) * blocks;
-    uint32_t wo[NT], ao[MT], so[MT];
+    uint32_t wo[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) wo[i] = (uint32_t)((16 * i + j) * K);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int src = fp8_source(g, t, 16 * i + j);
-        ao[i] = src < 0 ? kOut : (uint32_t)src * (uint32_t)K;
-        so[i] = src < 0 ? kOut : (uint32_t)src * (uint32_t)blocks * 4u;
-    }
-    auto issue = [&](Fp8Buf<MT> &b, int blk) {
+    const int src = fp8_source(g, t, j);
+    const uint32_t ao = src < 0 ? kOut : (uint32_t)src * (uint32_t)K;
+    const uint32_t so = src < 0 ? kOut : (uint32_t)src * (uint32_t)blocks * 4u;
+    auto issue = [&](Fp8Buf<NT> &b, int blk) {
         const int k = blk * kBlk + 16 * gq;
         const uint32_t k0 = k < K ? (uint32_t)k : kOut, k1 = k + 64 < K ? (uint32_t)(k + 64) : kOut;
 #pragma unroll
@@ -57,31 +57,23 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
             b.w[i][0] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i] + k0, 0, 2);
             b.w[i][1] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i] + k1, 0, 2);
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            // (both offsets may be past the buffer: the larger of the two is)
-            b.a[i][0] = __builtin_amdgcn_raw_buffer_load_b128(ar, max(ao[i], k0) == kOut ? kOut : ao[i] + k0, 0, 0);
-            b.a[i][1] = __builtin_amdgcn_raw_buffer_load_b128(ar, max(ao[i], k1) == kOut ? kOut : ao[i] + k1, 0, 0);
-            b.sa[i] = bit_as<float>(__builtin_amdgcn_raw_buffer_load_b32(sr, so[i] + 4u * blk, 0, 0));
-        }
+        // (one of the offsets, or both, may be past the buffer: their bit is set once)
+        b.a[0] = __builtin_amdgcn_raw_buffer_load_b128(ar, (ao | k0) & kOut ? kOut : ao + k0, 0, 0);
+        b.a[1] = __builtin_amdgcn_raw_buffer_load_b128(ar, (ao | k1) & kOut ? kOut : ao + k1, 0, 0);
+        b.sa = bit_as<float>(__builtin_amdgcn_raw_buffer_load_b32(sr, so + 4u * blk, 0, 0));
         b.sw = sw[blk];
     };
-    f32x4 acc[NT][MT];
+    f32x4 acc[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](const Fp8Buf<NT> &b) {
+        const i32x8 a = operand32(b.a[0], b.a[1]);
+        const float sc = b.sa * b.sw;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[i][m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    auto compute = [&](const Fp8Buf<MT> &b) {
+        for (int i = 0; i < NT; ++i) {
+            const f32x4 p = mfma_fp8(operand32(b.w[i][0], b.w[i][1]), a, (f32x4){0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const i32x8 a = operand32(b.a[m][0], b.a[m][1]);
-            const float sc = b.sa[m] * b.sw;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const f32x4 p = mfma_fp8(operand32(b.w[i][0], b.w[i][1]), a, (f32x4){0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][m][r] = __builtin_fmaf(p[r], sc, acc[i][m][r]);
-            }
+            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(p[r], sc, acc[i][r]);
         }
     };
     // keeps a buffer's loads where they are issued, a block ahead of their use
@@ -90,7 +82,7 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
         __builtin_amdgcn_sched_barrier(0);
     };
     auto block_of = [&](int i) { return lo + wave + i * WV; };
-    Fp8Buf<MT> b0, b1;
+    Fp8Buf<NT> b0, b1;
     if (n > 0) issue(b0, block_of(0));
     if (n > 1) issue(b1, block_of(1));
     fence();
@@ -111,12 +103,9 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
     if (i + 1 < n) compute(b1);
     if (i + 2 < n) compute(b0);
 
-    // lane: outputs n0 + 16 i + 4 gq + r of token 16 m + j
+    // lane: outputs n0 + 16 i + 4 gq + r of token j
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-            *(f32x4 *)(red + (wave * ROWS + 16 * m + j) * PITCH + 16 * c + 4 * gq) = acc[c][m];
+    for (int i = 0; i < NT; ++i) *(f32x4 *)(red + (wave * ROWS + j) * PITCH + 16 * i + 4 * gq) = acc[i];
     __syncthreads();
     const size_t at = (size_t)t.row0 * N;
     tile_store_or_exchange<64 * WV, DT, ROWS, COLS, PITCH, WV>(
@@ -124,24 +113,12 @@ __global__ __launch_bounds__(512, 2) void fp8_block_stream(Fp8BlockArgs g, uint6
         (char *)ws + split_counters_bytes(gridDim.x) + at * 4, (size_t)g.M * N * 4, t.rows, N, t.tile_n, S, 0);
 }
 
-template <int MT>
-static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
-    if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(p.tiles_n * p.tiles_m), (unsigned)p.splits);
-    if (g.dtype == DT_BF16)
-        hipLaunchKernelGGL((fp8_block_stream<MT, DT_BF16>), grid, dim3(512), 0, st, g, p.acc);
-    else
-        hipLaunchKernelGGL((fp8_block_stream<MT, DT_F16>), grid, dim3(512), 0, st, g, p.acc);
-    return hipGetLastError();
-}
-
 hipError_t launch_fp8_block_stream(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
-    switch (p.mt) {
-        case 1: return launch_t<1>(g, p, st);
-        case 2: return launch_t<2>(g, p, st);
-        case 4: return launch_t<4>(g, p, st);
-        default: return hipErrorInvalidValue;
-    }
+    if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(p.tiles_n * p.tiles_m), (unsigned)p.splits), block(64 * kFp8StreamWaves);
+    if (g.dtype == DT_BF16) hipLaunchKernelGGL(fp8_block_stream<DT_BF16>, grid, block, 0, st, g, p.acc);
+    else hipLaunchKernelGGL(fp8_block_stream<DT_F16>, grid, block, 0, st, g, p.acc);
+    return hipGetLastError();
 }
 
 }  // namespace awq4

@@ -149,10 +149,17 @@ def test_product(M, N, K):
     run_dense(M, N, K, "bf16" if M % 2 else "f16", seed=M)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 256, 14336), (3, 64, 4112), (40, 200, 8192), (1, 24, 131072)])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 14336), (3, 64, 4112), (40, 200, 8192), (1, 24, 131072), (70, 264, 4112),
+                                   (300, 256, 2064)])
 def test_product_split_k(M, N, K):
     assert awq.lib().awq_fp8_block_gemm_workspace_bytes(M, 0, N, K) > 0
     run_dense(M, N, K, "f16")
+
+
+@pytest.mark.parametrize("M,N,K", [(2600, 4104, 400), (2561, 4096, 128), (3000, 3848, 2064)])
+def test_product_of_large_tiles(M, N, K):
+    """As many tiles of 256 x 256 as take them."""
+    run_dense(M, N, K, "bf16", seed=K)
 
 
 def run_grouped(split, K, N, dtype, gather, top=2, seed=0, spare=0):
@@ -179,6 +186,11 @@ def run_grouped(split, K, N, dtype, gather, top=2, seed=0, spare=0):
 def test_grouped_product(split, dtype, gather, K, N):
     print(split, dtype, K, N, flush=True)
     run_grouped(SPLITS[split], K, N, dtype, gather)
+
+
+def test_grouped_product_of_large_tiles():
+    run_grouped([900, 0, 1100, 769], 272, 4096, "f16", True, seed=5)
+    run_grouped([900, 0, 1100, 769], 272, 4096, "bf16", False, seed=6, spare=3)
 
 
 def test_grouped_product_split_k():
