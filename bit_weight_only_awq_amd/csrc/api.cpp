@@ -670,7 +670,7 @@ static int check_route(int64_t T, int64_t E, int64_t k) {
 static RoutePlan plan_route(int64_t T, int64_t E, int64_t k) {
     RoutePlan p{};
     p.block_tokens = (int)std::min<int64_t>(std::max<int64_t>(16, cdiv(T, 256)), 8192 / k);
-    p.blocks = T <= 16 && E <= 512 ? 1 : (int)cdiv(T, p.block_tokens);
+    p.blocks = T <= 16 && E <= 512 ? 1 : (int)std::max<int64_t>(1, cdiv(T, p.block_tokens));
     if (p.blocks == 1 && E > 512) p.blocks = 2, p.block_tokens = (int)std::max<int64_t>(1, cdiv(T, 2));
     return p;
 }

@@ -34,7 +34,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-enum { DT_F16 = 0, DT_BF16 = 1 };
+enum { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2 };  // DT_F32: the router's logits only
 
 // f(std::integral_constant<int, 0>) ... f(std::integral_constant<int, N - 1>),
 // in order: a loop whose index is a compile-time constant in every body

@@ -191,7 +191,7 @@ hipError_t launch_rmsnorm(const NormArgs &n, hipStream_t st);
 // Mixture-of-experts routing and the weighted sum of the experts' rows (moe_route.hip).
 constexpr int kMoeMaxExperts = 1024, kMoeMaxTop = 32;
 struct RouteArgs {
-    const void *logits;  // [T, E], dtype (DT_F16, DT_BF16 or 2: fp32)
+    const void *logits;  // [T, E], dtype (DT_F32 too)
     float *weights;      // [T, k]
     int32_t *experts, *offsets, *rows, *places;  // [T, k], [E + 1], [T k], [T k]
     int64_t T;

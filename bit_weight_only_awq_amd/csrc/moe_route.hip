@@ -17,8 +17,8 @@
 // from group to group.  No atomics whose order could show: the plan is the
 // same on every run.
 //
-// One workgroup does both for few tokens; otherwise a first launch chooses and
-// counts, and a second places: its workgroups add up the counts of all others
+// One workgroup does both for few tokens; otherwise a first launch chooses, counts
+// and ranks, and a second places: its workgroups add up the counts of all others
 // for themselves, which for up to 256 of them costs less than a launch between.
 #include "device.hpp"
 #include "launch.hpp"
@@ -71,34 +71,61 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return bit_as<float>((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
-// The choice of token t by its group of LPT lanes, E <= LPT * PER experts;
-// lane j < k of the group writes the j-th.  live: false past the last token (every lane
-// takes part in the moves).  ids: LDS, the token's k slots.
+// PER logits from element `at` on as fp32, by one or two wide loads where every row allows it.
+template <int PER>
+__device__ __forceinline__ void load_logits(const RouteArgs &g, size_t at, int have, float (&l)[PER]) {
+    struct __attribute__((aligned(PER * 2 < 16 ? PER * 2 : 16))) Halves {
+        uint16_t v[PER];
+    };
+    struct __attribute__((aligned(PER * 4 < 16 ? PER * 4 : 16))) Singles {
+        float v[PER];
+    };
+    const bool wide = g.E % PER == 0;  // (then `at` is a multiple of PER, and the last lane with experts has PER of them)
+    if (g.dtype == DT_F32) {
+        const float *p = (const float *)g.logits + at;
+        if (wide && have > 0) {
+            const Singles s = *(const Singles *)p;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] = s.v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] = i < have ? p[i] : 0.0f;
+        }
+        return;
+    }
+    const uint16_t *p = (const uint16_t *)g.logits + at;
+    Halves h{};
+    if (wide && have > 0) {
+        h = *(const Halves *)p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) h.v[i] = i < have ? p[i] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = g.dtype == DT_F16 ? f16_bits_to_f32(h.v[i]) : bf16_bits_to_f32(h.v[i]);
+}
+
+// The choice of token t by its group of LPT lanes, E <= LPT * PER experts.  live: false past the last token (every
+// lane takes part in the moves).  ids, keys: LDS, the token's k slots; the lane that owns a choice writes it there, and
+// the lanes of the group then share the slots.
 template <int LPT, int PER>
-__device__ __forceinline__ void choose(const RouteArgs &g, int64_t t, bool live, int16_t *ids) {
+__device__ __forceinline__ void choose(const RouteArgs &g, int64_t t, bool live, int16_t *ids, uint32_t *keys) {
     const int lane = threadIdx.x & (LPT - 1);
     const int shift = (threadIdx.x & 63) & ~(LPT - 1);
-    uint32_t key[PER];
+    const int have = live ? min(max(g.E - lane * PER, 0), PER) : 0;
+    float l[PER];
+    load_logits<PER>(g, (size_t)t * g.E + lane * PER, have, l);
+    uint32_t key[PER], best = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = lane * PER + i;
         key[i] = 0;
-        if (live && e < g.E) {
-            const size_t at = (size_t)t * g.E + e;
-            float l = g.dtype == DT_F16    ? f16_bits_to_f32(((const uint16_t *)g.logits)[at])
-                      : g.dtype == DT_BF16 ? bf16_bits_to_f32(((const uint16_t *)g.logits)[at])
-                                           : ((const float *)g.logits)[at];
-            l += 0.0f;  // -0 and 0 are one logit
-            if (l > -__builtin_inff()) {  // (not for NaN)
-                l = fminf(l, 3.4028234663852886e38f);
-                const uint32_t u = bit_as<uint32_t>(l);
-                key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-            }
+        const float v = l[i] + 0.0f;  // -0 and 0 are one logit
+        if (i < have && v > -__builtin_inff()) {  // (not for NaN)
+            const uint32_t u = bit_as<uint32_t>(fminf(v, 3.4028234663852886e38f));
+            key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;
         }
+        best = max(best, key[i]);
     }
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
     const uint32_t top = group_max<LPT>(best);
     const float m = top ? key_value(top) : 0.0f;  // no expert: no weight
     float sum = 0.0f;
@@ -107,39 +134,40 @@ __device__ __forceinline__ void choose(const RouteArgs &g, int64_t t, bool live,
         for (int i = 0; i < PER; ++i) sum += key[i] ? expf(key_value(key[i]) - m) : 0.0f;
         sum = group_sum<LPT>(sum);
     }
-    int my_id = -1;
-    float my_w = 0.0f;
     for (int j = 0; j < g.k; ++j) {
         const uint32_t w = j == 0 ? top : group_max<LPT>(best);
-        const uint64_t holders = __ballot(best == w) >> shift;
-        const int owner = __builtin_ctzll(holders);
-        int id = -1;
+        const int owner = __builtin_ctzll(__ballot(best == w) >> shift);  // the lowest lane of the group that holds it
         if (lane == owner) {
-            // this lane's first expert with the key leaves, and its next best comes up
-            int at = PER;
+            // its first expert with the key leaves, and its next best comes up
+            int at = 0;
 #pragma unroll
             for (int i = PER - 1; i >= 0; --i) at = key[i] == w ? i : at;
-            id = lane * PER + at;
             best = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                if (i == at) key[i] = 0;
+                key[i] = i == at ? 0u : key[i];
                 best = max(best, key[i]);
             }
-        }
-        id = __shfl(id, shift + owner, 64);
-        const float e = w ? expf(key_value(w) - m) : 0.0f;
-        if (g.renormalize) sum += e;
-        if (lane == j && w) {
-            my_id = id;
-            my_w = e;
+            if (live) {
+                ids[j] = (int16_t)(w ? lane * PER + at : -1);
+                keys[j] = w;
+            }
         }
     }
-    if (live && lane < g.k) {
-        const size_t at = (size_t)t * g.k + lane;
-        g.experts[at] = my_id;
-        g.weights[at] = my_id >= 0 ? my_w / sum : 0.0f;
-        ids[lane] = (int16_t)my_id;
+    __builtin_amdgcn_wave_barrier();  // (LDS accesses of a wave stay in order)
+    if (!live) {
+        if (g.renormalize) (void)group_sum<LPT>(0.0f);
+        return;
+    }
+    auto weight = [&](int j) { return keys[j] ? expf(key_value(keys[j]) - m) : 0.0f; };
+    if (g.renormalize) {
+        for (int j = lane; j < g.k; j += LPT) sum += weight(j);
+        sum = group_sum<LPT>(sum);
+    }
+    for (int j = lane; j < g.k; j += LPT) {
+        const size_t at = (size_t)t * g.k + j;
+        g.experts[at] = ids[j];
+        g.weights[at] = ids[j] >= 0 ? weight(j) / sum : 0.0f;
     }
 }
 
@@ -185,6 +213,12 @@ __device__ __forceinline__ void scan_experts(int *total, int E, int *all) {
     if (lane == 63) *all = end;
 }
 
+// Slots that each wave of a workgroup takes of its n.
+template <int WAVES>
+__device__ __forceinline__ int slots_per_wave(int n) {
+    return ((n + WAVES - 1) / WAVES + 63) & ~63;
+}
+
 // Counts of the workgroup's slots by wave and expert; run[w][e] is left as the number of the
 // expert's slots in waves before w, total[e] as the sum.  id(s): the expert of slot s < n, -1: none.
 template <int WAVES, class Id>
@@ -192,7 +226,7 @@ __device__ __forceinline__ void count_slots(int n, int E, int bits, int *run, in
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i < WAVES * E; i += 64 * WAVES) run[i] = 0;
     __syncthreads();
-    const int per = ((n + WAVES - 1) / WAVES + 63) & ~63;
+    const int per = slots_per_wave<WAVES>(n);
     for (int s0 = wave * per; s0 < min(n, wave * per + per); s0 += 64) {
         const int s = s0 + lane;
         take_places(s < n ? id(s) : -1, bits, run + wave * E);
@@ -211,30 +245,28 @@ __device__ __forceinline__ void count_slots(int n, int E, int bits, int *run, in
     __syncthreads();
 }
 
-// The workgroup's slots to their places: slot s (s0 + s of the call) of expert e to base[e] + its place.
+// The slots of the only workgroup to their places: slot s of expert e to base[e] + its place.
 template <int WAVES, class Id>
-__device__ __forceinline__ void place_slots(const RouteArgs &g, int64_t s0, int n, int bits, int *run,
-                                            const int *base, int live, Id id) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = ((n + WAVES - 1) / WAVES + 63) & ~63;
+__device__ __forceinline__ void place_slots(const RouteArgs &g, int n, int bits, int *run, const int *base, int live, Id id) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = slots_per_wave<WAVES>(n);
     for (int g0 = wave * per; g0 < min(n, wave * per + per); g0 += 64) {
         const int s = g0 + lane;
         const int e = s < n ? id(s) : -1;
         const int at = take_places(e, bits, run + wave * g.E);
         if (s >= n) continue;
         const int to = e >= 0 ? base[e] + at : -1;
-        g.places[s0 + s] = to;
-        if (to >= 0) g.rows[to] = (int)(s0 + s);
-        if (s0 + s >= live) g.rows[s0 + s] = -1;  // behind the last expert's rows
+        g.places[s] = to;
+        if (to >= 0) g.rows[to] = s;
+        if (s >= live) g.rows[s] = -1;  // behind the last expert's rows
     }
 }
 
 template <int LPT, int PER, int WAVES>
-__device__ __forceinline__ void choose_all(const RouteArgs &g, int64_t t0, int tokens, int16_t *ids) {
+__device__ __forceinline__ void choose_all(const RouteArgs &g, int64_t t0, int tokens, int16_t *ids, uint32_t *keys) {
     constexpr int AT_ONCE = WAVES * (64 / LPT);
     for (int i = 0; i < tokens; i += AT_ONCE) {
         const int mine = i + (int)threadIdx.x / LPT;
-        choose<LPT, PER>(g, t0 + mine, mine < tokens, ids + (size_t)mine * g.k);
+        choose<LPT, PER>(g, t0 + mine, mine < tokens, ids + (size_t)mine * g.k, keys + (size_t)mine * g.k);
     }
     __syncthreads();
 }
@@ -247,106 +279,139 @@ __global__ __launch_bounds__(1024) void route_one(RouteArgs g) {
     constexpr int WAVES = 16;
     extern __shared__ int lds[];
     int *run = lds, *total = run + WAVES * g.E, *all = total + g.E;
-    int16_t *ids = (int16_t *)(all + 1);
-    choose_all<LPT, PER, WAVES>(g, 0, (int)g.T, ids);
-    const int n = (int)g.T * g.k, bits = expert_bits(g.E);
+    uint32_t *keys = (uint32_t *)(all + 1);
+    const int n = (int)g.T * g.k;
+    int16_t *ids = (int16_t *)(keys + n);
+    choose_all<LPT, PER, WAVES>(g, 0, (int)g.T, ids, keys);
+    const int bits = expert_bits(g.E);
     auto id = [&](int s) { return (int)ids[s]; };
     count_slots<WAVES>(n, g.E, bits, run, total, id);
     scan_experts(total, g.E, all);
     __syncthreads();
     for (int e = threadIdx.x; e <= g.E; e += 64 * WAVES) g.offsets[e] = e < g.E ? total[e] : *all;
-    place_slots<WAVES>(g, 0, n, bits, run, total, *all, id);
+    place_slots<WAVES>(g, n, bits, run, total, *all, id);
 }
 
-// First of two launches: choice of the workgroup's tokens, and its slots of each expert to counts[workgroup][e].
+constexpr int kChooseWaves = 8;
+
+// First of two launches: choice of the workgroup's tokens; each slot's place among the workgroup's of its expert (into
+// `places`, for now), and how many it has of each expert, to counts[workgroup][e].
 template <int LPT, int PER>
-__global__ __launch_bounds__(256) void route_choose(RouteArgs g, int block_tokens, int *__restrict__ counts) {
-    constexpr int WAVES = 4;
+__global__ __launch_bounds__(64 * kChooseWaves) void route_choose(RouteArgs g, int block_tokens, int *__restrict__ counts) {
+    constexpr int WAVES = kChooseWaves;
     extern __shared__ int lds[];
-    int *total = lds;
-    int16_t *ids = (int16_t *)(total + g.E);
+    int *run = lds, *total = run + WAVES * g.E;
+    uint32_t *keys = (uint32_t *)(total + g.E);
+    int16_t *ids = (int16_t *)(keys + block_tokens * g.k);
     const int64_t t0 = (int64_t)blockIdx.x * block_tokens;
-    const int tokens = (int)min((int64_t)block_tokens, g.T - t0);
-    for (int e = threadIdx.x; e < g.E; e += 64 * WAVES) total[e] = 0;
-    choose_all<LPT, PER, WAVES>(g, t0, tokens, ids);
-    for (int s = threadIdx.x; s < tokens * g.k; s += 64 * WAVES)
-        if (ids[s] >= 0) atomicAdd(total + ids[s], 1);  // (whole numbers: the order does not show)
-    __syncthreads();
+    const int tokens = (int)max((int64_t)0, min((int64_t)block_tokens, g.T - t0)), n = tokens * g.k;
+    choose_all<LPT, PER, WAVES>(g, t0, tokens, ids, keys);
+    const int bits = expert_bits(g.E);
+    auto id = [&](int s) { return (int)ids[s]; };
+    count_slots<WAVES>(n, g.E, bits, run, total, id);
     for (int e = threadIdx.x; e < g.E; e += 64 * WAVES) counts[(size_t)blockIdx.x * g.E + e] = total[e];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = slots_per_wave<WAVES>(n);
+    for (int s0 = wave * per; s0 < min(n, wave * per + per); s0 += 64) {
+        const int s = s0 + lane;
+        const int at = take_places(s < n ? id(s) : -1, bits, run + wave * g.E);
+        if (s < n) g.places[t0 * g.k + s] = at;
+    }
 }
 
 // Second: where each expert begins (the counts of all workgroups), where this workgroup's slots of it
 // begin (those before it), and the slots' places.
-__global__ __launch_bounds__(256) void route_place(RouteArgs g, int block_tokens, const int *__restrict__ counts) {
-    constexpr int WAVES = 4;
+__global__ __launch_bounds__(1024) void route_place(RouteArgs g, int block_tokens, const int *__restrict__ counts) {
+    constexpr int THREADS = 1024;
     extern __shared__ int lds[];
-    int *run = lds, *total = run + WAVES * g.E, *base = total + g.E, *all = base + g.E;
+    int *total = lds, *base = total + g.E, *all = base + g.E;
     const int blocks = gridDim.x, me = blockIdx.x, E = g.E;
     const int64_t s0 = (int64_t)me * block_tokens * g.k;
     const int n = (int)min((int64_t)block_tokens * g.k, g.T * g.k - s0);
-    const int bits = expert_bits(E);
-    const int32_t *mine = g.experts + s0;
-    auto id = [&](int s) { return mine[s]; };
-    count_slots<WAVES>(n, E, bits, run, total, id);
-    for (int e = threadIdx.x; e < E; e += 64 * WAVES) total[e] = base[e] = 0;
+    int expert = -1, rank = 0;  // of the thread's first slot, on their way while the counts are added up
+    if ((int)threadIdx.x < n) {
+        expert = g.experts[s0 + threadIdx.x];
+        rank = g.places[s0 + threadIdx.x];
+    }
+    for (int e = threadIdx.x; e < E; e += THREADS) total[e] = base[e] = 0;
     __syncthreads();
     // thread: one expert, every parts-th workgroup
-    const int parts = max(1, 64 * WAVES / E);
-    for (int i = threadIdx.x; i < E * parts; i += 64 * WAVES) {
+    const int parts = max(1, THREADS / E);
+    for (int i = threadIdx.x; i < E * parts; i += THREADS) {
         const int e = i % E;
         int sum = 0, before = 0;
-        for (int b = i / E; b < blocks; b += 8 * parts) {
-            int c[8];
+        constexpr int kB = 16;  // loads in flight together
+        for (int b = i / E; b < blocks; b += kB * parts) {
+            int c[kB];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) c[u] = b + u * parts < blocks ? counts[(size_t)(b + u * parts) * E + e] : 0;
+            for (int u = 0; u < kB; ++u) c[u] = b + u * parts < blocks ? counts[(size_t)(b + u * parts) * E + e] : 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < kB; ++u) {
                 sum += c[u];
                 before += b + u * parts < me ? c[u] : 0;
             }
         }
-        atomicAdd(total + e, sum);
+        atomicAdd(total + e, sum);  // (whole numbers: the order does not show)
         atomicAdd(base + e, before);
     }
     __syncthreads();
     scan_experts(total, E, all);
     __syncthreads();
     if (me == 0)
-        for (int e = threadIdx.x; e <= E; e += 64 * WAVES) g.offsets[e] = e < E ? total[e] : *all;
-    for (int e = threadIdx.x; e < E; e += 64 * WAVES) base[e] += total[e];
-    __syncthreads();
-    place_slots<WAVES>(g, s0, n, bits, run, base, *all, id);
+        for (int e = threadIdx.x; e <= E; e += THREADS) g.offsets[e] = e < E ? total[e] : *all;
+    const int live = *all;
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const int64_t s = s0 + i;
+        if (i >= THREADS) {
+            expert = g.experts[s];
+            rank = g.places[s];
+        }
+        const int to = expert >= 0 ? total[expert] + base[expert] + rank : -1;
+        g.places[s] = to;
+        if (to >= 0) g.rows[to] = (int)s;
+        if (s >= live) g.rows[s] = -1;  // behind the last expert's rows
+    }
 }
 
+// One launch: as many lanes to a token as it has experts for, for the shortest chain.
 template <int LPT, int PER>
-static hipError_t launch_route_t(const RouteArgs &g, const RoutePlan &p, hipStream_t st) {
-    if (p.blocks == 1) {
-        if constexpr (PER <= 8) {  // (the planner gives more experts two launches: their counts would not fit)
-            const size_t lds = (size_t)(17 * g.E + 1) * 4 + (size_t)g.T * g.k * 2;
-            hipLaunchKernelGGL((route_one<LPT, PER>), dim3(1), dim3(1024), lds, st, g);
-            return hipGetLastError();
-        }
-        return hipErrorInvalidValue;
-    }
-    const size_t lds = (size_t)g.E * 4 + (size_t)p.block_tokens * g.k * 2;
-    hipLaunchKernelGGL((route_choose<LPT, PER>), dim3((unsigned)p.blocks), dim3(256), lds, st, g, p.block_tokens,
-                       p.counts);
+static hipError_t launch_one(const RouteArgs &g, hipStream_t st) {
+    const size_t lds = (size_t)(17 * g.E + 1) * 4 + (size_t)g.T * g.k * 6;
+    hipLaunchKernelGGL((route_one<LPT, PER>), dim3(1), dim3(1024), lds, st, g);
+    return hipGetLastError();
+}
+// Two launches: up to eight experts a lane.  A round of choosing costs a wave about 3 instructions an expert of
+// its lanes and 12 more, whatever the tokens it has: 8191 tokens of 128 experts take 9.5 us by 64 lanes each and 5 by 16.
+template <int LPT, int PER>
+static hipError_t launch_two(const RouteArgs &g, const RoutePlan &p, hipStream_t st) {
+    const size_t lds = (size_t)(kChooseWaves + 1) * g.E * 4 + (size_t)p.block_tokens * g.k * 6;
+    hipLaunchKernelGGL((route_choose<LPT, PER>), dim3((unsigned)p.blocks), dim3(64 * kChooseWaves), lds, st, g,
+                       p.block_tokens, p.counts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(route_place, dim3((unsigned)p.blocks), dim3(256), (size_t)(6 * g.E + 1) * 4, st, g,
+    hipLaunchKernelGGL(route_place, dim3((unsigned)p.blocks), dim3(1024), (size_t)(2 * g.E + 1) * 4, st, g,
                        p.block_tokens, p.counts);
     return hipGetLastError();
 }
 
 hipError_t launch_route(const RouteArgs &g, const RoutePlan &p, hipStream_t st) {
-    if (g.E <= 8) return launch_route_t<8, 1>(g, p, st);
-    if (g.E <= 16) return launch_route_t<16, 1>(g, p, st);
-    if (g.E <= 32) return launch_route_t<32, 1>(g, p, st);
-    if (g.E <= 64) return launch_route_t<64, 1>(g, p, st);
-    if (g.E <= 128) return launch_route_t<64, 2>(g, p, st);
-    if (g.E <= 256) return launch_route_t<64, 4>(g, p, st);
-    if (g.E <= 512) return launch_route_t<64, 8>(g, p, st);
-    return launch_route_t<64, 16>(g, p, st);
+    if (p.blocks == 1) {
+        if (g.E <= 8) return launch_one<8, 1>(g, st);
+        if (g.E <= 16) return launch_one<16, 1>(g, st);
+        if (g.E <= 32) return launch_one<32, 1>(g, st);
+        if (g.E <= 64) return launch_one<64, 1>(g, st);
+        if (g.E <= 128) return launch_one<64, 2>(g, st);
+        if (g.E <= 256) return launch_one<64, 4>(g, st);
+        if (g.E <= 512) return launch_one<64, 8>(g, st);
+        return hipErrorInvalidValue;  // (the planner gives more experts two launches)
+    }
+    if (g.E <= 8) return launch_two<8, 1>(g, p, st);
+    if (g.E <= 16) return launch_two<8, 2>(g, p, st);
+    if (g.E <= 32) return launch_two<8, 4>(g, p, st);
+    if (g.E <= 64) return launch_two<8, 8>(g, p, st);
+    if (g.E <= 128) return launch_two<16, 8>(g, p, st);
+    if (g.E <= 256) return launch_two<32, 8>(g, p, st);
+    if (g.E <= 512) return launch_two<64, 8>(g, p, st);
+    return launch_two<64, 16>(g, p, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -73,6 +73,11 @@ def test_route_masks(T, E, k):
         check(l, k, renormalize)
 
 
+@pytest.mark.parametrize("T", [0, 1, 2, 3])
+def test_few_tokens_of_many_experts(T):
+    check(randn(T, T, 700), 8, False)
+
+
 def test_all_tokens_of_one_expert():
     l = torch.full((3000, 40), -torch.inf)
     l[:, 17] = 0
