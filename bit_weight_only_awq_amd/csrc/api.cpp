@@ -1173,9 +1173,10 @@ int awq_moe_route(const void *logits, float *weights, int32_t *experts, int32_t 
     if (!known_dtype(dtype) && dtype != AWQ_DTYPE_F32) return AWQ_EINVAL;
     if ((renormalize != 0 && renormalize != 1) || !offsets) return AWQ_EINVAL;
     if (T > 0 && (!logits || !weights || !experts || !rows || !places)) return AWQ_EINVAL;
-    for (const void *q : {logits, (const void *)weights, (const void *)experts, (const void *)offsets,
-                          (const void *)rows, (const void *)places})
-        if (!aligned16(q)) return AWQ_EALIGN;
+    if (!aligned16(logits)) return AWQ_EALIGN;
+    for (const void *q : {(const void *)weights, (const void *)experts, (const void *)offsets, (const void *)rows,
+                          (const void *)places})
+        if (!aligned_to(q, 4)) return AWQ_EALIGN;
     RoutePlan p = plan_route(T, E, k);
     rc = check_workspace(workspace, workspace_bytes, p.blocks == 1 ? 0 : (size_t)p.blocks * E * 4);
     if (rc != AWQ_OK) return rc;

@@ -593,13 +593,18 @@ def moe_route(logits, top_k: int, renormalize: bool = False, out=None):
     grouped by expert take; places: what moe_combine takes."""
     _need_gpu(logits, _LOGITS, 2, "logits")
     T, E = logits.shape
-    dev, index = logits.device, logits.get_device()
-    shapes = ((T, top_k), (T, top_k), (E + 1,), (T * top_k,), (T * top_k,))
+    dev, index, slots = logits.device, logits.get_device(), T * top_k
     if out is None:
-        out = tuple(torch.empty(s, dtype=torch.int32 if i else torch.float32, device=dev) for i, s in enumerate(shapes))
+        # (one piece of memory for the whole numbers: an allocation takes longer than a token's routing)
+        experts, rows, places, offsets = torch.empty(3 * slots + E + 1, dtype=torch.int32, device=dev).split(
+            (slots, slots, slots, E + 1))
+        out = (torch.empty(T, top_k, dtype=torch.float32, device=dev), experts.view(T, top_k), offsets, rows, places)
     else:
-        for i, (t, s) in enumerate(zip(out, shapes, strict=True)):
-            _tensor(t, s, torch.int32 if i else torch.float32, index, "weights, experts, offsets, rows and places")
+        weights, experts, offsets, rows, places = out
+        what = "weights, experts, offsets, rows and places"
+        _tensor(weights, (T, top_k), torch.float32, index, what)
+        for t, shape in ((experts, (T, top_k)), (offsets, (E + 1,)), (rows, (slots,)), (places, (slots,))):
+            _tensor(t, shape, torch.int32, index, what)
     lib = L.lib()
     need = lib.awq_moe_route_workspace_bytes(T, E, top_k)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None

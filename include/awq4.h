@@ -33,7 +33,7 @@
  *  - All tensors are dense, row-major and contiguous, in device memory owned
  *    by the caller (awq_kv4_append takes token strides).  Device pointers must
  *    be 16-byte aligned (AWQ_EALIGN), those of the kv4 calls' index arrays
- *    and of the products' offsets and rows aligned to their type.
+ *    and awq_moe_*'s index arrays and weights aligned to their type.
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *    Work is enqueued on it; no entry point synchronises or allocates device
  *    memory, so all of them are asynchronous and safe to call from several

@@ -22,9 +22,10 @@ def test_route_refuses(kw):
     assert route(**kw) == L.AWQ_EINVAL
 
 
-@pytest.mark.parametrize("arg", ["logits", "w", "ids", "off", "rows", "places"])
-def test_route_alignment(arg):
-    assert route(**{arg: MIS8}) == L.AWQ_EALIGN
+@pytest.mark.parametrize("kw", [dict(logits=MIS8), dict(w=MIS2), dict(ids=MIS2), dict(off=MIS2), dict(rows=MIS2),
+                                dict(places=MIS2)])
+def test_route_alignment(kw):
+    assert route(**kw) == L.AWQ_EALIGN
 
 
 def test_route_workspace():
