@@ -190,12 +190,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
 }
 
 // The K splits' sums [S][M][N], added in split order, written and cleared; one thread a quad of outputs.  Rows behind
-// the last expert's have none.
+// the last expert's are not written, but cleared like the others: offsets that are no plan leave nothing behind either.
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_block_split_sum(f32x4 *__restrict__ part, uint16_t *__restrict__ y,
                                                            const int32_t *__restrict__ rows, int64_t quads, int N, int S) {
     const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (q >= (rows ? min(quads, (int64_t)max(*rows, 0) * (N / 4)) : quads)) return;
+    if (q >= quads) return;
+    const bool live = !rows || q < (int64_t)max(*rows, 0) * (N / 4);
     f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
     constexpr int kB = 4;
     for (int s0 = 0; s0 < S; s0 += kB) {
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(256) void fp8_block_split_sum(f32x4 *__restrict__ p
         for (int i = 0; i < kB; ++i)
             if (s0 + i < S) v += b[i];
     }
-    *(uint2 *)(y + 4 * q) = quad_out_bits<DT>(v);
+    if (live) *(uint2 *)(y + 4 * q) = quad_out_bits<DT>(v);
     for (int s = 0; s < S; ++s) part[q + s * quads] = (f32x4){0.f, 0.f, 0.f, 0.f};
 }
 

@@ -570,7 +570,7 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _on_device(index: int, fn, *args):
-    """fn(*args) with device `index` current (the planners ask for the current device)."""
+    """fn(*args) with device `index` current: the planners ask for the current device, and launches go to it."""
     if torch._C._cuda_getDevice() == index:
         return fn(*args)
     with torch.cuda.device(index):
@@ -608,8 +608,8 @@ def moe_route(logits, top_k: int, renormalize: bool = False, out=None):
     lib = L.lib()
     need = lib.awq_moe_route_workspace_bytes(T, E, top_k)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    status = lib.awq_moe_route(logits.data_ptr(), *[t.data_ptr() for t in out], T, E, top_k, int(renormalize),
-                               _LOGITS[logits.dtype], _ptr(ws), need, _raw_stream(index))
+    status = _on_device(index, lib.awq_moe_route, logits.data_ptr(), *[t.data_ptr() for t in out], T, E, top_k,
+                        int(renormalize), _LOGITS[logits.dtype], _ptr(ws), need, _raw_stream(index))
     if status:
         L.check("awq_moe_route", status)
     return out
@@ -627,8 +627,8 @@ def moe_combine(y, weights, places, out=None):
         out = torch.empty(T, N, dtype=y.dtype, device=y.device)
     else:
         _tensor(out, (T, N), y.dtype, index, "out")
-    status = L.lib().awq_moe_combine(y.data_ptr(), weights.data_ptr(), places.data_ptr(), out.data_ptr(), T, R, N, k,
-                                     _F16[y.dtype], _raw_stream(index))
+    status = _on_device(index, L.lib().awq_moe_combine, y.data_ptr(), weights.data_ptr(), places.data_ptr(),
+                        out.data_ptr(), T, R, N, k, _F16[y.dtype], _raw_stream(index))
     if status:
         L.check("awq_moe_combine", status)
     return out
@@ -667,9 +667,9 @@ def moe_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, top_k: int = 
     need = _on_device(index, lib.awq_moe_gemm_w4a16_workspace_bytes, R, E, N, K, group_size)
     stream = _raw_stream(index)
     ws, ws_bytes = WORKSPACE.of_stream(index, stream, need) if need else (None, 0)
-    status = lib.awq_moe_gemm_w4a16(x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr(qzeros), offsets_ptr,
-                                    rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, group_size, _F16[x.dtype], ws,
-                                    ws_bytes, stream)
+    status = _on_device(index, lib.awq_moe_gemm_w4a16, x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr(qzeros),
+                        offsets_ptr, rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, group_size, _F16[x.dtype], ws,
+                        ws_bytes, stream)
     if status:
         L.check("awq_moe_gemm_w4a16", status)
     return out
@@ -689,8 +689,8 @@ def quant_act_fp8_block(x, a=None, s=None):
         s = torch.empty(M, blocks, dtype=torch.float32, device=x.device)
     else:
         _tensor(s, (M, blocks), torch.float32, index, "s")
-    status = L.lib().awq_fp8_block_quant_act(x.data_ptr(), a.data_ptr(), s.data_ptr(), M, K, _F16[x.dtype],
-                                             _raw_stream(index))
+    status = _on_device(index, L.lib().awq_fp8_block_quant_act, x.data_ptr(), a.data_ptr(), s.data_ptr(), M, K,
+                        _F16[x.dtype], _raw_stream(index))
     if status:
         L.check("awq_fp8_block_quant_act", status)
     return a, s
@@ -718,12 +718,12 @@ def _fp8_block(a, w, sa, sw, plan, top_k, dtype, out):
     stream = _raw_stream(index)
     ws, ws_bytes = WORKSPACE.of_stream(index, stream, need) if need else (None, 0)
     if plan is None:
-        status = lib.awq_fp8_block_gemm(a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(), out.data_ptr(), R, N,
-                                        K, _F16[dtype], ws, ws_bytes, stream)
+        status = _on_device(index, lib.awq_fp8_block_gemm, a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(),
+                            out.data_ptr(), R, N, K, _F16[dtype], ws, ws_bytes, stream)
     else:
-        status = lib.awq_moe_fp8_block_gemm(a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(), offsets_ptr,
-                                            rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, _F16[dtype], ws,
-                                            ws_bytes, stream)
+        status = _on_device(index, lib.awq_moe_fp8_block_gemm, a.data_ptr(), w.data_ptr(), sa.data_ptr(), sw.data_ptr(),
+                            offsets_ptr, rows_ptr, out.data_ptr(), R, x_rows, top_k, E, N, K, _F16[dtype], ws, ws_bytes,
+                            stream)
     if status:
         L.check("awq_fp8_block_gemm" if plan is None else "awq_moe_fp8_block_gemm", status)
     return out
