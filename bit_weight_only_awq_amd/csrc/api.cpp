@@ -666,7 +666,8 @@ static int check_route(int64_t T, int64_t E, int64_t k) {
 }
 // One launch for as many tokens as one workgroup's waves take at once, and up to 512 experts
 // (whose counts fit its LDS beside the slots); else two, of workgroups of 16 tokens or more,
-// 256 of them at most while the slots of one fit its LDS.
+// 256 of them at most while the slots of one fit its LDS.  (16 tokens of 64 experts: 7.1 us in one
+// launch; 17 in two: 9.4.)
 static RoutePlan plan_route(int64_t T, int64_t E, int64_t k) {
     RoutePlan p{};
     p.block_tokens = (int)std::min<int64_t>(std::max<int64_t>(16, cdiv(T, 256)), 8192 / k);
@@ -698,6 +699,16 @@ static int check_moe_w4a16_shape(int64_t R, int64_t E, int64_t N, int64_t K, int
     if ((G != 32 && G != 64 && G != 128) || K % G) return AWQ_EINVAL;
     return AWQ_OK;
 }
+// The kernel by the rows an expert has on average, over the experts that R rows reach.  Two
+// experts of eight a token, 14336 -> 4096, us by rows an expert:
+//   rows         8    12    16    32    48    64    80
+//   stream, 16  60    85    95   164   166
+//   stream, 32  79    82    84   133   135   200
+//   LDS, 128                           196   196   270
+// From 80 on the streaming kernel would read the weights three times.  Over 128 the LDS kernel's
+// 256-row tiles have 100 rows or more to take (a half as many reads of the weights' words per product).
+// Streaming workgroups split K while two a CU are not there (us for 1, 2, 3, 4 splits: 128 tiles 88,
+// 83, 64, 60; 210 tiles 32.3, 32.3, 34.4, 35.6) and every wave keeps two chunks.
 static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
     W4A16Plan p{};
     const double live = live_experts(R, E), avg = (double)R / live;
@@ -739,11 +750,18 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     // workgroups to be expected with tiles of so many rows and columns
     auto workgroups = [&](int64_t rows, int64_t cols) { return cdiv(N, cols) * live * std::ceil(avg / (double)rows); };
     // Up to 16 rows (of an expert: 4, whose tiles are many without a K split), the
-    // streaming kernel.
+    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128, 14336 -> 4096 with 17
+    // 22.2 against 18.5 (16 rows 21.2 against 19.6); 64 experts with 2.2 rows each 40 against 46, 4 rows 51
+    // against 48.5, 8 rows 64 against 52.  Tiles of 256 where they reach 6 of 10 CUs: 4096 -> 14336 with 512
+    // rows (112 tiles) 57 us against 45 by tiles of 128, 768 (168) 57 against 64, 2048 122 against 148; 14336 ->
+    // 4096 with 1024 (64) 161 against 89; and experts of more than 192 rows (187: 118 both, 375: 164
+    // against 194, 97: 105 against 87).
     p.tile = avg <= (E ? 4 : 16) ? 0 : avg > 192 && workgroups(256, 256) >= 0.6 * d.cus ? 256 : 128;
     const int64_t rows = p.tile ? p.tile : kFp8StreamRows, cols = p.tile ? p.tile : kFp8StreamCols;
     p.tiles_n = (int)cdiv(N, cols);
     p.tiles_m = (int)row_tiles(rows);
+    // K splits, of 8 blocks at least: workgroups of tiles of 128 up to 1.5 a CU (us for 1, 2, 4, 8 splits: 32
+    // tiles 82, 48, 30, 26; 64 tiles 85, 52, 36, 38; 112 tiles 29, 25, 27, 40; 224 tiles 31, 39), streaming ones 2.
     const double fill = p.tile == 256 ? 0 : p.tile ? 1.5 : 2;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(fill * d.cus / workgroups(rows, cols)), blocks / 8, 8}));
     if (p.splits > 1)

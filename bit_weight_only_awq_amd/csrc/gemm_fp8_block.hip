@@ -1,9 +1,11 @@
 // gemm_fp8_block.hip -- block-scaled E4M3 products of many rows (fp8_block.hpp
 // has the arithmetic): tiles through LDS.
 //
-// A workgroup of 8 waves has BN = 256 outputs n and BM = 256 or 128 tokens, a wave
-// NT x MT tiles of 16 x 16 of them.  A stage is one block of 128 k: 128 bytes of
-// each row of both matrices, copied straight into one of two LDS slots.
+// A workgroup has a tile of BN outputs n by BM tokens, a wave NT x MT tiles of 16 x 16 of them: 256 x 256 by
+// 8 waves, one workgroup a CU, or where those would leave CUs without work 128 x 128 by 4 waves, two a CU,
+// and K split over workgroups where even these are few (an fp32 sum for each split, added in
+// split order by a launch of its own).  A stage is one block of 128 k: 128 bytes of each row of both
+// matrices, copied straight into one of two LDS slots.
 //
 // One barrier a stage, and no wave waits for LDS behind it: a wave holds all NT weight
 // operands of the stage and goes through its tokens 16 at a time, the
@@ -23,7 +25,10 @@
 // sum's FMAs take issue slots from the matrix cores: beside four FMAs an instruction of 32 cycles
 // takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2400 are reached
 // where the tiles are as many as the CUs (4096 x 4096 x 14336), the rest goes to
-// the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).
+// the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).  4096 x 14336 x 4096 is 896 tiles,
+// 3.5 for each CU where the last half is waited for in full.  With few rows the memory bounds: 777
+// tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB) 88 us, of which the weights alone
+// take 53.
 #include "fp8_block.hpp"
 
 namespace awq4 {
@@ -82,18 +87,20 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     } else if (wave == BM / 64 && lane < BN / kBlk) {
         so = (uint32_t)((n0 / kBlk + lane) * blocks) * 4u;
     }
-    // copy i of stage st, whose rows have `left` 16-byte segments
+    // copy i of stage st, whose rows have `left` 16-byte segments (none past the last stage; the wave's offset then
+    // stays inside the buffers)
     auto copy1 = [&](int st, int left, auto ic) {
         constexpr int i = decltype(ic)::value;
         constexpr bool isw = i < W_COPIES;
         unsigned char *const dst = lds + (st & 1) * STAGE + (isw ? 0 : W_BYTES) +
                                    (wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES)) * 1024;
         const int c = wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES);
-        dma16_buf(isw ? wr : ar, (seg0 ^ (c & 1)) < left ? off[i] : kOut, (uint32_t)st * kBlk, dst);
+        dma16_buf(isw ? wr : ar, (seg0 ^ (c & 1)) < left ? off[i] : kOut, left ? (uint32_t)st * kBlk : 0u, dst);
     };
     auto copy_scales = [&](int st) {
         if (scales && (st & 3) == 0 && st < s_hi && (row_scales || lane < BN / kBlk))
-            dma16_buf(sr, so, (uint32_t)st * 4u, lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
+            // (in the lane's offset, which is checked: four scales may reach past the last row's)
+            dma16_buf(sr, so + (uint32_t)st * 4u, 0u, lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
     };
     auto left_of = [&](int st) { return st < s_hi ? min((K - st * kBlk) / 16, 8) : 0; };
 
@@ -189,14 +196,17 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     }
 }
 
-// The K splits' sums [S][M][N], added in split order, written and cleared; one thread a quad of outputs.  Rows behind
-// the last expert's are not written, but cleared like the others: offsets that are no plan leave nothing behind either.
+// The K splits' sums [S][M][N], added in split order, written and cleared; one thread a quad of outputs.  Rows before the
+// first expert's and behind the last's (offsets: the one and the other) are not written, but cleared like the others:
+// offsets that are no plan leave nothing behind either.
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_block_split_sum(f32x4 *__restrict__ part, uint16_t *__restrict__ y,
-                                                           const int32_t *__restrict__ rows, int64_t quads, int N, int S) {
+                                                           const int32_t *__restrict__ offsets, int E, int64_t quads,
+                                                           int N, int S) {
     const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (q >= quads) return;
-    const bool live = !rows || q < (int64_t)max(*rows, 0) * (N / 4);
+    const int64_t row = q / (N / 4);
+    const bool live = !offsets || (row >= offsets[0] && row < offsets[E]);
     f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
     constexpr int kB = 4;
     for (int s0 = 0; s0 < S; s0 += kB) {
@@ -221,13 +231,13 @@ static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStre
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t quads = (int64_t)g.M * g.N / 4;
     const dim3 sums((unsigned)((quads + 255) / 256));
-    const int32_t *const rows = g.groups.offsets ? g.groups.offsets + g.groups.E : nullptr;
+    const int32_t *const offsets = g.groups.offsets;
     if (g.dtype == DT_BF16)
-        hipLaunchKernelGGL(fp8_block_split_sum<DT_BF16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, rows, quads, g.N,
-                           p.splits);
+        hipLaunchKernelGGL(fp8_block_split_sum<DT_BF16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, offsets,
+                           g.groups.E, quads, g.N, p.splits);
     else
-        hipLaunchKernelGGL(fp8_block_split_sum<DT_F16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, rows, quads, g.N,
-                           p.splits);
+        hipLaunchKernelGGL(fp8_block_split_sum<DT_F16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, offsets,
+                           g.groups.E, quads, g.N, p.splits);
     return hipGetLastError();
 }
 

@@ -380,7 +380,7 @@ static hipError_t launch_one(const RouteArgs &g, hipStream_t st) {
     return hipGetLastError();
 }
 // Two launches: up to eight experts a lane.  A round of choosing costs a wave about 3 instructions an expert of
-// its lanes and 12 more, whatever the tokens it has: 8191 tokens of 128 experts take 9.5 us by 64 lanes each and 5 by 16.
+// its lanes and 12 more, whatever the tokens it has: 8191 tokens of 128 experts take 9.5 us by 64 lanes each and 6 by 16.
 template <int LPT, int PER>
 static hipError_t launch_two(const RouteArgs &g, const RoutePlan &p, hipStream_t st) {
     const size_t lds = (size_t)(kChooseWaves + 1) * g.E * 4 + (size_t)p.block_tokens * g.k * 6;

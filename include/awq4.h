@@ -593,18 +593,25 @@ size_t awq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  *   x:       device [x_rows, K] (dtype).
  *   qweight: device int32 [E, K, N/8], scales [E, K/G, N], qzeros int32
  *            [E, K/G, N/8] or NULL, each expert's as for awq_gemm_w4a16.
- *   offsets: device int32 [E + 1], from 0, not falling, at most R.  (Whatever
- *            they hold, nothing outside the tensors is read or written.)
+ *   offsets: device int32 [E + 1], not falling, in 0 .. R: a plan's, or for some
+ *            consecutive experts' matrices its part from the first of them on.
+ *            (Whatever they hold, nothing outside the tensors is read or written.)
  *   rows:    device int32 [R]: row r reads x[rows[r] / top_k] (the plan's rows:
  *            the first product of a layer, x one row a token); or NULL: it reads
  *            x[r] (x_rows == R; the second one, on rows in the plan's order).  An entry
  *            that names no row of x reads row 0.
- *   y:       device [R, N]; rows from offsets[E] on are not written.
+ *   y:       device [R, N]; rows before offsets[0] and from offsets[E] on are not
+ *            written.
  *   G, K, N as for awq_gemm_w4a16; E <= 1024, R <= 2^24, 1 <= top_k <= 32.  With
- *   rows, x is under 2^31 bytes (AWQ_EUNSUPPORTED).  One kernel takes the whole call, by
- *   R / E: rows per expert, if all had alike.
- * Numerics: up to 48 rows an expert (R over the experts that R rows reach on
- * average) as awq_gemm_w4a16 for M <= 64, else as for M > 64.
+ *   rows, x is under 2^31 bytes, and an expert's words are in any case (else
+ *   AWQ_EUNSUPPORTED).  One kernel takes the whole call, chosen by R over the
+ *   experts that R rows reach on average, as if all had alike.
+ * Numerics: up to 64 such rows an expert, and where K % 64 or N % 32 is not 0,
+ *   y = act( sum over runs of min(G, 64) k of s ( sum x q' - z' sum x ) )
+ * with q' = q and z' = z (fp16), or both 128 more (bf16): exact operands of the fp32
+ * matrix cores, weights that are not rounded, runs added by fp32 FMAs.  (So an
+ * infinity in a row of x makes the row of y NaN, and in bf16 |x| is to stay under
+ * 2^113.)  Else as awq_gemm_w4a16 for M > 64: weights rounded once to the activation type.
  * Workspace: as for the GEMMs (shared, zero before and after each call).  R == 0
  * is a no-op that returns AWQ_OK.
  * Errors: AWQ_EINVAL, AWQ_EUNSUPPORTED, AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
@@ -660,7 +667,8 @@ int awq_fp8_block_quant_act(const void *x, uint8_t *a, float *s, int64_t M, int6
  *
  * awq_moe_fp8_block_gemm -- the same with a matrix per expert: w [E, N, K], sw
  * [E, ceil(N/128), ceil(K/128)]; offsets, rows, R, x_rows, top_k and y as for
- * awq_moe_gemm_w4a16, the gathered rows' scales with them.
+ * awq_moe_gemm_w4a16, the gathered rows' scales with them.  With rows, a is under 2^31
+ * bytes (AWQ_EUNSUPPORTED).
  */
 int awq_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
                        int64_t N, int64_t K, int dtype, void *workspace, size_t workspace_bytes, void *stream);

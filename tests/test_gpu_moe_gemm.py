@@ -204,6 +204,33 @@ def test_grouped_product_rows_behind_the_last():
         run_grouped(SPLITS[split], 128, 64, "bf16", True, spare=37)
 
 
+@pytest.mark.parametrize("split,K,N", [([3, 1, 0, 5], 4096, 264), ([40, 33, 64, 31], 4096, 136), ([300, 150, 257, 90], 256, 160)])
+def test_part_of_the_experts(split, K, N):
+    """A plan's offsets from an expert on, with the matrices of some: rows of the others are left as they are."""
+    q, s, z = experts_weights(len(split), K, N, 128, True, "f16", 0)
+    w, sw = e4m3_weights(len(split), N, K, 0)
+    offsets, slots, tokens = plan(split, 2, 0)
+    x = randn(1, tokens, K).half()
+    a, sa = codes(tokens, K, 0)
+    xd, qd, sd, zd, wd, swd, ad, sad, od, rd = cuda(x, q, s, z, w, sw, a, sa, offsets, slots)
+    for part in (slice(0, 1), slice(1, 3), slice(2, 4)):
+        off = od[part.start:part.stop + 1]
+        where = (off.tolist(), slots.tolist(), 2)
+        print(split, part, flush=True)
+        out = torch.full((len(slots), N), 77.0, dtype=torch.float16, device=dev())
+        awq.moe_gemm_w4a16(xd, qd[part], sd[part], zd[part], off, rows=rd, top_k=2, out=out)
+        mats = [moe.dequant(q[e].numpy(), f64(s[e]), z[e].numpy(), 128) for e in range(len(split))[part]]
+        want, size = moe.grouped(f64(x), mats, *where)
+        check(out, len(slots), want, size, HALF_STEP["f16"] + K * 2.0 ** -24, "f16", f"{split} {part}")
+        out.fill_(77.0)
+        awq.moe_gemm_fp8_block(ad, wd[part], sad, swd[part], off, rows=rd, top_k=2, out=out, dtype=torch.float16)
+        mats = [moe.block_values(w[e].numpy(), sw[e].numpy(), 128).T for e in range(len(split))[part]]
+        want, _ = moe.grouped(moe.block_values(a.numpy(), sa.numpy(), 1), mats, *where)
+        sizes = [magnitudes(w[e].numpy(), sw[e].numpy(), 128).T for e in range(len(split))[part]]
+        size, _ = moe.grouped(magnitudes(a.numpy(), sa.numpy(), 1), sizes, *where)
+        check(out, len(slots), want, size, per_size(K), "f16", f"{split} {part}")
+
+
 def test_no_rows_at_all():
     """Offsets of zeros: nothing is written."""
     q, s, z = cuda(*experts_weights(3, 64, 64, 64, True, "f16", 0))

@@ -11,7 +11,9 @@ from oracle import moe
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("T,E,k", [(300001, 16, 2), (70000, 200, 8), (40000, 1024, 16)])
+@pytest.mark.parametrize("T,E,k", [(300001, 16, 2), (70000, 200, 8), (40000, 1024, 16),
+                                   (40000, 1024, 32),  # (more than 64 KB of LDS a workgroup)
+                                   (400000, 40, 32)])
 def test_route_of_many_tokens(T, E, k):
     g = torch.Generator(device=dev()).manual_seed(T)
     l = torch.randn(T, E, generator=g, device=dev()).half()
