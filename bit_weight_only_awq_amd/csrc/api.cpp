@@ -699,27 +699,43 @@ static int check_moe_w4a16_shape(int64_t R, int64_t E, int64_t N, int64_t K, int
     if ((G != 32 && G != 64 && G != 128) || K % G) return AWQ_EINVAL;
     return AWQ_OK;
 }
-// The kernel by the rows an expert has on average, over the experts that R rows reach.  Two
-// experts of eight a token, 14336 -> 4096, us by rows an expert:
-//   rows         8    12    16    32    48    64    80
-//   stream, 16  60    85    95   164   166
-//   stream, 32  79    82    84   133   135   200
-//   LDS, 128                           196   196   270
-// From 80 on the streaming kernel would read the weights three times.  Over 128 the LDS kernel's
-// 256-row tiles have 100 rows or more to take (a half as many reads of the weights' words per product).
+// Tiles of so many rows and columns to be expected, where the experts' rows are spread about their average by a
+// quarter of it: one row tile each, and a further one with the probability that they pass each multiple of `rows`.
+static double expected_tiles(double live, double avg, int64_t N, int64_t rows, int64_t cols) {
+    double t = avg / (double)rows + 0.5;
+    if (t < 8) {
+        const double last = 2 * t;
+        t = 1;
+        for (double j = 1; j < last; ++j) t += 0.5 * std::erfc((j * (double)rows - avg) / (avg / 4 * M_SQRT2));
+    }
+    return cdiv(N, cols) * live * t;
+}
+// The kernel by the rows an expert has on average, over the experts that R rows reach; us by rows an
+// expert, two of eight experts a token:
+//   14336 -> 4096        8    12    16    32    40    48    56   100   150   200   300
+//     stream, 16 rows   60    85    95   164         166
+//     stream, 32        79    82    84   133   134   135   199   242   359
+//     LDS, 128 x 128                     142   147   149   150   207   277   319   444
+//     LDS, 256 x 256                                             357   359   359   378
+//   4096 -> 28672: stream, 32 at 32, 40 and 48 rows 218, 253, 267; LDS, 128 x 128 233, 237, 238
+// The large tiles where a round of theirs (2.7 of the small ones a CU) takes less than all of the small ones.
+// Small tiles split K up to three workgroups a CU, 16 stages each at least: 14336 -> 4096 at 56 rows 198 -> 157 us
+// by 2 splits, at 100 rows 267 -> 207; 4096 -> 4096 at 75 62 -> 58.
 // Streaming workgroups split K while two a CU are not there (us for 1, 2, 3, 4 splits: 128 tiles 88,
 // 83, 64, 60; 210 tiles 32.3, 32.3, 34.4, 35.6) and every wave keeps two chunks.
 static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
     W4A16Plan p{};
     const double live = live_experts(R, E), avg = (double)R / live;
-    if (avg > 64 && K % 64 == 0 && N % 32 == 0) {
+    if (avg > 36 && K % 64 == 0 && N % 32 == 0) {
         p.kind = 3;
-        p.mt = avg > 128 ? 16 : 8;
-        p.wn = avg > 128 ? 8 : 4;
-        p.ksplit = 1;
-        p.splits = 1;
+        const double small = expected_tiles(live, avg, N, 128, 128);
+        const bool wide = 2.7 * d.cus * std::ceil(expected_tiles(live, avg, N, 256, 256) / d.cus) < small;
+        p.mt = wide ? 16 : 8;
+        p.wn = wide ? 8 : 4;
         p.tiles_n = (int)cdiv(N, 32 * p.wn);
         p.tiles_m = (int)group_tiles(R, E, 16 * p.mt);
+        p.splits = wide ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(3 * d.cus / small), K / 64 / 16, 8}));
+        if (p.splits > 1) p.workspace_bytes = (size_t)p.splits * R * N * 4;
         return p;
     }
     p.kind = 5;
@@ -747,26 +763,39 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     const double live = E ? live_experts(M, E) : 1.0, avg = (double)M / live;
     auto row_tiles = [&](int64_t rows) { return E ? group_tiles(M, E, rows) : cdiv(M, rows); };
     const int64_t blocks = cdiv(K, 128);
-    // workgroups to be expected with tiles of so many rows and columns
-    auto workgroups = [&](int64_t rows, int64_t cols) { return cdiv(N, cols) * live * std::ceil(avg / (double)rows); };
+    auto workgroups = [&](int64_t rows, int64_t cols) {
+        return E ? expected_tiles(live, avg, N, rows, cols) : (double)(cdiv(N, cols) * cdiv(M, rows));
+    };
     // Up to 16 rows (of an expert: 4, whose tiles are many without a K split), the
-    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128, 14336 -> 4096 with 17
+    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128 x 128, 14336 -> 4096 with 17
     // 22.2 against 18.5 (16 rows 21.2 against 19.6); 64 experts with 2.2 rows each 40 against 46, 4 rows 51
-    // against 48.5, 8 rows 64 against 52.  Tiles of 256 where they reach 6 of 10 CUs: 4096 -> 14336 with 512
-    // rows (112 tiles) 57 us against 45 by tiles of 128, 768 (168) 57 against 64, 2048 122 against 148; 14336 ->
-    // 4096 with 1024 (64) 161 against 89; and experts of more than 192 rows (187: 118 both, 375: 164
-    // against 194, 97: 105 against 87).
-    p.tile = avg <= (E ? 4 : 16) ? 0 : avg > 192 && workgroups(256, 256) >= 0.6 * d.cus ? 256 : 128;
-    const int64_t rows = p.tile ? p.tile : kFp8StreamRows, cols = p.tile ? p.tile : kFp8StreamCols;
-    p.tiles_n = (int)cdiv(N, cols);
-    p.tiles_m = (int)row_tiles(rows);
+    // against 48.5, 8 rows 64 against 52.
+    // Rows x columns of the others: 128 x 128 where 128 x 256 would leave a fifth of the CUs or more without work,
+    // 256 x 256 where its rounds over the CUs, each of which takes 1.5 of the second's, are fewer by more than
+    // that; by experts, whose last row tiles are part empty, over 2.5 tiles of 128.  us for 128 x 128, 128 x 256,
+    // 256 x 256:
+    //   4096 -> 14336, rows    96: 26, 28        256: 31, 38        500: 42, 41, 57     768: 66, 73, 58
+    //                        1024: 83, 80, 63   1100: 84, 81, 109  4096: 326, 295, 257
+    //   64 experts 2048 -> 2048, rows each 32: 53, 50      97: 89, 80, 105   187: 118, 104, 120
+    //                        250: 146, 131, 135   300: 167, 152, 158   375: 195, 180, 164
+    const bool stream = avg <= (E ? 4 : 16);
+    p.rows = p.cols = 128;
+    if (stream) p.rows = kFp8StreamRows, p.cols = kFp8StreamCols;
+    else if (workgroups(128, 256) >= 0.8 * d.cus) {
+        p.cols = 256;
+        const double large = workgroups(256, 256) / d.cus;
+        if (E ? avg > 320 && large >= 0.8 : 1.5 * std::ceil(large) < std::ceil(workgroups(128, 256) / d.cus)) p.rows = 256;
+    }
+    p.tiles_n = (int)cdiv(N, p.cols);
+    p.tiles_m = (int)row_tiles(p.rows);
     // K splits, of 8 blocks at least: workgroups of tiles of 128 up to 1.5 a CU (us for 1, 2, 4, 8 splits: 32
     // tiles 82, 48, 30, 26; 64 tiles 85, 52, 36, 38; 112 tiles 29, 25, 27, 40; 224 tiles 31, 39), streaming ones 2.
-    const double fill = p.tile == 256 ? 0 : p.tile ? 1.5 : 2;
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(fill * d.cus / workgroups(rows, cols)), blocks / 8, 8}));
+    const double fill = stream ? 2 : p.cols == 128 ? 1.5 : 0;
+    p.splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({(int64_t)(fill * d.cus / workgroups(p.rows, p.cols)), blocks / 8, 8}));
     if (p.splits > 1)
-        p.workspace_bytes = p.tile ? (size_t)p.splits * M * N * 4
-                                   : (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);
+        p.workspace_bytes = !stream ? (size_t)p.splits * M * N * 4
+                                    : (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);
     return p;
 }
 static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, const float *sw, void *y, int64_t M,
@@ -783,7 +812,7 @@ static int run_fp8_block(const uint8_t *a, const uint8_t *w, const float *sa, co
     groups.max_tiles = p.tiles_m;
     const Fp8BlockArgs g{a, w, sa, sw, y, (int)M, (int)N, (int)K, dtype, groups};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return hip_status(p.tile ? launch_fp8_block_gemm(g, p, st) : launch_fp8_block_stream(g, p, st));
+    return hip_status(p.rows > kFp8StreamRows ? launch_fp8_block_gemm(g, p, st) : launch_fp8_block_stream(g, p, st));
 }
 
 }  // namespace awq4

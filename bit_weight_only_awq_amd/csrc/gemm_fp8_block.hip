@@ -2,17 +2,17 @@
 // has the arithmetic): tiles through LDS.
 //
 // A workgroup has a tile of BN outputs n by BM tokens, a wave NT x MT tiles of 16 x 16 of them: 256 x 256 by
-// 8 waves, one workgroup a CU, or where those would leave CUs without work 128 x 128 by 4 waves, two a CU,
-// and K split over workgroups where even these are few (an fp32 sum for each split, added in
-// split order by a launch of its own).  A stage is one block of 128 k: 128 bytes of each row of both
-// matrices, copied straight into one of two LDS slots.
+// 8 waves, where experts or the matrix have fewer rows 256 x 128 by 8 waves, one workgroup a CU either way; or 128 x
+// 128 by 4 waves, two a CU, and K split over workgroups where even these are few (an fp32 sum for each split,
+// added in split order by a launch of its own, split_sum.hip).  A stage is one block of 128 k: 128 bytes of each row of
+// both matrices, copied straight into one of SLOTS LDS slots.
 //
 // One barrier a stage, and no wave waits for LDS behind it: a wave holds all NT weight
 // operands of the stage and goes through its tokens 16 at a time, the
 // operand of the next 16 being read meanwhile.  When the last 16 are in
 // registers, nothing of the stage is left to read: the barrier stands there.
-// Behind it the slot takes the copies of the stage after the next (in flight for a whole
-// stage), and each weight operand is replaced by the next stage's as soon as its last
+// Behind it the slot takes the copies of the stage SLOTS further (in flight for a whole stage, or two with
+// three slots), and each weight operand is replaced by the next stage's as soon as its last
 // matrix-core instruction is issued.  (With the barrier at the stage's end, where the first
 // operands of all waves are read at once while the matrix cores wait: 1566
 // TFLOP/s at 4096 x 14336 x 4096 against 1850.  Two groups of waves taking turns at the
@@ -26,9 +26,13 @@
 // takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2400 are reached
 // where the tiles are as many as the CUs (4096 x 4096 x 14336), the rest goes to
 // the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).  4096 x 14336 x 4096 is 896 tiles,
-// 3.5 for each CU where the last half is waited for in full.  With few rows the memory bounds: 777
-// tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB) 88 us, of which the weights alone
-// take 53.
+// 3.5 for each CU where the last half is waited for in full.  (One workgroup a CU going through its tiles without a
+// pause, the next one's copies under way before the last one's stores: 295 -> 285 us by tiles of 256 x 128, but 257 ->
+// 269 by the large ones, whose registers it overflows.)
+// With few rows the copies bound: 777 tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB of weights)
+// take 80 us, the same copies without a product 75 or so, the weights' alone 53; tiles of 128 x 128, which read the
+// tokens twice as often, 89; 256 x 128 with two slots 93 where three are 80.  Neither another order of the blocks
+// in each tile nor non-temporal copies and stores change that.
 #include "fp8_block.hpp"
 
 namespace awq4 {
@@ -39,14 +43,14 @@ __device__ __forceinline__ int blk_swz(int j) { return (j ^ (j >> 3)) & 7; }  //
 
 constexpr int kFp8Lag = 3;
 
-template <int DT, int NT, int MT, int WN, int WM>
+template <int DT, int NT, int MT, int WN, int WM, int SLOTS>
 __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g, f32x4 *__restrict__ part) {
     constexpr int WAVES = WN * WM, BN = 16 * NT * WN, BM = 16 * MT * WM;
     constexpr int W_BYTES = BN * kBlk, A_BYTES = BM * kBlk, STAGE = W_BYTES + A_BYTES;
-    constexpr int S_BYTES = BM * 16 + 64, LDS = 2 * (STAGE + S_BYTES);
+    constexpr int S_BYTES = BM * 16 + 64, LDS = SLOTS * STAGE + 2 * S_BYTES;
     constexpr int W_COPIES = BN / 8 / WAVES, A_COPIES = BM / 8 / WAVES, COPIES = W_COPIES + A_COPIES;
     static_assert(MT % 2 == 0 && kBlk % (16 * NT) == 0 && BM / 64 < WAVES && BN / kBlk <= 4 && LDS <= 163840, "fits");
-    static_assert(COPIES <= 2 * NT && COPIES < 16, "two copies beside each weight operand at most; the wait's field");
+    static_assert(SLOTS <= 4 && COPIES <= 2 * NT && (SLOTS - 1) * COPIES < 16, "two copies beside each weight operand at most; the wait's field");
     __shared__ __attribute__((aligned(16))) unsigned char lds[LDS];
     const int lane = threadIdx.x & 63, j = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -89,10 +93,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     }
     // copy i of stage st, whose rows have `left` 16-byte segments (none past the last stage; the wave's offset then
     // stays inside the buffers)
-    auto copy1 = [&](int st, int left, auto ic) {
+    auto copy1 = [&](int st, int slot, int left, auto ic) {
         constexpr int i = decltype(ic)::value;
         constexpr bool isw = i < W_COPIES;
-        unsigned char *const dst = lds + (st & 1) * STAGE + (isw ? 0 : W_BYTES) +
+        unsigned char *const dst = lds + slot * STAGE + (isw ? 0 : W_BYTES) +
                                    (wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES)) * 1024;
         const int c = wave * (isw ? W_COPIES : A_COPIES) + (isw ? i : i - W_COPIES);
         dma16_buf(isw ? wr : ar, (seg0 ^ (c & 1)) < left ? off[i] : kOut, left ? (uint32_t)st * kBlk : 0u, dst);
@@ -100,7 +104,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     auto copy_scales = [&](int st) {
         if (scales && (st & 3) == 0 && st < s_hi && (row_scales || lane < BN / kBlk))
             // (in the lane's offset, which is checked: four scales may reach past the last row's)
-            dma16_buf(sr, so + (uint32_t)st * 4u, 0u, lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
+            dma16_buf(sr, so + (uint32_t)st * 4u, 0u, lds + SLOTS * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
     };
     auto left_of = [&](int st) { return st < s_hi ? min((K - st * kBlk) / 16, 8) : 0; };
 
@@ -115,17 +119,19 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
         return operand32(*(const u32x4 *)(p + a0), *(const u32x4 *)(p + a1));
     };
     auto row_scale = [&](int st, int m) {
-        return *(const float *)(lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + 16 * (16 * (wm * MT + m) + j) + 4 * (st & 3));
+        return *(const float *)(lds + SLOTS * STAGE + ((st >> 2) & 1) * S_BYTES + 16 * (16 * (wm * MT + m) + j) + 4 * (st & 3));
     };
     auto col_scale = [&](int st) {
-        return *(const float *)(lds + 2 * STAGE + ((st >> 2) & 1) * S_BYTES + BM * 16 + 16 * (wn * NT * 16 / kBlk) + 4 * (st & 3));
+        return *(const float *)(lds + SLOTS * STAGE + ((st >> 2) & 1) * S_BYTES + BM * 16 + 16 * (wn * NT * 16 / kBlk) + 4 * (st & 3));
     };
     {
-        const int l0 = left_of(s_lo), l1 = left_of(s_lo + 1);
         copy_scales(s_lo);
-        static_for<COPIES>([&](auto ic) { copy1(s_lo, l0, ic); });
-        static_for<COPIES>([&](auto ic) { copy1(s_lo + 1, l1, ic); });
-        __builtin_amdgcn_s_waitcnt(0x0F70 | COPIES);  // stage 0's have landed
+        static_for<SLOTS>([&](auto sc) {
+            constexpr int slot = decltype(sc)::value;
+            const int left = left_of(s_lo + slot);
+            static_for<COPIES>([&](auto ic) { copy1(s_lo + slot, slot, left, ic); });
+        });
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (SLOTS - 1) * COPIES);  // the first stage's have landed
         asm volatile("s_barrier" ::: "memory");
     }
     i32x8 w[NT], b[2];
@@ -136,8 +142,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
 #pragma unroll
     for (int m = 0; m < MT; ++m) sa[m] = row_scale(s_lo, m);
     sw = col_scale(s_lo);
-    for (int st = s_lo; st < s_hi; ++st) {
-        const int slot = st & 1, left = left_of(st + 2);
+    int slot = 0;
+    for (int st = s_lo; st < s_hi; ++st, slot = slot + 1 == SLOTS ? 0 : slot + 1) {
+        const int left = left_of(st + SLOTS), next = slot + 1 == SLOTS ? 0 : slot + 1;
         constexpr int LAG = kFp8Lag, TILES = NT * MT;
         f32x4 p[LAG + 1];
         float sc[MT];
@@ -149,9 +156,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
                 constexpr int m = s / NT, i = s % NT;
                 if constexpr (m == MT - 1 && i == 0) {
                     // every operand of this stage is in registers and the next one's data have landed
-                    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+                    __builtin_amdgcn_s_waitcnt(0x0070 | (SLOTS - 2) * COPIES);  // vmcnt, lgkmcnt(0)
                     asm volatile("s_barrier" ::: "memory");
-                    copy_scales(st + 2);
+                    copy_scales(st + SLOTS);
                 }
                 if constexpr (i == 0) {
                     if constexpr (m + 1 < MT) b[(m + 1) & 1] = operand(slot, W_BYTES, wm * MT + m + 1);
@@ -160,15 +167,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
                 p[s % (LAG + 1)] = mfma_fp8(w[i], b[m & 1], (f32x4){0.f, 0.f, 0.f, 0.f});
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (m == MT - 1) {
-                    w[i] = operand(slot ^ 1, 0, wn * NT + i);
+                    w[i] = operand(next, 0, wn * NT + i);
                     if constexpr (i == 0) {
-                        b[0] = operand(slot ^ 1, W_BYTES, wm * MT);
+                        b[0] = operand(next, W_BYTES, wm * MT);
                     }
                     static_assert(MT <= NT, "a token scale beside each");
                     if constexpr (i < MT) sa[i] = row_scale(st + 1, i);
                     if constexpr (i == NT - 1) sw = col_scale(st + 1);
-                    if constexpr (i < COPIES) copy1(st + 2, left, std::integral_constant<int, i>{});
-                    if constexpr (i + NT < COPIES) copy1(st + 2, left, std::integral_constant<int, i + NT>{});
+                    if constexpr (i < COPIES) copy1(st + SLOTS, slot, left, std::integral_constant<int, i>{});
+                    if constexpr (i + NT < COPIES) copy1(st + SLOTS, slot, left, std::integral_constant<int, i + NT>{});
                 }
             }
             if constexpr (s >= LAG) {
@@ -196,59 +203,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     }
 }
 
-// The K splits' sums [S][M][N], added in split order, written and cleared; one thread a quad of outputs.  Rows before the
-// first expert's and behind the last's (offsets: the one and the other) are not written, but cleared like the others:
-// offsets that are no plan leave nothing behind either.
-template <int DT>
-__global__ __launch_bounds__(256) void fp8_block_split_sum(f32x4 *__restrict__ part, uint16_t *__restrict__ y,
-                                                           const int32_t *__restrict__ offsets, int E, int64_t quads,
-                                                           int N, int S) {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (q >= quads) return;
-    const int64_t row = q / (N / 4);
-    const bool live = !offsets || (row >= offsets[0] && row < offsets[E]);
-    f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
-    constexpr int kB = 4;
-    for (int s0 = 0; s0 < S; s0 += kB) {
-        f32x4 b[kB];
-#pragma unroll
-        for (int i = 0; i < kB; ++i) b[i] = s0 + i < S ? part[q + (s0 + i) * quads] : (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kB; ++i)
-            if (s0 + i < S) v += b[i];
-    }
-    if (live) *(uint2 *)(y + 4 * q) = quad_out_bits<DT>(v);
-    for (int s = 0; s < S; ++s) part[q + s * quads] = (f32x4){0.f, 0.f, 0.f, 0.f};
-}
-
-template <int NT, int MT, int WN, int WM>
+template <int NT, int MT, int WN, int WM, int SLOTS>
 static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles_n * p.tiles_m), (unsigned)p.splits), block(64 * WN * WM);
     f32x4 *const part = (f32x4 *)p.acc;
-    if (g.dtype == DT_BF16) hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, NT, MT, WN, WM>), grid, block, 0, st, g, part);
-    else hipLaunchKernelGGL((fp8_block_gemm<DT_F16, NT, MT, WN, WM>), grid, block, 0, st, g, part);
+    if (g.dtype == DT_BF16) hipLaunchKernelGGL((fp8_block_gemm<DT_BF16, NT, MT, WN, WM, SLOTS>), grid, block, 0, st, g, part);
+    else hipLaunchKernelGGL((fp8_block_gemm<DT_F16, NT, MT, WN, WM, SLOTS>), grid, block, 0, st, g, part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t quads = (int64_t)g.M * g.N / 4;
-    const dim3 sums((unsigned)((quads + 255) / 256));
-    const int32_t *const offsets = g.groups.offsets;
-    if (g.dtype == DT_BF16)
-        hipLaunchKernelGGL(fp8_block_split_sum<DT_BF16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, offsets,
-                           g.groups.E, quads, g.N, p.splits);
-    else
-        hipLaunchKernelGGL(fp8_block_split_sum<DT_F16>, sums, dim3(256), 0, st, part, (uint16_t *)g.y, offsets,
-                           g.groups.E, quads, g.N, p.splits);
-    return hipGetLastError();
+    return launch_split_sum(part, g.y, g.groups.offsets, g.groups.E, g.M, g.N, p.splits, g.dtype, st);
 }
 
-// Tiles of 128 x 128: 4 waves, two workgroups a CU; of 256 x 256: 8 waves, one.
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
     if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
-    switch (p.tile) {
-        case 128: return launch_t<4, 4, 2, 2>(g, p, st);
-        case 256: return launch_t<8, 4, 2, 4>(g, p, st);
-        default: return hipErrorInvalidValue;
-    }
+    if (p.rows == 128 && p.cols == 128) return launch_t<4, 4, 2, 2, 2>(g, p, st);
+    if (p.rows == 128 && p.cols == 256) return launch_t<4, 4, 4, 2, 3>(g, p, st);
+    if (p.rows == 256 && p.cols == 256) return launch_t<8, 4, 2, 4, 2>(g, p, st);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace awq4

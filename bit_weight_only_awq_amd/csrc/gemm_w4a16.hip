@@ -81,8 +81,8 @@ __host__ __device__ constexpr int gemm_col(int u) { return (u & 1) + ((u >> 1) <
 // groups trade partial sums through LDS at the end.  This doubles the waves
 // per SIMD for layers with no more tiles than CUs.
 // Grp: Groups, for rows grouped by expert (grid x: the column tiles of every
-// row tile that there may be; M: the rows of all experts; no K split over
-// workgroups), or NoGroups.
+// row tile that there may be, z: the K splits; M: the rows of all experts), or
+// NoGroups.
 template <int DT, bool SYM, int KS, int MT, int AB, int BB, int WN, class Grp>
 __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ? 3 : 2) void w4a16_gemm(const uint16_t *__restrict__ x,
                                                                 const uint32_t *__restrict__ qw,
@@ -438,10 +438,21 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
             }
         return;
     }
-    // (256-column tiles never split K, and neither do rows grouped by expert:
-    // the launchers refuse such a plan, and the split path below would only add to
-    // their register count)
-    if constexpr (WN == 8 || GROUPED) {
+    // (256-column tiles never split K: the launchers refuse such a plan, and the
+    // split path below would only add to their register count)
+    if constexpr (WN == 8) {
+        return;
+    } else if constexpr (GROUPED) {
+        // sums [S][R][N], added by the launch behind this one
+        if (!col_ok) return;
+        float *const sums = (float *)acc64 + (size_t)split * groups.R * N + n0;
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int m = m0 + 16 * (lo + i) + 4 * gq + r;
+                if (m < M) *(float2 *)(sums + (size_t)m * N) = make_float2(res[i][0][r], res[i][1][r]);
+            }
         return;
     } else {
     // K split.  The partials move as column quads, 16 bytes each, with the
@@ -629,11 +640,13 @@ hipError_t launch_w4a16_gemm(const W4A16Args &a, const W4A16Plan &p, hipStream_t
 // Rows grouped by expert: 128-row tiles, 128 columns (p.wn = 4), or 256-row ones, 256 columns (p.wn = 8).
 template <int DT, bool SYM, int KS, int MT, int WN>
 static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m)),
+    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), 1, p.splits),
                        dim3(64 * WN * KS), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
-                       (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, (uint64_t *)nullptr,
-                       (int)a.M, (int)a.N, (int)a.K, a.G, 1, 0, g);
-    return hipGetLastError();
+                       (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc,
+                       (int)a.M, (int)a.N, (int)a.K, a.G, p.splits, 0, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    return launch_split_sum(p.acc, a.y, g.offsets, g.E, a.M, a.N, p.splits, a.dtype, st);
 }
 
 template <int KS, int MT, int WN>
@@ -647,7 +660,7 @@ static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, cons
 }
 
 hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    if (p.splits != 1) return hipErrorInvalidValue;
+    if (p.splits > 1 && (p.wn == 8 || p.acc == nullptr)) return hipErrorInvalidValue;
     if (p.mt == 8) return launch_grouped_dt<1, 8, 4>(a, p, g, st);
     return p.wn == 8 ? launch_grouped_dt<1, 16, 8>(a, p, g, st) : hipErrorInvalidValue;
 }

@@ -128,6 +128,9 @@ hipError_t launch_w4a16_stream(const W4A16Args &a, const W4A16Plan &p, hipStream
 // rows grouped by expert (a.M = the rows of all, p.tiles_m = g.max_tiles): the LDS GEMM, and a streaming kernel
 // of their own
 hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
+// sums of S splits [S][M][N] (fp32) into y, and zeros behind; offsets [E + 1], or nullptr: every row
+hipError_t launch_split_sum(void *part, void *y, const int32_t *offsets, int E, int64_t M, int64_t N, int S, int dtype,
+                            hipStream_t st);
 constexpr int kGroupedWaves = 4, kGroupedCols = 256;  // of a workgroup
 hipError_t launch_w4a16_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st);
 // K-split reduction of the LDS GEMM and the streaming kernel in a launch of
@@ -225,7 +228,7 @@ struct Fp8BlockArgs {
     Groups groups;     // dense: offsets == nullptr, E = 1, R = M
 };
 struct Fp8BlockPlan {
-    int tile;     // rows and columns of the LDS-pipelined kernel's tile (128, 256), or 0: the streaming kernel
+    int rows, cols;  // of a tile: 128 x 128, 128 x 256 or 256 x 256 through LDS, or the streaming kernel's
     int tiles_n;  // column tiles
     int tiles_m;  // row tiles (grouped: at most)
     int splits;   // workgroups along K

@@ -88,6 +88,17 @@ def test_experts_sizes(G, K, N):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_experts_split_k_of_tiles(dtype):
+    """The same through LDS: more than 36 rows an expert, and few tiles."""
+    for split in ([50, 40, 60, 0], [129, 1, 0, 90], [64, 64]):
+        K, N = 4096, 288
+        assert awq.lib().awq_moe_gemm_w4a16_workspace_bytes(sum(split) + 7, len(split), N, K, 128) > 0
+        print(split, flush=True)
+        run_w4a16(split, K, N, 128, True, dtype, True, seed=len(split), spare=7)
+        run_w4a16(split, K, N, 64, False, dtype, False, seed=len(split), spare=7)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_experts_split_k(dtype):
     """Few tiles and a long K: the workgroups along K add up their shares, row tiles of several experts at once."""
     for split in ([1, 0, 2], [5, 3, 0, 1], [20, 19], [50, 3, 0, 0]):
@@ -162,6 +173,12 @@ def test_product_of_large_tiles(M, N, K):
     run_dense(M, N, K, "bf16", seed=K)
 
 
+@pytest.mark.parametrize("M,N,K", [(1601, 4104, 400), (1664, 4096, 128), (1537, 3848, 16), (1600, 4096, 144), (1590, 3896, 2112)])
+def test_product_of_wide_tiles(M, N, K):
+    """As many tiles of 128 x 256 as take them, in one round."""
+    run_dense(M, N, K, "f16", seed=K)
+
+
 def run_grouped(split, K, N, dtype, gather, top=2, seed=0, spare=0):
     E = len(split)
     offsets, slots, tokens = plan(split, top, seed, spare)
@@ -193,6 +210,13 @@ def test_grouped_product_of_large_tiles():
     run_grouped([900, 0, 1100, 769], 272, 4096, "bf16", False, seed=6, spare=3)
 
 
+def test_grouped_product_of_wide_tiles():
+    split = [0, 1, 130, 17, 64, 128, 129, 5, 33, 0, 90, 7, 200, 16, 15, 2]
+    for K in (272, 96):
+        run_grouped(split, K, 4096, "f16", True, seed=K, spare=11)
+        run_grouped(split, K, 3848, "bf16", False, seed=K)
+
+
 def test_grouped_product_split_k():
     for split in ([1, 0, 2], [20, 19], [50, 3, 0, 0]):
         assert awq.lib().awq_fp8_block_gemm_workspace_bytes(sum(split), len(split), 136, 8192) > 0
@@ -204,7 +228,7 @@ def test_grouped_product_rows_behind_the_last():
         run_grouped(SPLITS[split], 128, 64, "bf16", True, spare=37)
 
 
-@pytest.mark.parametrize("split,K,N", [([3, 1, 0, 5], 4096, 264), ([40, 33, 64, 31], 4096, 136), ([300, 150, 257, 90], 256, 160)])
+@pytest.mark.parametrize("split,K,N", [([3, 1, 0, 5], 4096, 264), ([40, 33, 64, 31], 4096, 136), ([60, 33, 64, 51], 4096, 160), ([300, 150, 257, 90], 256, 160)])
 def test_part_of_the_experts(split, K, N):
     """A plan's offsets from an expert on, with the matrices of some: rows of the others are left as they are."""
     q, s, z = experts_weights(len(split), K, N, 128, True, "f16", 0)

@@ -101,9 +101,10 @@ def test_experts_past_32_bits(tokens):
         awq.moe_gemm_w4a16(x, q, s, z, offsets, rows=torch.arange(tokens, dtype=torch.int32, device=dev()))
 
 
-def test_offsets_that_are_no_plan_leave_the_workspace_zero():
+@pytest.mark.parametrize("N,R", [(264, 40), (288, 400)])  # the streaming kernels, and tiles through LDS
+def test_offsets_that_are_no_plan_leave_the_workspace_zero(N, R):
     from bit_weight_only_awq_amd import ops
-    K, N, E, R = 4096, 264, 4, 40
+    K, E = 4096, 4
     q, s, z = cuda(*experts_weights(E, K, N, 128, True, "f16", 0))
     w, sw = cuda(*e4m3_weights(E, N, K, 0))
     x = torch.randn(R, K, device=dev(), dtype=torch.float16)
