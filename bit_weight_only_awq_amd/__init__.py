@@ -1,4 +1,5 @@
-"""MI355X (gfx950) 4-bit-weight GEMM library: AWQ W4A16 GEMV/GEMM and QQQ-style W4A8.
+"""MI355X (gfx950) 4-bit-weight GEMM library: AWQ W4A16 GEMV/GEMM and QQQ-style W4A8,
+what stands around them in a decoder layer, mixtures of experts, and block-scaled E4M3 products.
 
 The compute lives in libawq4.so (hand-written HIP, C ABI in include/awq4.h);
 this package is its thin torch binding.  Importing the package does not need

@@ -767,7 +767,7 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
         return E ? expected_tiles(live, avg, N, rows, cols) : (double)(cdiv(N, cols) * cdiv(M, rows));
     };
     // Up to 16 rows (of an expert: 4, whose tiles are many without a K split), the
-    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128 x 128, 14336 -> 4096 with 17
+    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128 x 128, 4096 -> 14336 with 17
     // 22.2 against 18.5 (16 rows 21.2 against 19.6); 64 experts with 2.2 rows each 40 against 46, 4 rows 51
     // against 48.5, 8 rows 64 against 52.
     // Rows x columns of the others: 128 x 128 where 128 x 256 would leave a fifth of the CUs or more without work,

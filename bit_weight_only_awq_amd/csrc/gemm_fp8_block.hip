@@ -26,7 +26,9 @@
 // takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2400 are reached
 // where the tiles are as many as the CUs (4096 x 4096 x 14336), the rest goes to
 // the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).  4096 x 14336 x 4096 is 896 tiles,
-// 3.5 for each CU where the last half is waited for in full.  (One workgroup a CU going through its tiles without a
+// 3.5 for each CU where the last half is waited for in full.  (Three rounds of it, and the other columns by the smaller
+// tiles in a launch behind: 257 -> 245 us in a graph, but 264 as before where calls follow each other on a stream and
+// the clock falls.  One workgroup a CU going through its tiles without a
 // pause, the next one's copies under way before the last one's stores: 295 -> 285 us by tiles of 256 x 128, but 257 ->
 // 269 by the large ones, whose registers it overflows.)
 // With few rows the copies bound: 777 tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB of weights)

