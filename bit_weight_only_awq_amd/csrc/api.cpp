@@ -712,29 +712,34 @@ static double expected_tiles(double live, double avg, int64_t N, int64_t rows, i
 }
 // The kernel by the rows an expert has on average, over the experts that R rows reach; us by rows an
 // expert, two of eight experts a token:
-//   14336 -> 4096        8    12    16    32    40    48    56   100   150   200   300
-//     stream, 16 rows   60    85    95   164         166
-//     stream, 32        79    82    84   133   134   135   199   242   359
-//     LDS, 128 x 128                     142   147   149   150   207   277   319   444
-//     LDS, 256 x 256                                             357   359   359   378
-//   4096 -> 28672: stream, 32 at 32, 40 and 48 rows 218, 253, 267; LDS, 128 x 128 233, 237, 238
-// The large tiles where a round of theirs (2.7 of the small ones a CU) takes less than all of the small ones.
-// Small tiles split K up to three workgroups a CU, 16 stages each at least: 14336 -> 4096 at 56 rows 198 -> 157 us
-// by 2 splits, at 100 rows 267 -> 207; 4096 -> 4096 at 75 62 -> 58.
+//   14336 -> 4096        8    12    16    24    32    48    60    75   100   150   200   300
+//     stream, 16 rows   60    82    95         164   166
+//     stream, 32        79    81    84   114   133   134   199   238   242   359
+//     LDS, 64 x 128                 110   113   119   135   152   192
+//     LDS, 128 x 128                           142   148   150   180   203   277   319   444
+//     LDS, 256 x 256                                       357         357   359   359   378
+//   4096 -> 28672, 16, 32 and 48 rows: stream, 32 159, 219, 267; LDS, 64 x 128 162, 174, 195, 128 x 128 -, 233, 232
+//   2048 -> 2048, 64 experts, 16 and 32 rows: stream, 32 68, 84; LDS, 64 x 128 52, 61, 128 x 128 -, 81
+// Tiles of 64 rows where they are less than 1.5 times those of 128; of 256 x 256 where a round of theirs (2.7 of
+// those of 128 a CU) takes less than all of the smaller ones.
+// The smaller tiles split K up to three (of 64 rows five) workgroups a CU, 16 stages each at least: 14336 -> 4096 at 32 rows
+// 185 us by one, 133, 128, 119 by 2, 3, 4 splits; at 100 rows 267 by one, 207 by 2.
 // Streaming workgroups split K while two a CU are not there (us for 1, 2, 3, 4 splits: 128 tiles 88,
 // 83, 64, 60; 210 tiles 32.3, 32.3, 34.4, 35.6) and every wave keeps two chunks.
 static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
     W4A16Plan p{};
     const double live = live_experts(R, E), avg = (double)R / live;
-    if (avg > 36 && K % 64 == 0 && N % 32 == 0) {
+    if (avg > 24 && K % 64 == 0 && N % 32 == 0) {
         p.kind = 3;
-        const double small = expected_tiles(live, avg, N, 128, 128);
-        const bool wide = 2.7 * d.cus * std::ceil(expected_tiles(live, avg, N, 256, 256) / d.cus) < small;
-        p.mt = wide ? 16 : 8;
-        p.wn = wide ? 8 : 4;
+        double tiles = expected_tiles(live, avg, N, 128, 128);
+        const double half = expected_tiles(live, avg, N, 64, 128);
+        p.mt = 2.7 * d.cus * std::ceil(expected_tiles(live, avg, N, 256, 256) / d.cus) < tiles ? 16 : half < 1.5 * tiles ? 4 : 8;
+        if (p.mt == 4) tiles = half;
+        p.wn = p.mt == 16 ? 8 : 4;
         p.tiles_n = (int)cdiv(N, 32 * p.wn);
         p.tiles_m = (int)group_tiles(R, E, 16 * p.mt);
-        p.splits = wide ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(3 * d.cus / small), K / 64 / 16, 8}));
+        const int fill = p.mt == 4 ? 5 : p.mt == 8 ? 3 : 0;
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(fill * d.cus / tiles), K / 64 / 16, 8}));
         if (p.splits > 1) p.workspace_bytes = (size_t)p.splits * R * N * 4;
         return p;
     }

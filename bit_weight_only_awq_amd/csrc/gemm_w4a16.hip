@@ -38,7 +38,7 @@ namespace awq4 {
 
 constexpr int GB_K = 64;
 constexpr int GA_PITCH = GB_K * 2;  // 128 bytes per X row (8 segments of 16 B, swizzled)
-constexpr int kPrefA = 6;           // X operand reads run this many row tiles ahead of the MFMAs
+constexpr int kPrefA = 6;           // X operand reads run this many row tiles ahead of the MFMAs (of fewer: all)
 
 // LDS ring of one group of WN waves (side by side along N, 32 columns each):
 // AB X buffers of 16*MT rows, BB buffers of packed words with the stage's
@@ -84,7 +84,7 @@ __host__ __device__ constexpr int gemm_col(int u) { return (u & 1) + ((u >> 1) <
 // row tile that there may be, z: the K splits; M: the rows of all experts), or
 // NoGroups.
 template <int DT, bool SYM, int KS, int MT, int AB, int BB, int WN, class Grp>
-__global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ? 3 : 2) void w4a16_gemm(const uint16_t *__restrict__ x,
+__global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT <= 8 ? 3 : 2) void w4a16_gemm(const uint16_t *__restrict__ x,
                                                                 const uint32_t *__restrict__ qw,
                                                                 const uint16_t *__restrict__ sc,
                                                                 const uint32_t *__restrict__ qz,
@@ -94,7 +94,8 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
     constexpr bool GROUPED = !std::is_same_v<Grp, NoGroups>;
     using R = GRing<MT, AB, BB, WN>;
     static_assert(KS == 1 || (WN == 4 && KS * R::LDS >= 2 * 4 * MT * 64 * 16), "the K-split handover fits in the rings");
-    static_assert(AB >= 2 && BB >= 3 && MT > kPrefA, "ring depths and prefetch distance");
+    constexpr int PREF = MT > kPrefA ? kPrefA : MT - 1;
+    static_assert(AB >= 2 && BB >= 3, "ring depths");
     constexpr int GB_M = R::M_TILE, GA_BYTES = R::A_BYTES, G_LDS = R::LDS;
     constexpr int GB_N = R::N_TILE, GB_PITCH = R::B_PITCH, GB_WORDS = R::B_WORDS, GM_SCALES = R::M_SCALES;
     constexpr int GB_BYTES = R::B_BYTES, WC = R::WC;
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
         const unsigned char *A = Abase + (rel % AB) * GA_BYTES;
         u32x4 a[MT];
 #pragma unroll
-        for (int mt = 0; mt < kPrefA; ++mt) a[mt] = load_a(A, 0, mt);
+        for (int mt = 0; mt < PREF; ++mt) a[mt] = load_a(A, 0, mt);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             // the next k-step: (st, 1) or (st + 1, 0).  After the last stage
@@ -361,9 +362,9 @@ __global__ __launch_bounds__(64 * WN * KS, WN == 8 ? 1 : KS == 2 ? 1 : MT == 8 ?
             for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) acc[mt][u] = mma<DT>(a[mt], bc[u], acc[mt][u]);
-                // X operands kPrefA row tiles ahead (within this stage only)
-                if (mt + kPrefA < MT) a[mt + kPrefA] = load_a(A, ks, mt + kPrefA);
-                else if (ks == 0) a[mt + kPrefA - MT] = load_a(A, 1, mt + kPrefA - MT);
+                // X operands PREF row tiles ahead (within this stage only)
+                if (mt + PREF < MT) a[mt + PREF] = load_a(A, ks, mt + PREF);
+                else if (ks == 0) a[mt + PREF - MT] = load_a(A, 1, mt + PREF - MT);
                 if (mt == 1) pair_words(w, px, py);
                 if (mt == 1 + MT / 4) bn[0] = dequant(px, 0);
                 if (mt == 1 + MT / 2) bn[1] = dequant(py, 1);
@@ -637,7 +638,7 @@ hipError_t launch_w4a16_gemm(const W4A16Args &a, const W4A16Plan &p, hipStream_t
     return p.ksplit == 2 ? launch_gemm_ks<2, 16, 2, 3, 4>(a, p, st) : launch_gemm_ks<1, 16, 2, 3, 4>(a, p, st);
 }
 
-// Rows grouped by expert: 128-row tiles, 128 columns (p.wn = 4), or 256-row ones, 256 columns (p.wn = 8).
+// Rows grouped by expert: 64-row or 128-row tiles, 128 columns (p.wn = 4), or 256-row ones, 256 columns (p.wn = 8).
 template <int DT, bool SYM, int KS, int MT, int WN>
 static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
     hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), 1, p.splits),
@@ -661,6 +662,7 @@ static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, cons
 
 hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
     if (p.splits > 1 && (p.wn == 8 || p.acc == nullptr)) return hipErrorInvalidValue;
+    if (p.mt == 4) return launch_grouped_dt<1, 4, 4>(a, p, g, st);
     if (p.mt == 8) return launch_grouped_dt<1, 8, 4>(a, p, g, st);
     return p.wn == 8 ? launch_grouped_dt<1, 16, 8>(a, p, g, st) : hipErrorInvalidValue;
 }

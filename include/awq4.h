@@ -606,7 +606,7 @@ size_t awq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  *   rows, x is under 2^31 bytes, and an expert's words are in any case (else
  *   AWQ_EUNSUPPORTED).  One kernel takes the whole call, chosen by R over the
  *   experts that R rows reach on average, as if all had alike.
- * Numerics: up to 36 such rows an expert, and where K % 64 or N % 32 is not 0,
+ * Numerics: up to 24 such rows an expert, and where K % 64 or N % 32 is not 0,
  *   y = act( sum over runs of min(G, 64) k of s ( sum x q' - z' sum x ) )
  * with q' = q and z' = z (fp16), or both 128 more (bf16): exact operands of the fp32
  * matrix cores, weights that are not rounded, runs added by fp32 FMAs.  (So an

@@ -87,10 +87,17 @@ def test_experts_sizes(G, K, N):
         run_w4a16(SPLITS[split], K, N, G, True, "f16", True, top=3, seed=K + N)
 
 
+@pytest.mark.parametrize("dtype,zeros,gather,K,G", [("f16", True, True, 192, 64), ("bf16", False, False, 128, 128),
+                                                    ("bf16", True, True, 64, 32), ("f16", False, False, 128, 32)])
+def test_experts_of_large_tiles(dtype, zeros, gather, K, G):
+    """As many tiles of 256 x 256 as take them."""
+    run_w4a16([700, 501, 0, 650, 599], K, 4352, G, zeros, dtype, gather, seed=K, spare=5)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_experts_split_k_of_tiles(dtype):
-    """The same through LDS: more than 36 rows an expert, and few tiles."""
-    for split in ([50, 40, 60, 0], [129, 1, 0, 90], [64, 64]):
+    """The same through LDS: more than 24 rows an expert, and few tiles (of 64 rows, and of 128)."""
+    for split in ([50, 40, 60, 0], [129, 1, 0, 90], [64, 64], [130, 90, 100], [30, 25]):
         K, N = 4096, 288
         assert awq.lib().awq_moe_gemm_w4a16_workspace_bytes(sum(split) + 7, len(split), N, K, 128) > 0
         print(split, flush=True)
