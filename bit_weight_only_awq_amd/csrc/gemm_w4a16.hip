@@ -639,10 +639,10 @@ hipError_t launch_w4a16_gemm(const W4A16Args &a, const W4A16Plan &p, hipStream_t
 }
 
 // Rows grouped by expert: 64-row or 128-row tiles, 128 columns (p.wn = 4), or 256-row ones, 256 columns (p.wn = 8).
-template <int DT, bool SYM, int KS, int MT, int WN>
+template <int DT, bool SYM, int MT, int WN>
 static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
-    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, KS, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), 1, p.splits),
-                       dim3(64 * WN * KS), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
+    hipLaunchKernelGGL((w4a16_gemm<DT, SYM, 1, MT, 2, 3, WN, Groups>), dim3((unsigned)(p.tiles_n * p.tiles_m), 1, p.splits),
+                       dim3(64 * WN), 0, st, (const uint16_t *)a.x, (const uint32_t *)a.qweight,
                        (const uint16_t *)a.scales, (const uint32_t *)a.qzeros, (uint16_t *)a.y, p.acc,
                        (int)a.M, (int)a.N, (int)a.K, a.G, p.splits, 0, g);
     const hipError_t e = hipGetLastError();
@@ -650,21 +650,21 @@ static hipError_t launch_grouped_t(const W4A16Args &a, const W4A16Plan &p, const
     return launch_split_sum(p.acc, a.y, g.offsets, g.E, a.M, a.N, p.splits, a.dtype, st);
 }
 
-template <int KS, int MT, int WN>
+template <int MT, int WN>
 static hipError_t launch_grouped_dt(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
     const bool sym = a.qzeros == nullptr;
     if (a.dtype == DT_F16)
-        return sym ? launch_grouped_t<DT_F16, true, KS, MT, WN>(a, p, g, st)
-                   : launch_grouped_t<DT_F16, false, KS, MT, WN>(a, p, g, st);
-    return sym ? launch_grouped_t<DT_BF16, true, KS, MT, WN>(a, p, g, st)
-               : launch_grouped_t<DT_BF16, false, KS, MT, WN>(a, p, g, st);
+        return sym ? launch_grouped_t<DT_F16, true, MT, WN>(a, p, g, st)
+                   : launch_grouped_t<DT_F16, false, MT, WN>(a, p, g, st);
+    return sym ? launch_grouped_t<DT_BF16, true, MT, WN>(a, p, g, st)
+               : launch_grouped_t<DT_BF16, false, MT, WN>(a, p, g, st);
 }
 
 hipError_t launch_w4a16_gemm_grouped(const W4A16Args &a, const W4A16Plan &p, const Groups &g, hipStream_t st) {
     if (p.splits > 1 && (p.wn == 8 || p.acc == nullptr)) return hipErrorInvalidValue;
-    if (p.mt == 4) return launch_grouped_dt<1, 4, 4>(a, p, g, st);
-    if (p.mt == 8) return launch_grouped_dt<1, 8, 4>(a, p, g, st);
-    return p.wn == 8 ? launch_grouped_dt<1, 16, 8>(a, p, g, st) : hipErrorInvalidValue;
+    if (p.mt == 4) return launch_grouped_dt<4, 4>(a, p, g, st);
+    if (p.mt == 8) return launch_grouped_dt<8, 4>(a, p, g, st);
+    return p.wn == 8 ? launch_grouped_dt<16, 8>(a, p, g, st) : hipErrorInvalidValue;
 }
 
 }  // namespace awq4

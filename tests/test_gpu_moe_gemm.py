@@ -276,6 +276,24 @@ def test_no_rows_at_all():
     assert awq.gemm_fp8_block(a[:0], w[0], sa[:0], sw[0]).shape == (0, 64)
 
 
+@pytest.mark.parametrize("T", [5, 60, 200, 500])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_infinities_stay_in_their_rows(T, dtype):
+    """A row of x with an infinity or a NaN gives no number where a weight meets it, and changes no other row."""
+    K, N, E = 256, 288, 2
+    q, s, z = cuda(*experts_weights(E, K, N, 128, True, dtype, 0))
+    x = randn(T, T, K).to(DT[dtype]).to(dev())
+    off = torch.tensor([0, T // 2, T], dtype=torch.int32, device=dev())
+    clean = awq.moe_gemm_w4a16(x, q, s, z, off)
+    bad = torch.tensor([0, T // 2 - 1, T - 1], device=dev())
+    x[bad, torch.tensor([3, 130, 255], device=dev())] = torch.tensor([torch.inf, torch.nan, -torch.inf], dtype=DT[dtype], device=dev())
+    got = awq.moe_gemm_w4a16(x, q, s, z, off)
+    rest = torch.ones(T, dtype=torch.bool, device=dev())
+    rest[bad] = False
+    assert torch.equal(got[rest], clean[rest])
+    assert not torch.isfinite(got[bad]).any()
+
+
 def test_offsets_that_are_no_plan():
     """Falling, negative, past the rows: whatever is computed, nothing outside the tensors is touched, and every row
     that is written is some row's product."""
