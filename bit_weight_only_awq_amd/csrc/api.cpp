@@ -771,33 +771,34 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     auto workgroups = [&](int64_t rows, int64_t cols) {
         return E ? expected_tiles(live, avg, N, rows, cols) : (double)(cdiv(N, cols) * cdiv(M, rows));
     };
-    // Up to 16 rows (of an expert: 4, whose tiles are many without a K split), the
-    // streaming kernel: 4096 -> 4096 with 8 rows 9.5 us against 12.5 by tiles of 128 x 128, 4096 -> 14336 with 17
-    // 22.2 against 18.5 (16 rows 21.2 against 19.6); 64 experts with 2.2 rows each 40 against 46, 4 rows 51
-    // against 48.5, 8 rows 64 against 52.
-    // Rows x columns of the others: 128 x 128 where 128 x 256 would leave a fifth of the CUs or more without work,
-    // 256 x 256 where its rounds over the CUs, each of which takes 1.5 of the second's, are fewer by more than
+    auto splits = [&](double tiles, double fill) {  // of 8 blocks at least
+        return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)(fill * d.cus / tiles), blocks / 8, 8}));
+    };
+    // The streaming kernel for up to four rows, of a matrix or an expert (64 experts, 2.2 rows each 39.6 us against 43.8 by
+    // the tiles below, 4 rows 50.4 against 46.4; one row, 4096 -> 14336, 15.3 against 15.7), and up to 16 of a matrix too small to give the CUs a 128 x 128 tile
+    // or a part of one (8 rows, 4096 -> 4096 9.5 against 12.0; 4096 -> 14336 19.9 against 18.2, 14336 -> 4096 20.8
+    // against 18.7).
+    // Rows x columns of the others, one a CU at a time: 128 x 128 where one round takes them, with K split to fill it;
+    // 256 x 256 where its rounds, each of which takes 1.5 of those of 128 x 256, are fewer by more than
     // that; by experts, whose last row tiles are part empty, over 2.5 tiles of 128.  us for 128 x 128, 128 x 256,
     // 256 x 256:
-    //   4096 -> 14336, rows    96: 26, 28        256: 31, 38        500: 42, 41, 57     768: 66, 73, 58
-    //                        1024: 83, 80, 63   1100: 84, 81, 109  4096: 326, 295, 257
-    //   64 experts 2048 -> 2048, rows each 32: 53, 50      97: 89, 80, 105   187: 118, 104, 120
-    //                        250: 146, 131, 135   300: 167, 152, 158   375: 195, 180, 164
-    const bool stream = avg <= (E ? 4 : 16);
+    //   4096 -> 14336, rows    96: 23, 28         200: 26, 38        384: 48, 38       500: -, 41, 57
+    //                         768: -, 73, 58     1024: -, 80, 63    1100: -, 81, 109  4096: -, 295, 257
+    //   64 experts 2048 -> 2048, rows each 32: 63, 50      97: 96, 80, 105   187: 126, 104, 120
+    //                        250: -, 131, 135     300: -, 152, 158     375: -, 180, 164
+    // (us for 1, 2, 3, 4 splits: 112 tiles 24.7, 23.8, 31.8, 34.2; 32 tiles 65, 38, 30, 25.)
+    const double small = workgroups(128, 128);
+    const bool stream = avg <= 4 || (!E && M <= 16 && small * splits(small, 1) < 0.8 * d.cus);
     p.rows = p.cols = 128;
     if (stream) p.rows = kFp8StreamRows, p.cols = kFp8StreamCols;
-    else if (workgroups(128, 256) >= 0.8 * d.cus) {
+    else if (small > d.cus) {
         p.cols = 256;
         const double large = workgroups(256, 256) / d.cus;
         if (E ? avg > 320 && large >= 0.8 : 1.5 * std::ceil(large) < std::ceil(workgroups(128, 256) / d.cus)) p.rows = 256;
     }
     p.tiles_n = (int)cdiv(N, p.cols);
     p.tiles_m = (int)row_tiles(p.rows);
-    // K splits, of 8 blocks at least: workgroups of tiles of 128 up to 1.5 a CU (us for 1, 2, 4, 8 splits: 32
-    // tiles 82, 48, 30, 26; 64 tiles 85, 52, 36, 38; 112 tiles 29, 25, 27, 40; 224 tiles 31, 39), streaming ones 2.
-    const double fill = stream ? 2 : p.cols == 128 ? 1.5 : 0;
-    p.splits = (int)std::max<int64_t>(
-        1, std::min<int64_t>({(int64_t)(fill * d.cus / workgroups(p.rows, p.cols)), blocks / 8, 8}));
+    p.splits = p.cols == 256 ? 1 : splits(workgroups(p.rows, p.cols), stream ? 2 : 1);
     if (p.splits > 1)
         p.workspace_bytes = !stream ? (size_t)p.splits * M * N * 4
                                     : (size_t)split_tiles_bytes((int64_t)p.tiles_n * p.tiles_m, p.splits, M, N);

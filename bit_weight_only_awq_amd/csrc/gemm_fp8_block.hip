@@ -2,17 +2,19 @@
 // has the arithmetic): tiles through LDS.
 //
 // A workgroup has a tile of BN outputs n by BM tokens, a wave NT x MT tiles of 16 x 16 of them: 256 x 256 by
-// 8 waves, where experts or the matrix have fewer rows 256 x 128 by 8 waves, one workgroup a CU either way; or 128 x
-// 128 by 4 waves, two a CU, and K split over workgroups where even these are few (an fp32 sum for each split,
-// added in split order by a launch of its own, split_sum.hip).  A stage is one block of 128 k: 128 bytes of each row of
+// 8 waves, where experts or the matrix have fewer rows 256 x 128 and then 128 x 128 by 8 waves as well, one workgroup a
+// CU; and K split over workgroups where even these are few (an fp32 sum for each split,
+// added in split order by a launch of its own, split_sum.hip).  The smaller a tile, the more slots: what is in flight sets
+// the rate where memory does (96 rows, 4096 -> 14336, tiles of 128 x 128: 23.4 us with four slots, 25.7 by four waves with
+// two slots and two workgroups a CU, 26.8 by these with three).  A stage is one block of 128 k: 128 bytes of each row of
 // both matrices, copied straight into one of SLOTS LDS slots.
 //
 // One barrier a stage, and no wave waits for LDS behind it: a wave holds all NT weight
 // operands of the stage and goes through its tokens 16 at a time, the
 // operand of the next 16 being read meanwhile.  When the last 16 are in
 // registers, nothing of the stage is left to read: the barrier stands there.
-// Behind it the slot takes the copies of the stage SLOTS further (in flight for a whole stage, or two with
-// three slots), and each weight operand is replaced by the next stage's as soon as its last
+// Behind it the slot takes the copies of the stage SLOTS further (in flight for a whole stage, or two or
+// three with more slots), and each weight operand is replaced by the next stage's as soon as its last
 // matrix-core instruction is issued.  (With the barrier at the stage's end, where the first
 // operands of all waves are read at once while the matrix cores wait: 1566
 // TFLOP/s at 4096 x 14336 x 4096 against 1850.  Two groups of waves taking turns at the
@@ -33,7 +35,7 @@
 // 269 by the large ones, whose registers it overflows.)
 // With few rows the copies bound: 777 tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB of weights)
 // take 80 us, the same copies without a product 75 or so, the weights' alone 53; tiles of 128 x 128, which read the
-// tokens twice as often, 89; 256 x 128 with two slots 93 where three are 80.  Neither another order of the blocks
+// tokens twice as often, 96; 256 x 128 with two slots 93 where three are 80.  Neither another order of the blocks
 // in each tile nor non-temporal copies and stores change that.
 #include "fp8_block.hpp"
 
@@ -218,7 +220,7 @@ static hipError_t launch_t(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStre
 
 hipError_t launch_fp8_block_gemm(const Fp8BlockArgs &g, const Fp8BlockPlan &p, hipStream_t st) {
     if (p.splits > 1 && p.acc == nullptr) return hipErrorInvalidValue;
-    if (p.rows == 128 && p.cols == 128) return launch_t<4, 4, 2, 2, 2>(g, p, st);
+    if (p.rows == 128 && p.cols == 128) return launch_t<4, 2, 2, 4, 4>(g, p, st);
     if (p.rows == 128 && p.cols == 256) return launch_t<4, 4, 4, 2, 3>(g, p, st);
     if (p.rows == 256 && p.cols == 256) return launch_t<8, 4, 2, 4, 2>(g, p, st);
     return hipErrorInvalidValue;

@@ -7,8 +7,9 @@
 // the end, then over the K splits in split order (split_exchange.hpp).  Bound by
 // memory: one token through 4096 x 14336 takes 18 us, of which 13 are what the
 // same loads take alone and 4 what the smallest call does (64 outputs a workgroup
-// 18.7, 16 of them 18.2, 8 waves 18.2).  From 17 tokens on the tiles of 128 through
-// LDS, split along K, take as long or less (17 tokens 18.5, here 22).
+// 18.7, 16 of them 18.2, 8 waves 18.2); 8 through 4096 x 4096 9.5.  Where tiles of 128 x 128 through LDS give
+// every CU work, those are level at one row and faster from about four
+// on (api.cpp: plan_fp8_block).
 #include "fp8_block.hpp"
 #include "split_exchange.hpp"
 
