@@ -20,7 +20,9 @@
 // both exact.  Scale and zero point are applied to a chunk's fp32 sums, s (sum x q - z
 // sum x), with sum x from one more matrix-core instruction against ones.  That is
 // one bitwise operation a pair, against two (fp16) and six (bf16) for the exact q - z:
-// what a stream at the memory's rate leaves time for.
+// what a stream at the memory's rate leaves time for.  Where an infinity in x meets q = 0, or both sums pass
+// binary32 on the way to a difference that does not, a wave's sums come out infinite or NaN: it then makes them again from the
+// exact q - z, whose sums are those of the definition.
 #include "moe.hpp"
 #include "split_exchange.hpp"
 #include "w4a16_ops.hpp"
@@ -78,6 +80,36 @@ __device__ __forceinline__ void grouped_column(const GroupedBuf<MT, CS> &b, int 
                 acc[m][T][r] = __builtin_fmaf(t[m][r], at, __builtin_fmaf(bt, rs[m][r], acc[m][T][r]));
         // four columns at a time: bounds how many temporaries are live at once
         if (T % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    });
+}
+
+// The same by the exact q - z.
+template <int MT, int CS, int DT, bool SYM>
+__device__ __forceinline__ void grouped_column_exact(const GroupedBuf<MT, CS> &b, int col, f32x4 (&acc)[MT][8]) {
+    ZeroConsts<DT> zc;
+    zero_consts<DT, SYM>(zc, SYM ? 0u : b.zw[col]);
+    static_for<8>([&](auto tc) {
+        constexpr int T = decltype(tc)::value;
+        f32x4 t[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) t[m] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < CS; ++s) {
+            u32x4 bop;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t w0 = b.w[s][2 * p][col], w1 = b.w[s][2 * p + 1][col];
+                bop[p] = qz_pair<DT, T>(col_src_y(T) ? pair_y(w0, w1) : pair_x(w0, w1), zc);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) t[m] = mma<DT>(b.a[m][s], bop, t[m]);
+        }
+        const float st = scale_f32<DT>(b.s4[col], T);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[m][T][r] = __builtin_fmaf(t[m][r], st, acc[m][T][r]);
+        __builtin_amdgcn_sched_barrier(0);
     });
 }
 
@@ -143,12 +175,15 @@ __global__ __launch_bounds__(64 * kGroupedWaves, 2) void w4a16_grouped(
         __builtin_amdgcn_sched_barrier(0);
     };
     f32x4 acc[2][MT][8];
+    auto clear = [&] {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) acc[c][m][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+                for (int u = 0; u < 8; ++u) acc[c][m][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
     auto run = [&](auto nr) {
         auto compute = [&](const GroupedBuf<MT, CS> &b) {
             constexpr uint32_t one = DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u;
@@ -176,6 +211,24 @@ __global__ __launch_bounds__(64 * kGroupedWaves, 2) void w4a16_grouped(
         if (i + 2 < n) issue(b0, i + 2);
         if (i + 1 < n) compute(b1);
         if (i + 2 < n) compute(b0);
+        // 0 while every sum is finite (an infinity or a NaN stays in its sum)
+        f32x4 odd = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                    for (int r = 0; r < decltype(nr)::value; ++r) odd[u & 3] = __builtin_fmaf(acc[c][m][u][r], 0.0f, odd[u & 3]);
+        if (__ballot((odd[0] + odd[1]) + (odd[2] + odd[3]) != 0.0f) == 0) return;
+        clear();
+#pragma unroll 1
+        for (i = 0; i < n; ++i) {
+            issue(b0, i);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) grouped_column_exact<MT, CS, DT, SYM>(b0, c, acc[c]);
+        }
     };
     if (MT == 1 && rows == 1) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 4>{});

@@ -609,9 +609,10 @@ size_t awq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  * Numerics: up to 24 such rows an expert, and where K % 64 or N % 32 is not 0,
  *   y = act( sum over runs of min(G, 64) k of s ( sum x q' - z' sum x ) )
  * with q' = q and z' = z (fp16), or both 128 more (bf16): exact operands of the fp32
- * matrix cores, weights that are not rounded, runs added by fp32 FMAs.  (So an
- * infinity in a row of x makes the row of y NaN, and in bf16 |x| is to stay under
- * 2^113.)  Else as awq_gemm_w4a16 for M > 64: weights rounded once to the activation type.
+ * matrix cores, weights that are not rounded, runs added by fp32 FMAs.  Where these
+ * are not finite, the sums are made again from the exact q - z, so that an
+ * infinity in x gives what it gives in the definition (bf16: |x| under 2^118).
+ * Else as awq_gemm_w4a16 for M > 64: weights rounded once to the activation type.
  * Workspace: as for the GEMMs (shared, zero before and after each call).  R == 0
  * is a no-op that returns AWQ_OK.
  * Errors: AWQ_EINVAL, AWQ_EUNSUPPORTED, AWQ_EALIGN, AWQ_EWORKSPACE, AWQ_EHIP.
