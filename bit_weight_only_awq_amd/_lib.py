@@ -28,6 +28,8 @@ AWQ_OP_GEMM_W4A16 = 0
 AWQ_OP_GEMV_W4A16 = 1
 AWQ_OP_W4A8_GEMM = 2
 AWQ_OP_W4A8_FP8_GEMM = 3
+AWQ_OP_MOE_GEMM_W4A16 = 4
+AWQ_OP_FP8_BLOCK_GEMM = 5
 AWQ_STATIC_SCRATCH_BYTES = 16 << 20
 
 _lib = None
@@ -96,13 +98,14 @@ def lib() -> ctypes.CDLL:
     L.awq_fp8_block_quant_act.argtypes = [vp, vp, vp, i64, i64, i32, vp]
     L.awq_fp8_block_gemm.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, sz, vp]
     L.awq_moe_fp8_block_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, vp, sz, vp]
+    L.awq_grouped_plan_info.argtypes = [i32, i64, i64, i64, i64, i32, i32, ctypes.POINTER(PlanInfo)]
     L.awq_moe_route_workspace_bytes.argtypes = [i64, i64, i64]
     L.awq_moe_gemm_w4a16_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
     L.awq_fp8_block_gemm_workspace_bytes.argtypes = [i64, i64, i64, i64]
     for f in ("awq_moe_route", "awq_moe_gemm_w4a16", "awq_fp8_block_gemm"):
         getattr(L, f + "_workspace_bytes").restype = sz
     for f in ("awq_moe_route", "awq_moe_combine", "awq_moe_gemm_w4a16", "awq_fp8_block_quant_act", "awq_fp8_block_gemm",
-              "awq_moe_fp8_block_gemm"):
+              "awq_moe_fp8_block_gemm", "awq_grouped_plan_info"):
         getattr(L, f).restype = i32
     for f in ("w4a8_rmsnorm_quant", "w4a8_fp8_rmsnorm_quant", "awq_kv4_append", "awq_kv4_attention"):
         getattr(L, f).restype = i32

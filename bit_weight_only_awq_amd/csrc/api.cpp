@@ -1249,6 +1249,29 @@ int awq_moe_combine(const void *y, const float *weights, const int32_t *places, 
     return hip_status(launch_combine(g, static_cast<hipStream_t>(stream)));
 }
 
+int awq_grouped_plan_info(int op, int64_t R, int64_t E, int64_t N, int64_t K, int group_size, int cu_count,
+                          awq_plan_t *out) {
+    if (!out || cu_count < 0 || R < 1) return AWQ_EINVAL;
+    const DeviceProps d = cu_count > 0 ? DeviceProps{cu_count} : stream_props(nullptr);
+    if (op == AWQ_OP_MOE_GEMM_W4A16) {
+        const int rc = check_moe_w4a16_shape(R, E, N, K, group_size);
+        if (rc != AWQ_OK) return rc;
+        const W4A16Plan p = plan_moe_w4a16(R, E, N, K, group_size, d);
+        *out = awq_plan_t{p.kind, p.tiles_n, p.tiles_m, p.splits, p.mt, 1, d.cus, (int64_t)p.workspace_bytes,
+                          p.kind == 3 ? 32 * p.wn : kGroupedCols};
+        return AWQ_OK;
+    }
+    if (op == AWQ_OP_FP8_BLOCK_GEMM) {
+        const int rc = check_fp8_block_shape(R, E, N, K);
+        if (rc != AWQ_OK) return rc;
+        const Fp8BlockPlan p = plan_fp8_block(R, E, N, K, d);
+        *out = awq_plan_t{p.rows > kFp8StreamRows ? 3 : 5, p.tiles_n, p.tiles_m, p.splits, p.rows / 16, 1, d.cus,
+                          (int64_t)p.workspace_bytes, p.cols};
+        return AWQ_OK;
+    }
+    return AWQ_EINVAL;
+}
+
 size_t awq_moe_gemm_w4a16_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K, int group_size) {
     if (check_moe_w4a16_shape(R, E, N, K, group_size) != AWQ_OK || R == 0) return 0;
     return plan_moe_w4a16(R, E, N, K, group_size, stream_props(nullptr)).workspace_bytes;

@@ -122,9 +122,15 @@ def workspace_bytes(op: int, M: int, N: int, K: int, group_size: int, split_k: i
         return int(L.lib().awq_workspace_bytes(op, M, N, K, group_size, split_k))
 
 
-def plan_info(op: int, M: int, N: int, K: int, group_size: int, split_k: int = 0, cu_count: int = 0) -> dict:
-    """How the library would launch a call (awq_plan_info); cu_count 0 = the current device."""
+def plan_info(op: int, M: int, N: int, K: int, group_size: int, split_k: int = 0, cu_count: int = 0,
+              experts: int = 0) -> dict:
+    """How the library would launch a call (awq_plan_info; of AWQ_OP_MOE_GEMM_W4A16 and AWQ_OP_FP8_BLOCK_GEMM
+    awq_grouped_plan_info, M rows of `experts` matrices); cu_count 0 = the current device."""
     info = L.PlanInfo()
+    if op in (L.AWQ_OP_MOE_GEMM_W4A16, L.AWQ_OP_FP8_BLOCK_GEMM):
+        L.check("awq_grouped_plan_info", L.lib().awq_grouped_plan_info(op, M, experts, N, K, group_size, cu_count,
+                                                                       ctypes.byref(info)))
+        return {f: getattr(info, f) for f, _ in L.PlanInfo._fields_}
     L.check("awq_plan_info", L.lib().awq_plan_info(op, M, N, K, group_size, split_k, cu_count,
                                                    ctypes.byref(info)))
     return {f: getattr(info, f) for f, _ in L.PlanInfo._fields_}

@@ -85,6 +85,9 @@ extern "C" {
 #define AWQ_OP_GEMV_W4A16 1
 #define AWQ_OP_W4A8_GEMM 2
 #define AWQ_OP_W4A8_FP8_GEMM 3
+/* Of awq_grouped_plan_info only. */
+#define AWQ_OP_MOE_GEMM_W4A16 4
+#define AWQ_OP_FP8_BLOCK_GEMM 5
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *awq_status_str(int status);
@@ -678,6 +681,19 @@ int awq_moe_fp8_block_gemm(const uint8_t *a, const uint8_t *w, const float *sa, 
                            int64_t top_k, int64_t E, int64_t N, int64_t K, int dtype, void *workspace,
                            size_t workspace_bytes, void *stream);
 size_t awq_fp8_block_gemm_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K);
+
+/*
+ * awq_grouped_plan_info -- as awq_plan_info, for the products above.
+ *   op: AWQ_OP_MOE_GEMM_W4A16 (awq_moe_gemm_w4a16), or AWQ_OP_FP8_BLOCK_GEMM
+ *   (awq_moe_fp8_block_gemm, or awq_fp8_block_gemm: E = 0; group_size is not
+ *   looked at).  R >= 1 rows.
+ *   out: kernel 5 is a streaming kernel, 3 one through LDS; row_tiles and
+ *   tile_cols are those of a workgroup's tile, tiles_m the row tiles that any
+ *   offsets can need.
+ * Errors: as awq_plan_info.
+ */
+int awq_grouped_plan_info(int op, int64_t R, int64_t E, int64_t N, int64_t K, int group_size, int cu_count,
+                          awq_plan_t *out);
 
 /*
  * awq_stream_read -- measurement helper, not a step of the method: reads
