@@ -59,3 +59,37 @@ def test_large_numbers(split, zeros):
     got = awq.moe_gemm_w4a16(xd, qd, sd, zd, od)
     want, size = (np.stack([v[t] for t in range(T)]) for v in (want, size))
     within(got, want, size, HALF_STEP["bf16"] + K * 2.0 ** -24, "bf16", f"{split}")
+
+
+def to_type(v, dtype):
+    return f64(torch.from_numpy(v).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("split", [[1, 1], [3, 2, 0, 4], [14, 17], [23, 20, 25]])
+@pytest.mark.parametrize("dtype,zeros,G,N", [("f16", True, 128, 1288), ("f16", False, 32, 264), ("bf16", True, 64, 264),
+                                             ("bf16", False, 128, 1288), ("bf16", True, 32, 264)])
+def test_weights_are_not_rounded(split, dtype, zeros, G, N):
+    """The streaming kernels' results are the exact ones rounded once, but where the sums' own error crosses a border.
+
+    With x, s of size 1: a run of 64 products x q' (q' <= 15, or 143 in bf16) of either sign sums to about 8 q', its at most
+    64 roundings of 2^-24 of that, independent, to 8 x 8 q' 2^-24; the same at worst for z' sum x.  Over the K / 64
+    runs these add like the results, sqrt(K) r with r the root mean square of q - z: d = sqrt(2) 8 q' / r 2^-24 of
+    the result.  A result less than d from a border (one in u / (2 d), u the type's step) moves by u: sqrt(2 d u) of
+    the norm.  Weights rounded to the type give several times as much, which the oracle shows."""
+    K, E, R = 512, len(split), sum(split)
+    info = awq.plan_info(awq.AWQ_OP_MOE_GEMM_W4A16, R, N, K, G, experts=E)
+    assert info["kernel"] == 5
+    q, s, z = experts_weights(E, K, N, G, zeros, dtype, R)
+    x = randn(R, R, K).to(DT[dtype])
+    mats = matrices(q, s, z, G)
+    want, _ = moe.grouped(f64(x), mats, split_rows(split).tolist(), None, 1)
+    coarse, _ = moe.grouped(f64(x), [to_type(m, dtype) for m in mats], split_rows(split).tolist(), None, 1)
+    want, coarse = (np.stack([v[t] for t in range(R)]) for v in (want, coarse))
+    ref, n = to_type(want, dtype), np.linalg.norm(want)
+    r = np.sqrt(np.mean([np.mean((m / np.repeat(f64(s[e]), G, 0)) ** 2) for e, m in enumerate(mats)]))
+    d = np.sqrt(2) * 8 * (15 if dtype == "f16" else 143) / r * 2.0 ** -24
+    bound = np.sqrt(2 * d * 2 * HALF_STEP[dtype])
+    assert np.linalg.norm(to_type(coarse, dtype) - ref) / n > 2 * bound
+    xd, qd, sd, zd, od = cuda(x, q, s, z, split_rows(split))
+    got = f64(awq.moe_gemm_w4a16(xd, qd, sd, zd, od, group_size=G))
+    assert np.linalg.norm(got - ref) / n <= bound
