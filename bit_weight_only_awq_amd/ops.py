@@ -599,6 +599,8 @@ def moe_route(logits, top_k: int, renormalize: bool = False, out=None):
     grouped by expert take; places: what moe_combine takes."""
     _need_gpu(logits, _LOGITS, 2, "logits")
     T, E = logits.shape
+    if not 1 <= top_k <= E:
+        L.check("awq_moe_route", L.AWQ_EINVAL)  # (before tensors of that size are made)
     dev, index, slots = logits.device, logits.get_device(), T * top_k
     if out is None:
         # (one piece of memory for the whole numbers: an allocation takes longer than a token's routing)
@@ -645,7 +647,7 @@ def _grouped(x_rows, experts, offsets, rows, index):
     _tensor(offsets, (experts + 1,), torch.int32, index, "offsets")
     if rows is None:
         return x_rows, offsets.data_ptr(), None
-    _tensor(rows, rows.shape[:1], torch.int32, index, "rows")
+    _tensor(rows, (rows.numel(),), torch.int32, index, "rows")
     return rows.shape[0], offsets.data_ptr(), rows.data_ptr()
 
 
@@ -661,6 +663,8 @@ def moe_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, top_k: int = 
     E, _, nw = qweight.shape
     N = 8 * nw
     _tensor(qweight, (E, K, nw), torch.int32, index, "qweight")
+    if group_size < 1:
+        L.check("awq_moe_gemm_w4a16", L.AWQ_EINVAL)
     _tensor(scales, (E, K // group_size, N), x.dtype, index, "scales")
     if qzeros is not None:
         _tensor(qzeros, (E, K // group_size, nw), torch.int32, index, "qzeros")
