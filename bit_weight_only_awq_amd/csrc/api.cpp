@@ -710,8 +710,14 @@ static double expected_tiles(double live, double avg, int64_t N, int64_t rows, i
     }
     return cdiv(N, cols) * live * t;
 }
-// The kernel by the rows an expert has on average, over the experts that R rows reach; us by rows an
-// expert, two of eight experts a token:
+// The kernel by the rows an expert has on average, over the experts that R rows reach.  Up to 24 rows the streaming
+// kernel, which rounds no weight; more go through LDS, where each weight is unpacked once for all rows of the tile and
+// rounded to the activation type, as the dense layer does above 32 rows (fp16) or 64 (bf16): the error
+// against 64 bits is 2.9 10^-4 of the norm instead of 2.1 10^-4 (fp16), 2.3 10^-3 instead of 1.7 10^-3 (bf16), for 32
+// rows in 119 us instead of 133, 100 in 203 instead of 242.  Shapes that rule these tiles out (K % 64, N % 32) stay with
+// the streaming kernel, which unpacks the words once for 32 rows: 1024 rows an expert, 4096 -> 1000 194 us where
+// 4096 -> 1024 takes 95; 4128 -> 4096 954 where 4096 -> 4096 takes 320.  us by rows an
+// expert, two of eight experts a token, bf16:
 //   14336 -> 4096        8    12    16    24    32    48    60    75   100   150   200   300
 //     stream, 16 rows   60    82    95         164   166
 //     stream, 32        79    81    84   114   133   134   199   238   242   359
@@ -725,7 +731,7 @@ static double expected_tiles(double live, double avg, int64_t N, int64_t rows, i
 // The smaller tiles split K up to three (of 64 rows five) workgroups a CU, 16 stages each at least: 14336 -> 4096 at 32 rows
 // 185 us by one, 133, 128, 119 by 2, 3, 4 splits; at 100 rows 267 by one, 207 by 2.
 // Streaming workgroups split K while two a CU are not there (us for 1, 2, 3, 4 splits: 128 tiles 88,
-// 83, 64, 60; 210 tiles 32.3, 32.3, 34.4, 35.6) and every wave keeps two chunks.
+// 83, 64, 60; 210 tiles 32.3, 32.3, 34.4, 35.6; 16-row tiles both) and every wave keeps two chunks.
 static W4A16Plan plan_moe_w4a16(int64_t R, int64_t E, int64_t N, int64_t K, int G, const DeviceProps &d) {
     W4A16Plan p{};
     const double live = live_experts(R, E), avg = (double)R / live;

@@ -167,7 +167,8 @@ __device__ __forceinline__ void dma16(const void *src, void *dst) {
                  : "memory", "m0");
 }
 // through a buffer descriptor: address = base + voff (per lane) + soff
-// (wave-uniform); offsets past the descriptor's size read as zero
+// (wave-uniform); words whose voff + soff is past the descriptor's size read as
+// zero, each for itself (measured: a load that straddles the end gets what lies before it)
 constexpr int kBufDword3 = 0x00020000;  // raw 32-bit buffer, no format conversion
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void *base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)bytes, kBufDword3);

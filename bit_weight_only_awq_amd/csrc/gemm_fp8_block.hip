@@ -25,12 +25,13 @@
 //
 // The matrix cores' sum of a tile is added to the running ones LAG instructions later.  The
 // sum's FMAs take issue slots from the matrix cores: beside four FMAs an instruction of 32 cycles
-// takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2400 are reached
-// where the tiles are as many as the CUs (4096 x 4096 x 14336), the rest goes to
-// the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).  4096 x 14336 x 4096 is 896 tiles,
-// 3.5 for each CU where the last half is waited for in full.  (Three rounds of it, and the other columns by the smaller
-// tiles in a launch behind: 257 -> 245 us in a graph, but 264 as before where calls follow each other on a stream and
-// the clock falls.  One workgroup a CU going through its tiles without a
+// takes 42, which bounds the rate to 3650 TFLOP/s on this card; 2370 to 2400 are reached
+// where the tiles are as many as the CUs and K is long (4096 x 4096 x 14336), the rest goes to
+// the LDS (192 KB read and 64 KB written a stage, 2048 cycles of it).  With K = 4096 a tile has 32 stages, beside
+// which its first copies and its stores count: 1980 in one round (4096 x 4096 x 4096), 2030 in four (N = 16384).
+// N = 14336 is 896 tiles, 3.5 for each CU where the last half is waited for in full: 1940, 248 to 262 us.  (Three
+// rounds of it, and the other columns by the smaller tiles in a launch behind: 257 -> 245 us in a graph, but 264 as
+// before where calls follow each other on a stream.  One workgroup a CU going through its tiles without a
 // pause, the next one's copies under way before the last one's stores: 295 -> 285 us by tiles of 256 x 128, but 257 ->
 // 269 by the large ones, whose registers it overflows.)
 // With few rows the copies bound: 777 tokens through 64 experts' 2048 x 2048 (top 8, 97 rows each; 268 MB of weights)
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_block_gemm(Fp8BlockArgs g
     };
     auto copy_scales = [&](int st) {
         if (scales && (st & 3) == 0 && st < s_hi && (row_scales || lane < BN / kBlk))
-            // (in the lane's offset, which is checked: four scales may reach past the last row's)
+            // (four scales may reach past the last row's: past the buffer)
             dma16_buf(sr, so + (uint32_t)st * 4u, 0u, lds + SLOTS * STAGE + ((st >> 2) & 1) * S_BYTES + (row_scales ? wave * 1024 : BM * 16));
     };
     auto left_of = [&](int st) { return st < s_hi ? min((K - st * kBlk) / 16, 8) : 0; };

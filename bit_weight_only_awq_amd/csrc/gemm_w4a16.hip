@@ -28,7 +28,8 @@
 // tiles ahead.  One wait and one barrier end each stage.
 //
 // MT = 16 row tiles per wave (256-row workgroup tiles) or 8 (128 rows, for
-// M <= 128, where 256-row tiles would be half padding).
+// M <= 128, where 256-row tiles would be half padding); rows grouped by expert
+// also 4 (64 rows).
 #include "device.hpp"
 #include "launch.hpp"
 #include "moe.hpp"

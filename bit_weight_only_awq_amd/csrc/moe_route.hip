@@ -7,8 +7,8 @@
 // be chosen has key 0).  Each of the k rounds takes the largest key of the group
 // (a butterfly of moves inside the registers), the lowest lane that holds it and
 // that lane's lowest expert -- which is the lower expert of equal logits --
-// and takes it out.  Bound by the rounds' chain of dependent moves (about 100
-// cycles each), not by memory: a token's wave has 2 E bytes to read.
+// and takes it out.  Bound by chains of dependent moves and LDS accesses, not by
+// memory: a token's wave has 2 E bytes to read.
 //
 // Plan.  A stable counting sort of the slots t k + j by expert.  Every wave takes
 // consecutive slots, 64 at a time: the lanes of one expert find each other by a
@@ -19,8 +19,11 @@
 //
 // One workgroup does both for few tokens; otherwise a first launch chooses, counts
 // and ranks, and a second places: its workgroups add up the counts of all others
-// for themselves, which for up to 256 of them costs less than a launch between.  (8191 tokens of 128 experts: 7.4 us
-// and 5.3 to 6.2; one token: 4.9.)
+// for themselves, which for up to 256 of them costs less than a launch between.  (8191 tokens of 128 experts, top 8: the
+// first launch 6.6 us in a graph -- 2.0 of an empty one, 0.8 loads and stores, 0.5 the softmax's sum, 1.8 the eight
+// rounds, 1.0 the counts, 0.5 the ranks -- and the second 5.9; one token: 4.9.  More than 256 workgroups there are
+// from 2^21 slots on, where it is little beside the rest: 2^19 tokens of 1024 experts, top 32, 2048 workgroups, 6.06 ms, a
+// quarter of the tokens 1.33.)
 #include "device.hpp"
 #include "launch.hpp"
 

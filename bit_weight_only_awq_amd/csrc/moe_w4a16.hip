@@ -5,7 +5,8 @@
 // of 16 MT of its rows; its four waves take the chunks of 32 CS consecutive k (inside
 // one quantisation group) in turn -- with a K split, of the workgroup's share of
 // them -- with two chunks' loads in flight, and their sums are added through LDS in wave
-// order, then over the K splits in split order (split_exchange.hpp).
+// order, then over the K splits in split order (split_exchange.hpp).  (The four tiles of
+// 32 rows are 128 KB of LDS: one workgroup a CU, where 16 rows leave room for two.)
 //
 // Lane (j, gq) holds two neighbouring word-columns (16 outputs) at the 8 k-rows 8 gq + e
 // of each 32-k step: a load takes whole 128-byte lines of four k-rows.  That sets the
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(64 * kGroupedWaves, 2) void w4a16_grouped(
     const int lo = blockIdx.y * per, hi = min(chunks, lo + per);
     const int n = hi - lo > wave ? (hi - lo - wave + WV - 1) / WV : 0;
     // (an expert's weights, and gathered rows, are under 2^31 bytes.)  Columns past the last are past the buffers:
-    // nothing is loaded for them, and rows past the tile's read its first: neither's sums are stored.
+    // nothing is loaded for them, and rows past the tile's read its first: neither's sums are stored.  (Nor are those of
+    // the second word-column of a row's last pair where N / 8 is odd: the next row's first, or past the buffer.)
     const __amdgpu_buffer_rsrc_t qr = buf_rsrc(qw + e * K * nw, (int64_t)K * nw * 4);
     const __amdgpu_buffer_rsrc_t sr = buf_rsrc(sc + e * groups * N, (int64_t)groups * N * 2);
     const __amdgpu_buffer_rsrc_t zr = buf_rsrc(SYM ? qw : qz + e * groups * nw, SYM ? 0 : (int64_t)groups * nw * 4);

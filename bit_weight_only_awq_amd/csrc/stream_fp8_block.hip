@@ -5,9 +5,10 @@
 // blocks of 128 k in turn (with a K split: of the workgroup's share of them), two
 // blocks' loads in flight, and their sums are added through LDS in wave order at
 // the end, then over the K splits in split order (split_exchange.hpp).  Bound by
-// memory: one token through 4096 x 14336 takes 18 us, of which 13 are what the
+// memory: one token through 4096 x 14336 takes 16 to 18 us in a graph, of which 13 are what the
 // same loads take alone and 4 what the smallest call does (64 outputs a workgroup
-// 18.7, 16 of them 18.2, 8 waves 18.2); 8 through 4096 x 4096 9.5.  Where tiles of 128 x 128 through LDS give
+// 18.7, 16 of them 18.2, 8 waves 18.2), and 15.3 to 15.8 where calls follow each other on a stream; 8 through
+// 4096 x 4096 9.5.  Where tiles of 128 x 128 through LDS give
 // every CU work, those are level at one row and faster from about four
 // on (api.cpp: plan_fp8_block).
 #include "fp8_block.hpp"
