@@ -792,6 +792,8 @@ static Fp8BlockPlan plan_fp8_block(int64_t M, int64_t E, int64_t N, int64_t K, c
     //                         768: -, 73, 58     1024: -, 80, 63    1100: -, 81, 109  4096: -, 295, 257
     //   64 experts 2048 -> 2048, rows each 32: 63, 50      97: 96, 80, 105   187: 126, 104, 120
     //                        250: -, 131, 135     300: -, 152, 158     375: -, 180, 164
+    //   8 experts 4096 -> 4096, rows each 325: -, 78, 68    400: -, 81, 70    425: -, 85, 104    500: -, 116, 121
+    //                        625: -, 122, 124    (the rule for experts does not see their rounds: 425 is its worst)
     // (us for 1, 2, 3, 4 splits: 112 tiles 24.7, 23.8, 31.8, 34.2; 32 tiles 65, 38, 30, 25.)
     const double small = workgroups(128, 128);
     const bool stream = avg <= 4 || (!E && M <= 16 && small * splits(small, 1) < 0.8 * d.cus);

